@@ -12,6 +12,14 @@ library's hand-written gfx950 kernels.  Names follow the C ABI:
     kda_decode_verify(q, k, v, g, beta, S, ...) -> o      (K drafts, S read only)
     kda_decode_commit(k, v, g, beta, n_accept, S)         (replay accepted, S in place)
     kda_decode_spec(q, k, v, g, beta, S, prev, n_accept) -> o   (both in one pass)
+
+and of the gated delta rule with one decay per head (C ABI: include/gdr.h):
+
+    gdr_fwd_chunked(q, k, v, g, beta, S0=None, cu_seqlens=None, ...) -> (o, S_T)
+    gdr_decode_step(q, k, v, g, beta, S, slots=None, ...) -> o      (pool S updated in place)
+    gdr_bwd_chunked(q, k, v, g, beta, dO, ...) -> (dq, dk, dv, dg, dbeta, dS0)
+    gdr_save8(q, k, v) -> Saved8;  gdr_load8(saved) -> (q, k, v)    (inputs kept in 8 bits)
+    gdr_bwd_chunked_saved8(saved, g, beta, dO, ...) -> (dq, dk, dv, dg, dbeta, dS0)
 """
 from __future__ import annotations
 
@@ -21,11 +29,15 @@ import torch
 
 from . import _lib
 from ._lib import KDAError, KDA_BF16, KDA_F32, KDA_OK  # noqa: F401
+from .gdr import (Saved8, gdr_bwd_chunked, gdr_bwd_chunked_saved8, gdr_bwd_workspace_bytes,
+                  gdr_decode_step, gdr_fwd_chunked, gdr_load8, gdr_save8)
 
 __all__ = ["kda_fwd_chunked", "kda_fwd_chunked_gated", "kda_fwd_workspace_bytes",
            "kda_bwd_chunked", "kda_bwd_workspace_bytes",
            "kda_decode_step",
            "kda_decode_verify", "kda_decode_commit", "kda_decode_spec", "KDAError",
+           "gdr_fwd_chunked", "gdr_decode_step", "gdr_bwd_chunked", "gdr_bwd_workspace_bytes",
+           "gdr_save8", "gdr_load8", "gdr_bwd_chunked_saved8", "Saved8",
            "version", "library_path"]
 
 

@@ -1,4 +1,4 @@
-"""ctypes binding of libkda.so (the C ABI in include/kda.h).
+"""ctypes binding of libkda.so (the C ABI in include/kda.h and include/gdr.h).
 
 Argument marshalling only: every step of KDA runs in the library's HIP
 kernels.  There is no fallback: if libkda.so is missing or cannot be loaded
@@ -70,6 +70,23 @@ def load() -> ctypes.CDLL:
         lib.kda_bwd_chunked.restype = ctypes.c_int
         lib.kda_bwd_chunked.argtypes = [P, P, P, P, P, P, P, I32, I64, I32, I32, I32,
                                         ctypes.c_int, P, P, P, P, P, P, P, P, P, SZ, P]
+        F32, U = ctypes.c_float, ctypes.c_int
+        lib.gdr_fwd_chunked.restype = ctypes.c_int
+        lib.gdr_fwd_chunked.argtypes = [P] * 7 + [I32, I64, I32, I32, I32, I32, F32, U, P, P, P]
+        lib.gdr_decode_step.restype = ctypes.c_int
+        lib.gdr_decode_step.argtypes = [P] * 7 + [I32] * 6 + [F32, U, P, P]
+        lib.gdr_bwd_workspace_bytes.restype = SZ
+        lib.gdr_bwd_workspace_bytes.argtypes = [I32, I64, I32, I32, I32, I32, U]
+        lib.gdr_bwd_chunked.restype = ctypes.c_int
+        lib.gdr_bwd_chunked.argtypes = ([P] * 7 + [I32, I64, I32, I32, I32, I32, F32, U] + [P] * 9
+                                        + [SZ, P])
+        lib.gdr_bwd_chunked_saved8.restype = ctypes.c_int
+        lib.gdr_bwd_chunked_saved8.argtypes = ([P] * 10 + [I32, I64, I32, I32, I32, I32, F32]
+                                               + [P] * 9 + [SZ, P])
+        lib.gdr_save8.restype = ctypes.c_int
+        lib.gdr_save8.argtypes = [P] * 3 + [I64, I32, I32, I32, I32] + [P] * 7
+        lib.gdr_load8.restype = ctypes.c_int
+        lib.gdr_load8.argtypes = [P] * 6 + [I64, I32, I32, I32, I32] + [P] * 4
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_last_error.restype = ctypes.c_char_p

@@ -4,7 +4,7 @@
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 instruction
 selection disabled (-packed-fp32-ops), and linked into one shared library
-next to this file.  The C-ABI declarations are in include/kda.h.
+next to this file.  The C-ABI declarations are in include/kda.h and include/gdr.h.
 """
 from __future__ import annotations
 
@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libkda.so")
 ARCH = "gfx950"
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill.hip", "kda_noalloc.hip",
-           "kda_spec.hip", "kda_backward.hip"]
+           "kda_spec.hip", "kda_backward.hip",
+           "gdr_api.cpp", "gdr_decode.hip", "gdr_recurrent.hip", "gdr_grad.hip", "gdr_save8.hip"]
 
 
 def hipcc() -> str:
@@ -38,7 +39,7 @@ def flags() -> list:
             "-I" + INCLUDE, "-I" + CSRC]
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 8) -> str:
     cc = hipcc()
     tmpdir = tempfile.mkdtemp(prefix="kda_build_")
     try:

@@ -1,0 +1,157 @@
+// Gated delta rule, decode: one token per (request, value head), the state
+// updated in place in a pool:
+//     S' = exp(g) S;  u = beta (v - S'^T k);  S = S' + k u^T;
+//     o  = scale (S'^T q + u (k . q))
+// A stream over the state (64 KiB a head at d = 128, read once and written
+// once), built for HBM bandwidth: one workgroup per (request, head), each
+// thread four columns of four rows, its four 16-byte loads issued first,
+// nontemporal both ways.  Both column sums share one pass over the rows.
+#include "gdr_device.h"
+
+namespace gdr {
+namespace {
+
+template <int DK, int DV>
+struct Shape {
+    static constexpr int NT = DK * DV / 16;     // 16 .. 1024 threads
+    static constexpr int CB = DV / 4;           // 4-column blocks per row
+    static constexpr int RP = NT / CB;          // rows covered per pass
+    static constexpr int R = DK / RP;           // rows per thread (4)
+};
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__((Shape<DK, DV>::NT))
+void gdr_decode_kernel(DecodeArgs a)
+{
+    using Sh = Shape<DK, DV>;
+    const int tid = threadIdx.x;
+    const int cb = tid % Sh::CB, r0 = tid / Sh::CB;
+    const int n = blockIdx.x / a.Hv, hv = blockIdx.x % a.Hv, hk = hv / (a.Hv / a.Hk);
+    const int64_t nh = blockIdx.x, nk = (int64_t)n * a.Hk + hk;
+    const int slot = a.slots ? a.slots[n] : n;
+    T *o = static_cast<T *>(a.o) + nh * DV;
+    if (slot < 0 || slot >= a.n_slots) {        // a padded row
+        for (int i = tid; i < DV; i += Sh::NT) kda::Elem<T>::st(o + i, 0.f);
+        return;
+    }
+    float *S = a.S + ((int64_t)slot * a.Hv + hv) * (DK * DV);
+    f32x4 s[Sh::R];
+#pragma unroll
+    for (int p = 0; p < Sh::R; ++p)
+        s[p] = __builtin_nontemporal_load(
+            reinterpret_cast<const f32x4 *>(S + (r0 + p * Sh::RP) * DV + 4 * cb));
+    __shared__ float s_k[DK], s_q[DK];
+    const T *kp = static_cast<const T *>(a.k) + nk * DK, *qp = static_cast<const T *>(a.q) + nk * DK;
+    for (int i = tid; i < DK; i += Sh::NT) {
+        s_k[i] = kda::Elem<T>::ld(kp + i);
+        s_q[i] = kda::Elem<T>::ld(qp + i);
+    }
+    const f32x4 vv = kda::Elem<T>::ld4(static_cast<const T *>(a.v) + nh * DV + 4 * cb);
+    const float b = a.beta[nh], al = kda::fast_exp2(floor_g(a.g[nh]) * LOG2E);
+    __syncthreads();
+
+    f32x4 pk = {0.f, 0.f, 0.f, 0.f}, pq = pk;
+    float kq = 0.f;
+#pragma unroll
+    for (int p = 0; p < Sh::R; ++p) {
+        const int i = r0 + p * Sh::RP;
+        const float ki = s_k[i], qi = s_q[i];
+        s[p] *= al;
+        pk += s[p] * ki;
+        pq += s[p] * qi;
+        kq += ki * qi;
+    }
+    f32x4 u;
+    if constexpr (Sh::CB == 32) {
+        // the two 32-lane halves of a wave hold the same columns: one
+        // register swap adds them, one half wave adds the per-wave sums
+        constexpr int NWV = Sh::NT / WAVE;
+        __shared__ f32x4 s_wk[NWV][32], s_wq[NWV][32], s_u[32];
+        __shared__ float s_wkq[NWV];
+        const int w = tid / WAVE, l = tid % WAVE;
+        f32x4 wk, wq;
+        float lo, hi;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            kda::half_pair(pk[e], lo, hi);
+            wk[e] = lo + hi;
+            kda::half_pair(pq[e], lo, hi);
+            wq[e] = lo + hi;
+        }
+        kda::half_pair(kq, lo, hi);
+        if (l < 32) {
+            s_wk[w][l] = wk;
+            s_wq[w][l] = wq;
+        }
+        if (l == 0) s_wkq[w] = lo + hi;
+        __syncthreads();
+        if (tid < 32) {
+            f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
+            float kqt = 0.f;
+#pragma unroll
+            for (int r = 0; r < NWV; ++r) {
+                ks += s_wk[r][tid];
+                qs += s_wq[r][tid];
+                kqt += s_wkq[r];
+            }
+            const f32x4 uu = b * (vv - ks);
+            s_u[tid] = uu;
+            kda::Elem<T>::st4(o + 4 * cb, a.scale * (qs + uu * kqt));
+        }
+        __syncthreads();
+        u = s_u[cb];
+    } else {
+        __shared__ f32x4 s_pk[Sh::RP][Sh::CB], s_pq[Sh::RP][Sh::CB];
+        __shared__ float s_kq[Sh::RP];
+        s_pk[r0][cb] = pk;
+        s_pq[r0][cb] = pq;
+        if (cb == 0) s_kq[r0] = kq;
+        __syncthreads();
+        f32x4 ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
+        float kqt = 0.f;
+#pragma unroll
+        for (int r = 0; r < Sh::RP; ++r) {
+            ks += s_pk[r][cb];
+            qs += s_pq[r][cb];
+            kqt += s_kq[r];
+        }
+        u = b * (vv - ks);
+        if (r0 == 0) kda::Elem<T>::st4(o + 4 * cb, a.scale * (qs + u * kqt));
+    }
+#pragma unroll
+    for (int p = 0; p < Sh::R; ++p) {
+        const int i = r0 + p * Sh::RP;
+        __builtin_nontemporal_store(s[p] + s_k[i] * u,
+                                    reinterpret_cast<f32x4 *>(S + i * DV + 4 * cb));
+    }
+}
+
+template <typename T, int DK, int DV>
+hipError_t launch_t(const DecodeArgs &a)
+{
+    const int64_t heads = (int64_t)a.N * a.Hv;
+    if (heads * Shape<DK, DV>::NT >= ((int64_t)1 << 32)) return hipErrorInvalidValue;  // grid size limit
+    hipLaunchKernelGGL((gdr_decode_kernel<T, DK, DV>), dim3((unsigned)heads),
+                       dim3(Shape<DK, DV>::NT), 0, a.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dispatch(const DecodeArgs &a)
+{
+#define GDR_CASE(DK_, DV_) if (a.dk == DK_ && a.dv == DV_) return launch_t<T, DK_, DV_>(a);
+#define GDR_ROW(DK_) GDR_CASE(DK_, 16) GDR_CASE(DK_, 32) GDR_CASE(DK_, 64) GDR_CASE(DK_, 128)
+    GDR_ROW(16) GDR_ROW(32) GDR_ROW(64) GDR_ROW(128)
+#undef GDR_ROW
+#undef GDR_CASE
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_decode(const DecodeArgs &a)
+{
+    return a.bf16 ? dispatch<bf16>(a) : dispatch<float>(a);
+}
+
+}  // namespace gdr

@@ -1,0 +1,87 @@
+// Device-side helpers shared by the gated delta rule kernels (gfx950 only).
+#pragma once
+
+#include "gdr_launch.h"
+#include "kda_device.h"
+
+namespace gdr {
+
+using kda::bf16;
+using kda::bf16x4;
+using kda::bf16x8;
+using kda::f32x2;
+using kda::f32x4;
+using kda::WAVE;
+using kda::LOG2E;
+
+// a byte of e4m3 beside the exponent bytes of its blocks
+struct e4m3 {
+    uint8_t x;
+};
+
+// q, k or v as stored.  ld4: four consecutive channels of a head row, in fp32.
+template <typename T> struct Src {
+    const T *p;
+    __device__ __forceinline__ f32x4 ld4(int64_t row, int d, int c) const
+    {
+        return kda::Elem<T>::ld4(p + row * d + c);
+    }
+};
+template <> struct Src<e4m3> {
+    const uint8_t *p, *e;
+    __device__ __forceinline__ f32x4 ld4(int64_t row, int d, int c) const
+    {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p + row * d + c);
+        const int blk = d < 32 ? d : 32;
+        // exponent bytes are in [17, 246]: the factor is a normal power of
+        // two and the product exact
+        const float f = __uint_as_float((uint32_t)e[row * (d / blk) + c / blk] << 23);
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+        const auto b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+        return f32x4{a[0] * f, a[1] * f, b[0] * f, b[1] * f};
+    }
+};
+template <typename T> __device__ __host__ inline Src<T> src(const void *p, const uint8_t *)
+{
+    return Src<T>{static_cast<const T *>(p)};
+}
+template <> __device__ __host__ inline Src<e4m3> src<e4m3>(const void *p, const uint8_t *e)
+{
+    return Src<e4m3>{static_cast<const uint8_t *>(p), e};
+}
+// storage type of o, dO and the gradients of q, k, v
+template <typename T> struct OutOf { typedef T type; };
+template <> struct OutOf<e4m3> { typedef bf16 type; };
+
+// first token and length of sequence n; a table that breaks its contract
+// gives lengths >= 0 inside [0, n_tokens]
+struct Seq {
+    int bos, len;
+};
+__device__ __forceinline__ int seq_edge(const SeqArgs &s, int n)
+{
+    if (!s.cu_seqlens) return n * s.seqlen;
+    const int x = s.cu_seqlens[n];
+    return x < 0 ? 0 : x > s.n_tokens ? s.n_tokens : x;
+}
+__device__ __forceinline__ Seq seq_of(const SeqArgs &s, int n)
+{
+    const int b = seq_edge(s, n), e = seq_edge(s, n + 1);
+    return Seq{b, e > b ? e - b : 0};
+}
+
+// log-decay with its floor (a NaN stays): exp of the floor is 0, and sums of
+// 64 such values keep far more than single precision in their differences
+__device__ __forceinline__ float floor_g(float g) { return g < -1e4f ? -1e4f : g; }
+
+// sum over the lanes of equal lane % 16
+__device__ __forceinline__ float sum_groups(float x)
+{
+    float a, b;
+    kda::row_pair(x, a, b);
+    x = a + b;
+    kda::half_pair(x, a, b);
+    return a + b;
+}
+
+}  // namespace gdr

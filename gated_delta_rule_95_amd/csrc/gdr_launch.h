@@ -1,0 +1,70 @@
+// Internal launch interface of the gated delta rule (gdr_*) between the
+// C-ABI layer (gdr_api.cpp) and the kernel translation units.  Arguments
+// arrive here already validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdr.h"
+
+namespace gdr {
+
+// q, k, v as stored: bf16, fp32, or e4m3 bytes with their exponent bytes
+enum class In { F32, BF16, E4M3 };
+
+struct SeqArgs {
+    const int32_t *cu_seqlens;   // nullptr: equal lengths seqlen
+    int32_t n_seqs;
+    int32_t n_tokens;
+    int32_t seqlen;
+};
+
+struct Args {
+    const void *q, *k, *v;
+    const uint8_t *qe, *ke, *ve;         // exponents (In::E4M3)
+    const float *g, *beta, *S0;
+    SeqArgs seq;
+    int32_t Hk, Hv, dk, dv;
+    float scale;
+    In in;
+    void *o;                             // forward
+    float *S_T;
+    // backward: cotangents, gradients and the workspace's parts
+    const void *dO;
+    const float *dS_T;
+    void *dq, *dkey, *dval;
+    float *dg, *dbeta, *dS0;
+    float *Sc, *Lc;                      // [slots, Hv, dk, dv] chunk-entry states, exit cotangents
+    float *R, *Ub;                       // [n_tokens, Hv, dv]
+    hipStream_t stream;
+};
+
+struct DecodeArgs {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    float *S;
+    const int32_t *slots;
+    int32_t n_slots, N, Hk, Hv, dk, dv;
+    float scale;
+    bool bf16;
+    void *o;
+    hipStream_t stream;
+};
+
+// tokens between two kept states of the backward
+int bwd_chunk(int dk, int dv, bool bf16);
+// chunk slots cu_seqlens[n] / C + n + c of a batch: an upper bound on every slot + 1
+inline int64_t bwd_slots(int32_t n_seqs, int64_t n_tokens, int C)
+{
+    return n_tokens / C + n_seqs + 1;
+}
+
+hipError_t launch_fwd(const Args &a);
+hipError_t launch_bwd(const Args &a);
+hipError_t launch_decode(const DecodeArgs &a);
+hipError_t launch_save8(const void *x, int64_t rows, int d, uint8_t *x8, uint8_t *xe, hipStream_t s);
+hipError_t launch_load8(const uint8_t *x8, const uint8_t *xe, int64_t rows, int d, void *x,
+                        hipStream_t s);
+
+}  // namespace gdr

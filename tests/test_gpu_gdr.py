@@ -1,0 +1,426 @@
+"""GPU tests of the gated delta rule (gdr_*) through the Python entry points
+against the fp64 oracle (oracle/gdr.py).
+
+Tolerances, from the roundings an output's path may take:
+- an output stored in bf16 is rounded once, by at most 2^-8 of the value; the
+  kernels may round single bf16 operands on the way to such an output (the
+  state, a residual row and a chunk product, each by at most 2^-8, signs
+  random).  So the 2-norm of the error is at most sqrt(1 + 3) 2^-8 of the
+  result's, and an element is off by its own half step and at most
+  8 * 2^-8 rms (a sum of three such errors at five of their deviations,
+  2^-8 / sqrt 3 each: 5 * sqrt 3 / sqrt 3 = 5, and 8 for heavy tails).
+- fp32 outputs come from products in fp32 or from operands held to at least
+  2^-17 (pairs of bf16), so the 2-norm of the error is at most 2^-17 times a
+  growth of a few through the chain of chunks: 1e-5.  An element is off by at
+  most 40 times that, 4e-4 rms: sums of some 10^4 terms with tails.
+- decode is one step in fp32: 2^-24 times the some 128 terms of a column sum,
+  a random walk: 1e-6.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle.gdr import gdr_recurrent, gdr_recurrent_vjp, kept8, packed
+from tests._gpu_util import half_ulp_bf16
+
+pytestmark = pytest.mark.gpu
+GRADS = ("dq", "dk", "dv", "dg", "dbeta", "dS0")
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def lib():
+    import gated_delta_rule_95_amd as m
+    return m
+
+
+def close(x, ref, name, fp32_tol=1e-5):
+    got = x.detach().double().cpu().numpy()
+    ref = np.asarray(ref, np.float64)
+    assert got.shape == ref.shape, (name, got.shape, ref.shape)
+    assert np.array_equal(np.isfinite(got), np.isfinite(ref)), name
+    norm = np.linalg.norm(ref)
+    if norm == 0:
+        assert np.abs(got).max(initial=0.0) == 0.0, name
+        return
+    rms = norm / np.sqrt(ref.size)
+    d = np.abs(got - ref)
+    rel = np.linalg.norm(d) / norm
+    if x.dtype == BF:
+        off = np.maximum(d - half_ulp_bf16(ref), 0).max() / rms
+        tol, most = 2 * 2.0 ** -8, 8 * 2.0 ** -8
+    else:
+        off = d.max() / rms
+        tol, most = fp32_tol, 40 * fp32_tol
+    print(f"  {name}: rel {rel:.2e} (<= {tol:.1e}) max {off:.2e} (<= {most:.1e})", flush=True)
+    assert rel <= tol and off <= most, (name, rel, off)
+
+
+def make(seed, lens, Hk, Hv, dk, dv, dtype=BF, s0=True, gates="usual", dscale=1.0):
+    r = np.random.default_rng(seed)
+    N, n = int(sum(lens)), len(lens)
+
+    def unit(x):
+        return x / np.sqrt((x * x).sum(-1, keepdims=True) + 1e-6)
+
+    def t(x, dt=F32):
+        return torch.from_numpy(np.ascontiguousarray(x)).to(dt).cuda()
+
+    b = {"q": t(unit(r.standard_normal((N, Hk, dk))), dtype), "k": t(unit(r.standard_normal((N, Hk, dk))), dtype),
+         "v": t(r.standard_normal((N, Hv, dv)), dtype), "dO": t(dscale * r.standard_normal((N, Hv, dv)), dtype)}
+    if gates == "usual":
+        g = -np.exp(r.uniform(-6, 1.5, (N, Hv)))
+    elif gates == "slow":
+        g = -1e-4 * r.random((N, Hv))
+    else:                                        # fast: up to -60 a token, some tokens forget everything
+        g = -60 * r.random((N, Hv))
+        g[r.random((N, Hv)) < 0.1] = -np.inf
+        g[r.random((N, Hv)) < 0.1] = 0
+    b["g"], b["beta"] = t(g), t(1 / (1 + np.exp(-r.standard_normal((N, Hv)))))
+    b["S0"] = t(0.3 * r.standard_normal((n, Hv, dk, dv))) if s0 else None
+    b["dS_T"] = t(dscale * 0.3 * r.standard_normal((n, Hv, dk, dv))) if s0 else None
+    b["cu"] = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    b["scale"] = dk ** -0.5
+    return b
+
+
+def host(b):
+    return {x: None if y is None else y.double().cpu().numpy() if isinstance(y, torch.Tensor) else y
+            for x, y in b.items()}
+
+
+def oracle_fwd(b):
+    h = host(b)
+    cu = b["cu"].tolist()
+    return packed(lambda q, k, v, g, be, S0: gdr_recurrent(q, k, v, g, be, b["scale"], S0), cu,
+                  [h[x] for x in ("q", "k", "v", "g", "beta")], (h["S0"],))
+
+
+def oracle_bwd(b):
+    h = host(b)
+    return packed(lambda q, k, v, g, be, dO, S0, dS: gdr_recurrent_vjp(q, k, v, g, be, dO, b["scale"], S0, dS),
+                  b["cu"].tolist(), [h[x] for x in ("q", "k", "v", "g", "beta", "dO")], (h["S0"], h["dS_T"]))
+
+
+def fwd(b, **kw):
+    out = lib().gdr_fwd_chunked(b["q"], b["k"], b["v"], b["g"], b["beta"], S0=b["S0"], cu_seqlens=b["cu"],
+                                scale=b["scale"], **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+def bwd(b, **kw):
+    out = lib().gdr_bwd_chunked(b["q"], b["k"], b["v"], b["g"], b["beta"], b["dO"], S0=b["S0"],
+                                dS_T=b["dS_T"], cu_seqlens=b["cu"], scale=b["scale"], **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+RAGGED = [1, 0, 63, 130, 64, 2, 65]
+DIMS = [(128, 128), (64, 64), (128, 64), (64, 128), (16, 16), (32, 64), (64, 16), (16, 128), (128, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_fwd_ragged(dk, dv, dtype):
+    b = make(1 + dk + dv, RAGGED, 2, 4, dk, dv, dtype)
+    o, S = fwd(b)
+    ro, rS = oracle_fwd(b)
+    close(o, ro, "o")
+    close(S, rS, "S_T")
+    assert torch.equal(S[1], b["S0"][1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_bwd_ragged(dk, dv, dtype):
+    b = make(31 + dk + dv, RAGGED, 2, 4, dk, dv, dtype)
+    got, ref = bwd(b), oracle_bwd(b)
+    for name, x, y in zip(GRADS, got, ref):
+        close(x, y, name)
+    assert torch.equal(got[5][1], b["dS_T"][1])
+
+
+@pytest.mark.parametrize("gates", ["slow", "fast"])
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (3, 3), (1, 3), (2, 6)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gates_and_shared_heads(gates, Hk, Hv, dtype):
+    """Decays that hardly forget and decays that forget at once (-inf among
+    them), one to three value heads to a key head, no states given."""
+    b = make(77 + Hv, [70, 129], Hk, Hv, 64, 64, dtype, s0=False, gates=gates)
+    o, S = fwd(b)
+    for name, x, y in zip(("o", "S_T"), (o, S), oracle_fwd(b)):
+        close(x, y, name)
+    for name, x, y in zip(GRADS, bwd(b), oracle_bwd(b)):
+        close(x, y, name)
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (32, 16)])
+def test_longer_sequences_and_small_cotangents(dk, dv):
+    """Many chunks, and the 1e-6 cotangents that a mean over tokens gives."""
+    b = make(5, [700, 1100], 1, 2, dk, dv, dscale=1e-6)
+    for name, x, y in zip(("o", "S_T"), fwd(b), oracle_fwd(b)):
+        close(x, y, name)
+    for name, x, y in zip(GRADS, bwd(b), oracle_bwd(b)):
+        close(x, y, name)
+
+
+def dg_growth(b):
+    """2-norm of the terms that dg is a sum of, over dg's own.
+
+    Whatever the form, dg_t = <L, S'> - beta (L^T k).(S'^T k), and with
+    beta |k|^2 = 1 - eps both terms agree up to eps: a token-by-token
+    evaluation in fp32 loses 1 / eps already.  In chunks dg_t is the sum
+    over j < t <= i of E_ij = scale (dO_i.U_j)(q_i.k_j) - (Yb_i.U_j)(k_i.k_j)
+    (decays left out: this is used where they are 1), each product known to
+    some 2^-24 of itself, so the error is that of the root of the sum of the
+    terms' squares and cannot follow dg below it."""
+    h = host(b)
+    dg = oracle_bwd(b)[3]
+    r = h["v"].shape[1] // h["q"].shape[1]
+    q, k = np.repeat(h["q"], r, 1), np.repeat(h["k"], r, 1)
+    _, _, kept = gdr_recurrent(h["q"], h["k"], h["v"], h["g"], h["beta"], b["scale"], keep=True)
+    U = np.stack([h["beta"][t][:, None] * kept[t][1] for t in range(len(kept))])
+    Yb = oracle_bwd(b)[2]
+    total = 0.0
+    for c in range(0, len(kept), 64):
+        s = slice(c, c + 64)
+        dot = lambda x, y: np.einsum("ihd,jhd->hij", x[s], y[s])       # noqa: E731
+        E2 = np.tril((b["scale"] * dot(h["dO"], U) * dot(q, k)) ** 2 + (dot(Yb, U) * dot(k, k)) ** 2, -1)
+        n = E2.shape[1]
+        total += sum(E2[:, t:, :t].sum() for t in range(n))
+    return max(1.0, np.sqrt(total) / np.linalg.norm(dg))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_repeated_keys(dtype):
+    """Equal keys with beta near 1 and no decay: the chunk's triangular system
+    is at its worst (its inverse by powers would cancel), and dg cancels
+    (dg_growth)."""
+    b = make(8, [200], 1, 2, 128, 128, dtype, s0=False, gates="slow")
+    b["k"][:] = b["k"][:1]
+    b["beta"][:] = 0.999
+    for name, x, y in zip(("o", "S_T"), fwd(b), oracle_fwd(b)):
+        close(x, y, name)
+    for name, x, y in zip(GRADS, bwd(b), oracle_bwd(b)):
+        close(x, y, name, 1e-5 * (dg_growth(b) if name == "dg" else 1))
+
+
+def test_equal_lengths_layout_and_no_final_state():
+    """[B, T, H, d] without cu_seqlens is the packed batch of equal lengths."""
+    b = make(11, [96] * 3, 2, 2, 64, 64)
+    o, S = fwd(b)
+    f = lambda x: x.view((3, 96) + x.shape[1:])           # noqa: E731
+    o4, S4 = lib().gdr_fwd_chunked(f(b["q"]), f(b["k"]), f(b["v"]), f(b["g"]), f(b["beta"]), S0=b["S0"])
+    assert torch.equal(o4.flatten(0, 1), o) and torch.equal(S4, S)
+    o5, none = fwd(b, output_final_state=False)
+    assert none is None and torch.equal(o5, o)
+    g4 = lib().gdr_bwd_chunked(f(b["q"]), f(b["k"]), f(b["v"]), f(b["g"]), f(b["beta"]), f(b["dO"]),
+                               S0=b["S0"], dS_T=b["dS_T"])
+    for x, y in zip(g4, bwd(b)):
+        assert torch.equal(x.reshape(y.shape), y)
+
+
+def test_beta_zero_and_zero_tokens():
+    b = make(12, [40, 100], 1, 2, 64, 64)
+    b["beta"][:] = 0
+    for name, x, y in zip(("o", "S_T"), fwd(b), oracle_fwd(b)):
+        close(x, y, name)
+    got, ref = bwd(b), oracle_bwd(b)
+    for name, x, y in zip(GRADS, got, ref):
+        close(x, y, name)
+    e = make(13, [0, 0], 1, 2, 64, 64)
+    o, S = fwd(e)
+    assert o.numel() == 0 and torch.equal(S, e["S0"])
+    assert torch.equal(bwd(e)[5], e["dS_T"])
+
+
+@pytest.mark.parametrize("dk", [128, 32])
+def test_nan_stays_in_its_sequence_and_head(dk):
+    b = make(14, [100, 80], 2, 2, dk, 64)
+    clean_o, clean_S = fwd(b)
+    clean = bwd(b)
+    b["k"][30, 1, 3] = float("nan")
+    o, S = fwd(b)
+    assert torch.isnan(o[30:100, 1]).any() and torch.isnan(S[0, 1]).any()
+    assert torch.equal(o[:, 0], clean_o[:, 0]) and torch.equal(o[100:], clean_o[100:])
+    assert torch.equal(S[1], clean_S[1]) and torch.equal(S[0, 0], clean_S[0, 0])
+    g = bwd(b)
+    for x, y in zip(g[:5], clean[:5]):
+        assert torch.equal(x[:, 0], y[:, 0]) and torch.equal(x[100:], y[100:])
+    assert torch.equal(g[5][1], clean[5][1])
+
+
+def test_rows_behind_the_last_sequence_are_left_as_they_were():
+    """cu_seqlens that ends before n_tokens: the rows behind keep what they hold."""
+    b = make(15, [50, 30], 1, 2, 128, 128)
+    n = 96
+    pad = lambda x: torch.cat([x, torch.full((n - 80,) + x.shape[1:], float("nan"), dtype=x.dtype, device="cuda")])  # noqa: E731
+    o = torch.full((n, 2, 128), 7.0, dtype=BF, device="cuda")
+    want, wS = fwd(b)
+    got, S = lib().gdr_fwd_chunked(*(pad(b[x]) for x in ("q", "k", "v", "g", "beta")), S0=b["S0"],
+                                   cu_seqlens=b["cu"], scale=b["scale"], o=o)
+    assert torch.equal(o[:80], want) and torch.equal(S, wS) and bool((o[80:] == 7).all())
+
+
+def test_runs_are_bit_identical_and_streams_work():
+    b = make(16, RAGGED, 2, 4, 128, 128)
+    o, S = fwd(b)
+    gr = bwd(b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o2, S2 = lib().gdr_fwd_chunked(b["q"], b["k"], b["v"], b["g"], b["beta"], S0=b["S0"],
+                                       cu_seqlens=b["cu"], scale=b["scale"])
+        gr2 = lib().gdr_bwd_chunked(b["q"], b["k"], b["v"], b["g"], b["beta"], b["dO"], S0=b["S0"],
+                                    dS_T=b["dS_T"], cu_seqlens=b["cu"], scale=b["scale"])
+    side.synchronize()
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    for x, y in zip(gr, gr2):
+        assert torch.equal(x, y)
+
+
+def test_captured_step_replays():
+    """Forward, 8-bit keeping and backward in one captured graph, replayed on
+    new inputs with eager work in between."""
+    m = lib()
+    b = make(17, [100, 29], 2, 4, 128, 64)
+    ws = torch.empty(m.gdr_bwd_workspace_bytes(2, 129, 2, 4, 128, 64), dtype=torch.uint8, device="cuda")
+
+    def step(x):
+        o, S = m.gdr_fwd_chunked(x["q"], x["k"], x["v"], x["g"], x["beta"], S0=x["S0"], cu_seqlens=x["cu"])
+        kept = m.gdr_save8(x["q"], x["k"], x["v"])
+        return (o, S) + m.gdr_bwd_chunked_saved8(kept, x["g"], x["beta"], x["dO"], S0=x["S0"],
+                                                 dS_T=x["dS_T"], cu_seqlens=x["cu"], workspace=ws)
+
+    step(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(b)
+    for seed in (18, 19, 20):
+        new = make(seed, [100, 29], 2, 4, 128, 64)
+        for x in ("q", "k", "v", "g", "beta", "dO", "S0", "dS_T"):
+            b[x].copy_(new[x])
+        want = [x.clone() for x in step(new)]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(out, want):
+            assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ decode
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("N,Hk,Hv", [(1, 1, 1), (7, 2, 6)])
+def test_decode(dk, dv, dtype, N, Hk, Hv):
+    b = make(41 + dk, [1] * N, Hk, Hv, dk, dv, dtype)
+    pool = torch.randn(N + 3, Hv, dk, dv, device="cuda")
+    slots = torch.randperm(N + 3)[:N].to(torch.int32)
+    if N > 1:
+        slots[2], slots[4] = -1, N + 3                    # padded rows
+    ref_o, ref_S = np.zeros((N, Hv, dv)), pool.double().cpu().numpy()
+    h = host(b)
+    for i, s in enumerate(slots.tolist()):
+        if 0 <= s < N + 3:
+            o1, ref_S[s] = gdr_recurrent(*(h[x][i:i + 1] for x in ("q", "k", "v", "g", "beta")), b["scale"],
+                                         ref_S[s])
+            ref_o[i] = o1[0]
+    S = pool.clone()
+    o = lib().gdr_decode_step(b["q"], b["k"], b["v"], b["g"], b["beta"], S, slots=slots.cuda())
+    torch.cuda.synchronize()
+    close(o, ref_o, "o", 1e-6)
+    close(S, ref_S, "S", 1e-6)
+    left = [i for i in range(N + 3) if i not in slots.tolist()]
+    assert torch.equal(S[left], pool[left])
+
+
+def test_decode_without_slots_continues_a_prefill():
+    """A prefill's final states as the pool, then tokens one at a time, give
+    what the whole sequences give."""
+    b = make(51, [40, 40, 40], 2, 4, 128, 128)
+    f = lambda x, a, e: x.view((3, 40) + x.shape[1:])[:, a:e].contiguous()     # noqa: E731
+    want, wS = oracle_fwd(b)
+    o, S = lib().gdr_fwd_chunked(*(f(b[x], 0, 33) for x in ("q", "k", "v", "g", "beta")), S0=b["S0"])
+    outs = [o]
+    for t in range(33, 40):
+        one = [f(b[x], t, t + 1)[:, 0].contiguous() for x in ("q", "k", "v", "g", "beta")]
+        outs.append(lib().gdr_decode_step(*one, S)[:, None])
+    torch.cuda.synchronize()
+    close(torch.cat(outs, 1).flatten(0, 1), want, "o")
+    close(S, wS, "S")
+
+
+# ------------------------------------------------------------------ 8 bits
+@pytest.mark.parametrize("dk,dv", [(128, 128), (16, 64), (32, 16)])
+def test_save8_round_trip(dk, dv):
+    b = make(61, [77], 2, 4, dk, dv)
+    b["q"] *= 2.0 ** torch.randint(-120, 120, (77, 2, 1), device="cuda")
+    b["k"][3] = 0
+    b["v"][5, 0, 2], b["v"][5, 1, 3] = float("inf"), float("nan")
+    m = lib()
+    kept = m.gdr_save8(b["q"], b["k"], b["v"])
+    out = m.gdr_load8(kept)
+    torch.cuda.synchronize()
+    for name, y in zip(("q", "k", "v"), out):
+        want = kept8(b[name].double().cpu().numpy())
+        got = y.double().cpu().numpy()
+        assert np.array_equal(np.isnan(want), np.isnan(got)), name
+        assert np.array_equal(want[~np.isnan(want)], got[~np.isnan(want)]), name
+
+
+@pytest.mark.parametrize("dk,dv,Hk,Hv", [(128, 128, 2, 4), (64, 128, 1, 1), (16, 32, 1, 3), (128, 16, 2, 2)])
+def test_bwd_from_saved8_is_bwd_of_loaded(dk, dv, Hk, Hv):
+    m = lib()
+    b = make(62, RAGGED, Hk, Hv, dk, dv)
+    kept = m.gdr_save8(b["q"], b["k"], b["v"])
+    got = m.gdr_bwd_chunked_saved8(kept, b["g"], b["beta"], b["dO"], S0=b["S0"], dS_T=b["dS_T"],
+                                   cu_seqlens=b["cu"])
+    b["q"], b["k"], b["v"] = m.gdr_load8(kept)
+    for name, x, y in zip(GRADS, got, bwd(b)):
+        assert torch.equal(x, y), name
+
+
+def test_far_offsets():
+    """Element offsets beyond 2^31: the last of many sequences gives what it
+    gives alone."""
+    m = lib()
+    n, T, H, d = 1026, 128, 128, 128
+    N = n * T
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    v = torch.randn(N, H, d, generator=gen, device="cuda", dtype=BF)
+    q = torch.randn(N, 1, d, generator=gen, device="cuda", dtype=BF) / d ** 0.5
+    k = torch.randn(N, 1, d, generator=gen, device="cuda", dtype=BF) / d ** 0.5
+    g = -torch.rand(N, H, generator=gen, device="cuda")
+    beta = torch.rand(N, H, generator=gen, device="cuda")
+    cu = torch.arange(0, N + 1, T, dtype=torch.int32, device="cuda")
+    o, S = m.gdr_fwd_chunked(q, k, v, g, beta, cu_seqlens=cu)
+    at = slice(N - T, N)
+    c = lambda x: x[at].contiguous()                       # noqa: E731
+    o1, S1 = m.gdr_fwd_chunked(c(q), c(k), c(v), c(g), c(beta))
+    torch.cuda.synchronize()
+    assert v.numel() > 2 ** 31 and torch.equal(o[at], o1) and torch.equal(S[-1:], S1)
+
+
+# ------------------------------------------------------------------ refusals
+def test_refusals_on_the_device():
+    m = lib()
+    b = make(71, [32], 1, 2, 64, 64)
+    args = [b[x] for x in ("q", "k", "v", "g", "beta")]
+    with pytest.raises(ValueError, match="contiguous"):
+        m.gdr_fwd_chunked(b["q"].transpose(0, 1).contiguous().transpose(0, 1).expand(32, 1, 64)[:, :, ::2],
+                          *args[1:])
+    with pytest.raises(TypeError, match="g must be"):
+        m.gdr_fwd_chunked(*args[:3], b["g"].to(BF), b["beta"])
+    with pytest.raises(ValueError, match="beta must have shape"):
+        m.gdr_fwd_chunked(*args[:4], b["beta"][:, :1].contiguous())
+    with pytest.raises(m.KDAError, match="overlaps"):
+        m.gdr_fwd_chunked(*args, o=b["v"])
+    with pytest.raises(m.KDAError, match="workspace"):
+        m.gdr_bwd_chunked(*args, b["dO"], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="H_k"):
+        m.gdr_decode_step(b["q"][None], *args[1:], b["S0"])
+    with pytest.raises(m.KDAError, match="n_slots"):
+        m.gdr_decode_step(*args, b["S0"])
+    with pytest.raises(TypeError, match="bfloat16"):
+        m.gdr_save8(b["q"].float(), b["k"].float(), b["v"].float())
