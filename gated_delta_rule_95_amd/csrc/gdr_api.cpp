@@ -8,6 +8,30 @@
 
 #define GDR_API extern "C" __attribute__((visibility("default")))
 
+namespace gdr {
+
+// Matrix-core chunks for bf16 (or 8-bit) inputs and heads of 64 or 128;
+// everything else token by token in fp32.
+static bool chunked(int dk, int dv, bool bf16) { return bf16 && dk >= 64 && dv >= 64; }
+
+int bwd_chunk(int, int, bool) { return 32; }
+
+static hipError_t launch_fwd(const Args &a)
+{
+    return chunked(a.dk, a.dv, a.in == In::BF16) ? launch_chunk_fwd(a) : launch_recurrent_fwd(a);
+}
+
+static hipError_t launch_bwd(const Args &a)
+{
+    const int C = bwd_chunk(a.dk, a.dv, a.in != In::F32);
+    hipError_t e;
+    if ((e = launch_recurrent_keep(a, C)) != hipSuccess) return e;
+    if ((e = launch_recurrent_sweep(a, C)) != hipSuccess) return e;
+    return a.seq.n_tokens == 0 ? hipSuccess : launch_grad32(a);
+}
+
+}  // namespace gdr
+
 namespace {
 
 using kda::set_error;
@@ -31,8 +55,9 @@ kda_status check_heads(int32_t Hk, int32_t Hv, int32_t dk, int32_t dv)
     if (!head_dim_ok(dk) || !head_dim_ok(dv))
         return set_error(KDA_ERR_UNSUPPORTED, "d_k and d_v must be 16, 32, 64 or 128 (got %d, %d)",
                          dk, dv);
-    if ((int64_t)Hv * (dk > dv ? dk : dv) >= ((int64_t)1 << 25))
-        return set_error(KDA_ERR_INVALID_ARG, "H_v * d must be below 2^25");
+    if ((int64_t)Hv * (dk > dv ? dk : dv) >= ((int64_t)1 << 22))
+        return set_error(KDA_ERR_INVALID_ARG, "H_v * d must be below 2^22 (64 rows of a tensor must stay "
+                                              "below 2^31 bytes)");
     return KDA_OK;
 }
 

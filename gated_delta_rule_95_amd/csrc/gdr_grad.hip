@@ -288,20 +288,8 @@ hipError_t dispatch(const Args &a)
 
 }  // namespace
 
-hipError_t launch_recurrent_fwd(const Args &a);
-hipError_t launch_recurrent_keep(const Args &a, int C);
-hipError_t launch_recurrent_sweep(const Args &a, int C);
-
-int bwd_chunk(int, int, bool) { return C32; }
-
-hipError_t launch_fwd(const Args &a) { return launch_recurrent_fwd(a); }
-
-hipError_t launch_bwd(const Args &a)
+hipError_t launch_grad32(const Args &a)
 {
-    hipError_t e;
-    if ((e = launch_recurrent_keep(a, C32)) != hipSuccess) return e;
-    if ((e = launch_recurrent_sweep(a, C32)) != hipSuccess) return e;
-    if (a.seq.n_tokens == 0) return hipSuccess;
     if (a.in == In::F32) return dispatch<float>(a);
     if (a.in == In::BF16) return dispatch<bf16>(a);
     return dispatch<e4m3>(a);

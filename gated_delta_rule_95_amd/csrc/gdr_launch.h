@@ -60,8 +60,13 @@ inline int64_t bwd_slots(int32_t n_seqs, int64_t n_tokens, int C)
     return n_tokens / C + n_seqs + 1;
 }
 
-hipError_t launch_fwd(const Args &a);
-hipError_t launch_bwd(const Args &a);
+// the kernels behind launch_fwd and launch_bwd (gdr_api.cpp), by form: token
+// by token in fp32, or chunks of 64 on the matrix cores
+hipError_t launch_recurrent_fwd(const Args &a);
+hipError_t launch_recurrent_keep(const Args &a, int C);
+hipError_t launch_recurrent_sweep(const Args &a, int C);
+hipError_t launch_grad32(const Args &a);
+hipError_t launch_chunk_fwd(const Args &a);
 hipError_t launch_decode(const DecodeArgs &a);
 hipError_t launch_save8(const void *x, int64_t rows, int d, uint8_t *x8, uint8_t *xe, hipStream_t s);
 hipError_t launch_load8(const uint8_t *x8, const uint8_t *xe, int64_t rows, int d, void *x,

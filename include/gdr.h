@@ -30,14 +30,14 @@
  *                 sequences of n_tokens / n_seqs tokens each
  * g = -inf is allowed and forgets the state (every g below -1e4 counts as
  * -1e4, whose exponential is 0).  g > 0 is computed as given where nothing
- * overflows.  NaN in g, beta, q, k or v of a token reaches that token's
- * outputs and everything that depends on them, in its own sequence and
- * heads only.  Inside a chunk of 64 tokens the factors exp(G_i - G_j) of the
+ * overflows.  NaN in g, beta, q, k or v of a token may reach any output of
+ * its own sequence and heads (tokens before it in its chunk among them), and
+ * none of another's.  Inside a chunk of 64 tokens the factors exp(G_i - G_j) of the
  * log-decay's cumulative sums are formed from their differences, so no
  * decay, however fast, overflows.
  *
  * Sizes: d_k, d_v in {16, 32, 64, 128}, independently; 1 <= H_k, H_v a
- * multiple of H_k, H_v * max(d_k, d_v) < 2^25; 0 <= n_tokens <= 2^31 - 64.
+ * multiple of H_k, H_v * max(d_k, d_v) < 2^22; 0 <= n_tokens <= 2^31 - 64.
  * in_dtype KDA_BF16 or KDA_F32.
  *
  * Alignment (bytes): q, k, v, o, dO, dq, dk, dv: eight elements of bf16 and

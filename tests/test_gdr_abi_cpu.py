@@ -48,7 +48,7 @@ def fwd(lib, **kw):
     (dict(n=3), 1, "multiple"), (dict(n=0), 1, "n_seqs == 0"), (dict(dt=7), 1, "in_dtype"),
     (dict(q=P + 8), 1, "aligned"), (dict(S0=7 * P + 4), 1, "aligned"), (dict(cu=7 * P + 2), 1, "aligned"),
     (dict(o=3 * P), 1, "overlaps"), (dict(ST=3 * P), 1, "overlaps"), (dict(ST=6 * P + 64), 1, "overlaps"),
-    (dict(N=1 << 31), 1, "2^31"), (dict(Hv=1 << 18, dk=128), 1, "2^25"),
+    (dict(N=1 << 31), 1, "2^31"), (dict(Hv=1 << 16, dk=128), 1, "2^22"),
 ])
 def test_fwd_refusals(lib, kw, status, msg):
     assert fwd(lib, **kw) == status
