@@ -126,22 +126,23 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void *base, int bytes)
                                              __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
 
-// Rows of one head of q, k or v of a chunk: n rows from token tok on, zeros
-// behind them.  raw() requests eight channels, bf() gives them in bf16.
+// Rows of q, k or v: n rows from token tok on (n <= 0: none), zeros behind
+// them.  at() is a lane's place (row, channel of head h), raw() requests the
+// eight channels c (a constant) behind it, bf() gives them in bf16.
 template <typename T> struct Rows;
 template <> struct Rows<bf16> {
     typedef u32x4 raw_t;
+    typedef int at_t;
     rsrc_t r;
-    int row_bytes, head;
-    __device__ __forceinline__ Rows(const void *p, const uint8_t *, int64_t tok, int n, int H, int h, int d)
+    __device__ __forceinline__ Rows(const void *p, const uint8_t *, int64_t tok, int n, int H, int d)
     {
-        row_bytes = H * d * 2;
-        head = h * d * 2;
-        r = make_rsrc(static_cast<const char *>(p) + tok * row_bytes, n * row_bytes);
+        const int row_bytes = H * d * 2;
+        r = make_rsrc(static_cast<const char *>(p) + tok * row_bytes, (n > 0 ? n : 0) * row_bytes);
     }
-    __device__ __forceinline__ raw_t raw(int row, int c) const
+    static __device__ __forceinline__ at_t at(int row, int H, int h, int d, int c) { return ((row * H + h) * d + c) * 2; }
+    __device__ __forceinline__ raw_t raw(at_t at, int c) const
     {
-        return __builtin_amdgcn_raw_buffer_load_b128(r, row * row_bytes + head + 2 * c, 0, 0);
+        return __builtin_amdgcn_raw_buffer_load_b128(r, at + 2 * c, 0, 0);
     }
     static __device__ __forceinline__ bf16x8 bf(raw_t w) { return __builtin_bit_cast(bf16x8, w); }
 };
@@ -150,22 +151,27 @@ template <> struct Rows<e4m3> {
         u32x2 w;
         uint32_t e;
     };
+    struct at_t {
+        int x, e;
+    };
     rsrc_t r, re;
-    int row_bytes, head, erow, ehead;
-    __device__ __forceinline__ Rows(const void *p, const uint8_t *e, int64_t tok, int n, int H, int h, int d)
+    __device__ __forceinline__ Rows(const void *p, const uint8_t *e, int64_t tok, int n, int H, int d)
     {
-        row_bytes = H * d;
-        head = h * d;
-        erow = H * (d / 32);
-        ehead = h * (d / 32);
+        const int row_bytes = H * d;
+        n = n > 0 ? n : 0;
         r = make_rsrc(static_cast<const char *>(p) + tok * row_bytes, n * row_bytes);
-        re = make_rsrc(e + tok * erow, n * erow);
+        re = make_rsrc(e + tok * (row_bytes / 32), n * (row_bytes / 32));
     }
-    __device__ __forceinline__ raw_t raw(int row, int c) const
+    static __device__ __forceinline__ at_t at(int row, int H, int h, int d, int c)
+    {
+        const int x = (row * H + h) * d + c;
+        return at_t{x, x / 32};              // exact for raw()'s c: it never crosses a block from c % 32
+    }
+    __device__ __forceinline__ raw_t raw(at_t at, int c) const
     {
         raw_t x;
-        x.w = __builtin_amdgcn_raw_buffer_load_b64(r, row * row_bytes + head + c, 0, 0);
-        x.e = __builtin_amdgcn_raw_buffer_load_b8(re, row * erow + ehead + c / 32, 0, 0);
+        x.w = __builtin_amdgcn_raw_buffer_load_b64(r, at.x + c, 0, 0);
+        x.e = __builtin_amdgcn_raw_buffer_load_b8(re, at.e + c / 32, 0, 0);
         return x;
     }
     static __device__ __forceinline__ bf16x8 bf(raw_t x)

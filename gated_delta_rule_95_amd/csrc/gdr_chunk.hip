@@ -61,51 +61,78 @@ __device__ __forceinline__ f32x4 ld4f(const float *p) { return *reinterpret_cast
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-template <typename TI, int DK, int NC, int MODE>
+// inclusive sum over the 64 lanes in double, on register moves between lanes
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+    return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double scan64(double x)
+{
+    x = scan_step<0x111, 0xf>(x);       // row_shr 1, 2, 4, 8
+    x = scan_step<0x112, 0xf>(x);
+    x = scan_step<0x114, 0xf>(x);
+    x = scan_step<0x118, 0xf>(x);
+    x = scan_step<0x142, 0xa>(x);       // lane 15 of each even row to the row behind it
+    return scan_step<0x143, 0xc>(x);    // lane 31 to the upper half
+}
+__device__ __forceinline__ double last_lane(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, 63), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Producer W of four.  Its tiles pair the lane tokens of block W (K K^T) and
+// of block 3 - W (K Q^T) with the row tokens of the blocks b before and at
+// them (forward) or at and behind them (sweep).
+template <typename TI, int DK, int NC, int MODE, int W>
 struct Producer {
     using R = Rows<TI>;
+    using St = Stage<DK, NC, MODE>;
     static constexpr int KS = DK / 32;
     static constexpr int VL = NC / 2;            // 16-byte loads of V a thread
     static constexpr bool SW = MODE == SWEEP;
-    // operand rows: K blocks, and in the sweep Q blocks; the lane blocks
-    typename R::raw_t kb[4][KS], qb[SW ? 4 : 1][KS], kw[KS], xw[KS];
-    u32x4 v[VL > 0 ? VL : 1];
-    typename Rows<TI>::raw_t v8[VL > 0 ? VL : 1];
+    static constexpr int X = 3 - W;
+    static constexpr bool kk_tile(int b) { return SW ? b >= W : b <= W; }
+    static constexpr bool kq_tile(int b) { return MODE != KEEP && (SW ? b >= X : b <= X); }
+    // row operands: K blocks (sweep: Q blocks for the second kind of tile)
+    static constexpr bool need_k(int b) { return kk_tile(b) || (!SW && kq_tile(b)); }
+    typename R::raw_t kb[4][KS], qb[4][KS], kw[KS], xw[KS];
+    u32x4 v[VL];
+    typename R::raw_t v8[VL];
     float g, beta;
 
     // requests chunk inputs: n rows from token tok
     __device__ __forceinline__ void load(const Args &a, int64_t tok, int n, int hk, int hv, int col,
-                                         int w, int ln, int lg, int ptid)
+                                         int ln, int lg, int ptid)
     {
-        const R K(a.k, a.ke, tok, n, a.Hk, hk, DK), Q(a.q, a.qe, tok, n, a.Hk, hk, DK);
-        const int hi = w > 3 - w ? w : 3 - w;
+        // one resource a block of 16 rows: a lane's place is the same in each
+        const typename R::at_t at = R::at(ln, a.Hk, hk, DK, 8 * lg);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const int c = 32 * s + 8 * lg;
-            kw[s] = K.raw(16 * w + ln, c);
-            if constexpr (SW) {
-                xw[s] = K.raw(16 * (3 - w) + ln, c);
+        for (int b = 0; b < 4; ++b) {
+            const R K(a.k, a.ke, tok + 16 * b, n - 16 * b, a.Hk, DK), Q(a.q, a.qe, tok + 16 * b, n - 16 * b, a.Hk, DK);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b >= w) kb[b][s] = K.raw(16 * b + ln, c);
-                    if (b >= 3 - w) qb[b][s] = Q.raw(16 * b + ln, c);
-                }
-            } else {
-                if constexpr (MODE == FWD) xw[s] = Q.raw(16 * (3 - w) + ln, c);
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (b <= (MODE == FWD ? hi : w)) kb[b][s] = K.raw(16 * b + ln, c);
+            for (int s = 0; s < KS; ++s) {
+                if (b == W) kw[s] = K.raw(at, 32 * s);
+                else if (need_k(b)) kb[b][s] = K.raw(at, 32 * s);
+                if (MODE == FWD && b == X) xw[s] = Q.raw(at, 32 * s);
+                if (SW && b == X) xw[s] = K.raw(at, 32 * s);
+                if (SW && kq_tile(b)) qb[b][s] = Q.raw(at, 32 * s);
             }
         }
         const int row = ptid / 4, cv = col + (ptid % 4) * (4 * NC);
         if constexpr (SW) {
-            const Rows<bf16> V(a.dO, nullptr, tok, n, a.Hv, hv, a.dv);
+            const Rows<bf16> V(a.dO, nullptr, tok, n, a.Hv, a.dv);
 #pragma unroll
-            for (int i = 0; i < VL; ++i) v[i] = V.raw(row, cv + 8 * i);
+            for (int i = 0; i < VL; ++i) v[i] = V.raw(Rows<bf16>::at(row, a.Hv, hv, a.dv, cv), 8 * i);
         } else {
-            const R V(a.v, a.ve, tok, n, a.Hv, hv, a.dv);
+            const R V(a.v, a.ve, tok, n, a.Hv, a.dv);
 #pragma unroll
-            for (int i = 0; i < VL; ++i) v8[i] = V.raw(row, cv + 8 * i);
+            for (int i = 0; i < VL; ++i) v8[i] = V.raw(R::at(row, a.Hv, hv, a.dv, cv), 8 * i);
         }
         const int lane = ln + 16 * lg;
         const rsrc_t rg = make_rsrc(a.g + tok * a.Hv, n * a.Hv * 4), rb = make_rsrc(a.beta + tok * a.Hv, n * a.Hv * 4);
@@ -133,54 +160,46 @@ struct Producer {
     // builds the stage; `next` requests the chunk after it once the
     // registers of this one are free
     template <typename F>
-    __device__ __forceinline__ void build(Stage<DK, NC, MODE> &st, float (*gp)[C], const Eye &eye, float scale,
-                                          int w, int ln, int lg, int ptid, F next)
+    __device__ __forceinline__ void build(St &st, float (*gp)[C], const Eye &eye, float scale,
+                                          int ln, int lg, int ptid, F next)
     {
         const int lane = ln + 16 * lg;
         // cumulative log2-decay in double, held as two floats
-        double G = (double)floor_g(g) * (double)LOG2E;
-#pragma unroll
-        for (int d = 1; d < C; d *= 2) {
-            const double y = __shfl_up(G, d);
-            if (lane >= d) G += y;
-        }
-        const double Gend = __shfl(G, C - 1);
-        const float gh = (float)G, gl = (float)(G - (double)gh);
+        const double G = scan64((double)floor_g(g) * (double)LOG2E), Gend = last_lane(G);
+        const float gh = (float)G;
         gp[0][lane] = gh;
-        gp[1][lane] = gl;
+        gp[1][lane] = (float)(G - (double)gh);
         gp[2][lane] = beta;
-        if (w == 0) {
+        if constexpr (W == 0) {
             const float er = kda::fast_exp2((float)(Gend - G));
-            st.eG[lane] = kda::fast_exp2((float)G);
+            st.eG[lane] = kda::fast_exp2(gh);
             st.eR[lane] = SW ? er : er * beta;
             st.beta[lane] = beta;
             if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
         }
         // K and Q blocks to the stage, tile products
         f32x4 kk[4] = {}, kq[4] = {};
-        bf16x8 kwf[KS], xwf[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            kwf[s] = R::bf(kw[s]);
-            *reinterpret_cast<bf16x8 *>(&st.K[16 * w + ln][32 * s + 8 * lg]) = kwf[s];
-            if constexpr (MODE != KEEP) xwf[s] = R::bf(xw[s]);
-            if constexpr (MODE == FWD)
-                *reinterpret_cast<bf16x8 *>(&st.Q[16 * (3 - w) + ln][32 * s + 8 * lg]) = xwf[s];
-        }
+            const int c = 32 * s + 8 * lg;
+            const bf16x8 kf = R::bf(kw[s]);
+            *reinterpret_cast<bf16x8 *>(&st.K[16 * W + ln][c]) = kf;
+            bf16x8 xf = {};
+            if constexpr (MODE != KEEP) xf = R::bf(xw[s]);
+            if constexpr (MODE == FWD) *reinterpret_cast<bf16x8 *>(&st.Q[16 * X + ln][c]) = xf;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const bool in_kk = SW ? b >= w : b <= w, in_kq = SW ? b >= 3 - w : b <= 3 - w;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                if (in_kk) kk[b] = mma(R::bf(kb[b][s]), kwf[s], kk[b]);
-                if constexpr (MODE == FWD)
-                    if (in_kq) kq[b] = mma(R::bf(kb[b][s]), xwf[s], kq[b]);
-                if constexpr (SW)
-                    if (in_kq) {
+            for (int b = 0; b < 4; ++b) {
+                bf16x8 bf = {};
+                if (need_k(b)) bf = b == W ? kf : R::bf(kb[b][s]);
+                if (kk_tile(b)) kk[b] = mma(bf, kf, kk[b]);
+                if constexpr (SW) {
+                    if (kq_tile(b)) {
                         const bf16x8 qf = R::bf(qb[b][s]);
-                        kq[b] = mma(qf, xwf[s], kq[b]);
-                        if (b == 3 - w) *reinterpret_cast<bf16x8 *>(&st.Q[16 * b + ln][32 * s + 8 * lg]) = qf;
+                        kq[b] = mma(qf, xf, kq[b]);
+                        if (b == X) *reinterpret_cast<bf16x8 *>(&st.Q[16 * X + ln][c]) = qf;
                     }
+                } else if (kq_tile(b))
+                    kq[b] = mma(bf, xf, kq[b]);
             }
         }
         {
@@ -190,80 +209,104 @@ struct Producer {
                 *reinterpret_cast<bf16x8 *>(&st.V[row][c + 8 * i]) = SW ? Rows<bf16>::bf(v[i]) : R::bf(v8[i]);
         }
         next();
-        // tiles: lane token x = 16 (block) + ln, row tokens y = 16 b + 4 lg + e;
-        // x is the later one in the forward, the earlier one in the sweep
-        const float sgn = SW ? -1.f : 1.f;
-        const int xk = 16 * w + ln, xq = 16 * (3 - w) + ln;
-        f32x4 diag = {0.f, 0.f, 0.f, 0.f};
+        // tiles: lane token x, row tokens y = 16 b + 4 lg + e; x is the later
+        // one in the forward, the earlier one in the sweep
+        const int xk = 16 * W + ln, xq = 16 * X + ln;
         const float ghk = gp[0][xk], glk = gp[1][xk], ghq = gp[0][xq], glq = gp[1][xq];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const bool in_kk = SW ? b >= w : b <= w, in_kq = SW ? b >= 3 - w : b <= 3 - w;
+            if (!kk_tile(b) && !kq_tile(b)) continue;
             const int y = 16 * b + 4 * lg;
             const f32x4 yh = ld4f(&gp[0][y]), yl = ld4f(&gp[1][y]), yb = ld4f(&gp[2][y]);
-            if (in_kk) {
-                f32x4 x;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool off = SW ? y + e > xk : y + e < xk;
-                    const float d = kda::fast_exp2(sgn * ((ghk - yh[e]) + (glk - yl[e])));
-                    x[e] = off ? d * yb[e] * kk[b][e] : 0.f;
+            for (int e = 0; e < 4; ++e) {
+                if (kk_tile(b)) {
+                    const float d = (ghk - yh[e]) + (glk - yl[e]);
+                    kk[b][e] = kda::fast_exp2(SW ? -d : d) * (yb[e] * kk[b][e]);
+                    if (b == W && !(SW ? y + e > xk : y + e < xk)) kk[b][e] = 0.f;
                 }
-                if (b == w) {
-                    diag = x;
-                } else {
-                    x = -x;
-                    // forward: 1 <- 0, 3 <- 2 one block, 2 and 3 <- (0, 1);
-                    // sweep: 2 <- 3, 0 <- 1 one block, 1 and 0 <- (2, 3)
-                    if ((w ^ 1) == b) put_block(st.Aone[SW ? (w == 2 ? 0 : 1) : (w == 1 ? 0 : 1)], lane, x, eye);
-                    else put_side(st.Apair[SW ? (w == 1 ? 0 : 1) : (w == 2 ? 0 : 1)], lane, b & 1, x, eye);
+                if (kq_tile(b)) {
+                    const float d = (ghq - yh[e]) + (glq - yl[e]);
+                    kq[b][e] = kda::fast_exp2(SW ? -d : d) * ((SW ? scale : yb[e]) * kq[b][e]);
+                    if (b == X && !(SW ? y + e >= xq : y + e <= xq)) kq[b][e] = 0.f;
                 }
-            }
-            if (MODE != KEEP && in_kq) {
-                f32x4 x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool in = SW ? y + e >= xq : y + e <= xq;
-                    const float d = kda::fast_exp2(sgn * ((ghq - yh[e]) + (glq - yl[e])));
-                    x[e] = in ? d * (SW ? scale : scale * yb[e]) * kq[b][e] : 0.f;
-                }
-                const int r = 3 - w, op = SW ? (r < 2 ? 2 * r + (b >> 1) : r + 2) : (r < 2 ? r : 2 * r - 2 + (b >> 1));
-                u32x2 h, m, l;
-                split_half(x, eye, h, m, l);
-                reinterpret_cast<u32x2 *>(&st.P[0][op][lane])[b & 1] = h;
-                reinterpret_cast<u32x2 *>(&st.P[1][op][lane])[b & 1] = m;
             }
         }
-        // (I + A)^-1 of the diagonal block row by row: lane row i = ln solves
-        // t (I + A) = e_i from the last column to the first (sweep: A is
-        // upper triangular, from the first on)
-        float *sc = reinterpret_cast<float *>(&st.T[w]);     // [column][row], 20 floats a column
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[(4 * lg + e) * 20 + ln] = diag[e];
+        float *sc = reinterpret_cast<float *>(&st.T[W]);     // the diagonal block, 20 floats a row
+        *reinterpret_cast<f32x4 *>(&sc[20 * ln + 4 * lg]) = kk[W];
         __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            // forward: 1 <- 0, 3 <- 2 one block, 2 and 3 <- (0, 1);
+            // sweep: 2 <- 3, 0 <- 1 one block, 1 and 0 <- (2, 3)
+            if (kk_tile(b) && b != W) {
+                if ((W ^ 1) == b) put_block(st.Aone[SW ? (W == 2 ? 0 : 1) : (W == 1 ? 0 : 1)], lane, -kk[b], eye);
+                else put_side(st.Apair[SW ? (W == 1 ? 0 : 1) : (W == 2 ? 0 : 1)], lane, b & 1, -kk[b], eye);
+            }
+            if (kq_tile(b)) {
+                constexpr int r = X;
+                const int op = SW ? (r < 2 ? 2 * r + (b >> 1) : r + 2) : (r < 2 ? r : 2 * r - 2 + (b >> 1));
+                const u32x2 h = pack4(kq[b]);
+                const f32x4 rest = mma(eye.a, join(h, h), kq[b]);
+                reinterpret_cast<u32x2 *>(&st.P[0][op][lane])[b & 1] = h;
+                reinterpret_cast<u32x2 *>(&st.P[1][op][lane])[b & 1] = pack4(rest);
+            }
+        }
+        // (I + A)^-1 of the diagonal block by rows: lane row i = ln solves
+        // t (I + A) = e_i, each entry when final taken out of those left
+        // (from the last to the first; sweep: A is upper triangular, from the
+        // first on)
         float t[16];
 #pragma unroll
-        for (int jj = 0; jj < 16; ++jj) {
+        for (int j = 0; j < 16; ++j) t[j] = ln == j ? 1.f : 0.f;
+        f32x4 av[4];
+#pragma unroll
+        for (int jj = 0; jj < 15; ++jj) {
             const int j = SW ? jj : 15 - jj;
-            float acc = ln == j ? 1.f : 0.f;
+            // row j is read a step ahead
+            const auto row = [&](int j, f32x4 *av) {
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-                if (SW ? 4 * k4 >= j : 4 * k4 + 3 <= j) continue;
-                const f32x4 av = ld4f(&sc[j * 20 + 4 * k4]);
+                for (int k4 = 0; k4 < 4; ++k4)
+                    if (SW ? 4 * k4 + 3 > j : 4 * k4 < j) av[k4] = ld4f(&sc[20 * j + 4 * k4]);
+            };
+            if (jj == 0) row(j, av);
+            f32x4 ahead[4];
+            if (jj < 14) row(SW ? j + 1 : j - 1, ahead);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int k = 4 * k4 + e;
-                    if (SW ? k < j : k > j) acc -= t[k] * av[e];
-                }
-            }
-            t[j] = acc;
+            for (int k = 0; k < 16; ++k)
+                if (SW ? k > j : k < j) t[k] -= t[j] * av[k / 4][k % 4];
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) av[k4] = ahead[k4];
         }
         f32x4 tv;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             tv[e] = lg == 0 ? t[e] : lg == 1 ? t[4 + e] : lg == 2 ? t[8 + e] : t[12 + e];
         __builtin_amdgcn_wave_barrier();
-        put_block(st.T[w], lane, tv, eye);
+        put_block(st.T[W], lane, tv, eye);
+    }
+
+    // every chunk of the chain: first .. in steps of `step` (chunks of them)
+    template <typename Tok>
+    static __device__ __forceinline__ void run(const Args &a, Smem<DK, NC, MODE> &sm, int chunks, Tok where, int hk, int hv,
+                                               int col, int lane, int ptid)
+    {
+        const int ln = lane % 16, lg = lane / 16;
+        const Eye eye = make_eye(lane);
+        Producer p;
+        const auto request = [&](int c) {
+            if (c < chunks) {
+                int64_t tok;
+                int n;
+                where(c, tok, n);
+                p.load(a, tok, n, hk, hv, col, ln, lg, ptid);
+            }
+        };
+        request(0);
+        for (int c = 0; c < chunks; ++c) {
+            p.build(sm.st[c & 1], sm.G[W], eye, a.scale, ln, lg, ptid, [&] { request(c + 1); });
+            __syncthreads();
+        }
     }
 };
 
@@ -306,80 +349,96 @@ struct Consumer {
         return join(lds_tr(&X[r][c]), lds_tr(&X[r + 16][c]));
     }
 
+    // S += K^T (or Q^T) u over the tokens 32 s .. of the chunk
+    __device__ __forceinline__ void update(const bf16 (*M)[Stage<DK, NC, MODE>::LK], const Parts<3> &u, int s, int ln, int lg)
+    {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) S[t] = mma_parts<3>(transposed(M, t, s, ln, lg), u, S[t]);
+    }
+
+    // out: buffer of the chunk's rows of o (R); off: this lane's byte in row 4 lg
     __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Eye &eye, float scale, int w, int ln, int lg,
-                                            rsrc_t out, int row_bytes, int head)
+                                            rsrc_t out, int row_bytes, int off)
     {
         const int lane = ln + 16 * lg;
-        f32x4 X[4] = {}, O[4] = {};
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        f32x4 X[4] = {}, O[4] = {}, R[4];
+        Parts<3> p[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const Parts<3> p = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
+            p[s] = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                X[t] = mma_parts<3>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p, X[t]);
-                if constexpr (MODE == FWD) O[t] = mma_parts<2>(lds8(&st.Q[16 * t + ln][32 * s + 8 * lg]), Parts<2>{{p.p[0], p.p[1]}}, O[t]);
-            }
+            for (int t = 0; t < 4; ++t) X[t] = mma_parts<3>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], X[t]);
         }
-        f32x4 R[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const f32x4 v = widen(lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]));
-            const f32x4 eg = ld4f(&st.eG[16 * t + 4 * lg]);
-            R[t] = v - eg * X[t];
-            if constexpr (MODE == FWD) O[t] *= scale * eg;
+            R[t] = v - ld4f(&st.eG[16 * t + 4 * lg]) * X[t];
         }
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        // the substitution is one long dependent chain: products that do not
+        // wait for it stand between its steps
+        const auto qs = [&](int s) {
+            if (MODE == FWD && s < KS)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    O[t] = mma_parts<2>(lds8(&st.Q[16 * t + ln][32 * s + 8 * lg]), Parts<2>{{p[s].p[0], p[s].p[1]}}, O[t]);
+        };
         u32x2 h, m, l;
         Half x = split_half(R[0], eye, h, m, l);
+        qs(0);
         R[0] = mul_block(st.T[0], lane, x, zero);
+        qs(1);
         x = split_half(R[0], eye, h, m, l);
         R[1] = mul_block(st.Aone[0], lane, x, R[1]);
+        qs(2);
         x = split_half(R[1], eye, h, m, l);
+        qs(3);
         R[1] = mul_block(st.T[1], lane, x, zero);
+        const float gam = st.gamma;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) S[t] *= gam;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) O[t] *= ld4f(&st.eG[16 * t + 4 * lg]);
         const Parts<3> r01 = split_pair<3>(R[0], R[1], eye);
         R[2] = mul_pair(st.Apair[0], lane, r01, R[2]);
         R[3] = mul_pair(st.Apair[1], lane, r01, R[3]);
+        const Parts<3> u0 = split_pair<3>(ld4f(&st.eR[4 * lg]) * R[0], ld4f(&st.eR[16 + 4 * lg]) * R[1], eye);
         x = split_half(R[2], eye, h, m, l);
+        update(st.K, u0, 0, ln, lg);
         R[2] = mul_block(st.T[2], lane, x, zero);
+        // operands 0, 1, 2a, 2b, 3a, 3b: rows 0, 1, 2, 2, 3, 3 against tokens
+        // 0-31 (2b, 3b: 32-63)
+        const auto pr = [&](int i, int t, bf16x8 rh, bf16x8 rm) {
+            if constexpr (MODE == FWD) {
+                const bf16x8 ph = st.P[0][i][lane], pm = st.P[1][i][lane];
+                O[t] = mma(pm, rh, O[t]);
+                O[t] = mma(ph, rm, O[t]);
+                O[t] = mma(ph, rh, O[t]);
+            }
+        };
+        pr(0, 0, r01.p[0], r01.p[1]);
+        pr(1, 1, r01.p[0], r01.p[1]);
         x = split_half(R[2], eye, h, m, l);
+        pr(2, 2, r01.p[0], r01.p[1]);
         R[3] = mul_block(st.Aone[1], lane, x, R[3]);
+        pr(4, 3, r01.p[0], r01.p[1]);
         x = split_half(R[3], eye, h, m, l);
         R[3] = mul_block(st.T[3], lane, x, zero);
-        if constexpr (MODE == FWD) {
-            const Parts<2> r23 = split_pair<2>(R[2], R[3], eye);
-#pragma unroll
-            for (int i = 0; i < 6; ++i) {
-                // operands 0, 1, 2a, 2b, 3a, 3b: rows 0, 1, 2, 2, 3, 3 against tokens 0-31 (2b, 3b: 32-63)
-                const int t = i < 2 ? i : 1 + i / 2;
-                const bool late = i == 3 || i == 5;
-                const bf16x8 h = st.P[0][i][lane], m = st.P[1][i][lane];
-                const bf16x8 rh = late ? r23.p[0] : r01.p[0], rm = late ? r23.p[1] : r01.p[1];
-                O[t] = mma(m, rh, O[t]);
-                O[t] = mma(h, rm, O[t]);
-                O[t] = mma(h, rh, O[t]);
-            }
-        }
+        const Parts<3> u1 = split_pair<3>(ld4f(&st.eR[32 + 4 * lg]) * R[2], ld4f(&st.eR[48 + 4 * lg]) * R[3], eye);
+        const Parts<2> r23 = split_pair<2>(R[2], R[3], eye);
+        pr(3, 2, r23.p[0], r23.p[1]);
+        pr(5, 3, r23.p[0], r23.p[1]);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int off = (16 * t + 4 * lg + e) * row_bytes + head;
+                const int so = (16 * t + e) * row_bytes;
                 if constexpr (MODE == FWD)
-                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)O[t][e]), out, off, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)(scale * O[t][e])), out, off + so, 0, 0);
                 else
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(R[t][e]), out, off, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(R[t][e]), out, off + so, 0, 0);
             }
-        const float gam = st.gamma;
-        Parts<3> u[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-            u[s] = split_pair<3>(ld4f(&st.eR[32 * s + 4 * lg]) * R[2 * s], ld4f(&st.eR[32 * s + 16 + 4 * lg]) * R[2 * s + 1], eye);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            S[t] *= gam;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) S[t] = mma_parts<3>(transposed(st.K, t, s, ln, lg), u[s], S[t]);
-        }
+        update(st.K, u1, 1, ln, lg);
     }
 };
 
@@ -436,37 +495,39 @@ void gdr_chunk_kernel(Args a)
         (&sm.st[1].P[0][0][0])[i] = bf16x8{};
     }
     __syncthreads();
-    const Eye eye = make_eye(lane);
-    const auto nrows = [&](int c) { return len - c * C < C ? len - c * C : C; };
+    const auto where = [&](int c, int64_t &tok, int &nrow) {
+        tok = bos + (int64_t)c * C;
+        nrow = len - c * C < C ? len - c * C : C;
+    };
     if (wave >= NC) {
         const int w = wave - NC, ptid = tid - NC * WAVE;
-        Producer<TI, DK, NC, MODE> p;
-        const auto request = [&](int c) {
-            if (c < chunks) p.load(a, bos + (int64_t)c * C, nrows(c), hk, hv, col, w, ln, lg, ptid);
-        };
-        request(0);
-        for (int c = 0; c < chunks; ++c) {
-            p.build(sm.st[c & 1], sm.G[w], eye, a.scale, w, ln, lg, ptid, [&] { request(c + 1); });
-            __syncthreads();
-        }
-    } else {
-        Consumer<TI, DK, NC, MODE> q;
-        const int64_t st = ((int64_t)n * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln;
-        load_state<DK / 16>(q.S, a.S0 ? a.S0 + st : nullptr, a.dv, lg);
-        for (int c = 0; c < chunks; ++c) {
-            __syncthreads();
-            const int64_t tok = bos + (int64_t)c * C;
-            const int es = MODE == FWD ? 2 : 4, rb = a.Hv * a.dv * es;
-            char *base = MODE == FWD ? static_cast<char *>(a.o) : reinterpret_cast<char *>(a.R);
-            if constexpr (MODE == KEEP) {
-                const int64_t slot = bos / C + n + c;
-                store_state<DK / 16>(q.S, a.Sc + (slot * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln, a.dv, lg);
-            }
-            q.forward(sm.st[c & 1], eye, a.scale, wave, ln, lg, make_rsrc(base + tok * rb, nrows(c) * rb), rb,
-                      (hv * a.dv + col + 16 * wave + ln) * es);
-        }
-        if (MODE == FWD && a.S_T) store_state<DK / 16>(q.S, a.S_T + st, a.dv, lg);
+#define GDR_RUN(W_) Producer<TI, DK, NC, MODE, W_>::run(a, sm, chunks, where, hk, hv, col, lane, ptid)
+        if (w == 0) GDR_RUN(0);
+        else if (w == 1) GDR_RUN(1);
+        else if (w == 2) GDR_RUN(2);
+        else GDR_RUN(3);
+#undef GDR_RUN
+        return;
     }
+    const Eye eye = make_eye(lane);
+    Consumer<TI, DK, NC, MODE> q;
+    const int64_t st = ((int64_t)n * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln;
+    load_state<DK / 16>(q.S, a.S0 ? a.S0 + st : nullptr, a.dv, lg);
+    constexpr int es = MODE == FWD ? 2 : 4;
+    const int rb = a.Hv * a.dv * es, off = 4 * lg * rb + (hv * a.dv + col + 16 * wave + ln) * es;
+    for (int c = 0; c < chunks; ++c) {
+        __syncthreads();
+        int64_t tok;
+        int nrow;
+        where(c, tok, nrow);
+        const char *base = MODE == FWD ? static_cast<const char *>(a.o) : reinterpret_cast<const char *>(a.R);
+        if constexpr (MODE == KEEP) {
+            const int64_t slot = bos / C + n + c;
+            store_state<DK / 16>(q.S, a.Sc + (slot * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln, a.dv, lg);
+        }
+        q.forward(sm.st[c & 1], eye, a.scale, wave, ln, lg, make_rsrc(base + tok * rb, nrow * rb), rb, off);
+    }
+    if (MODE == FWD && a.S_T) store_state<DK / 16>(q.S, a.S_T + st, a.dv, lg);
 }
 
 template <typename TI, int DK, int NC, int MODE>
