@@ -99,9 +99,7 @@ struct Producer {
     static constexpr int X = 3 - W;
     static constexpr bool kk_tile(int b) { return SW ? b >= W : b <= W; }
     static constexpr bool kq_tile(int b) { return MODE != KEEP && (SW ? b >= X : b <= X); }
-    // row operands: K blocks (sweep: Q blocks for the second kind of tile)
-    static constexpr bool need_k(int b) { return kk_tile(b) || (!SW && kq_tile(b)); }
-    typename R::raw_t kb[4][KS], qb[4][KS], kw[KS], xw[KS];
+    typename R::raw_t kw[KS], qx[KS];            // rows of K block W and of Q block X
     u32x4 v[VL];
     typename R::raw_t v8[VL];
     float g, beta;
@@ -110,19 +108,12 @@ struct Producer {
     __device__ __forceinline__ void load(const Args &a, int64_t tok, int n, int hk, int hv, int col,
                                          int ln, int lg, int ptid)
     {
-        // one resource a block of 16 rows: a lane's place is the same in each
         const typename R::at_t at = R::at(ln, a.Hk, hk, DK, 8 * lg);
+        const R K(a.k, a.ke, tok + 16 * W, n - 16 * W, a.Hk, DK), Q(a.q, a.qe, tok + 16 * X, n - 16 * X, a.Hk, DK);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const R K(a.k, a.ke, tok + 16 * b, n - 16 * b, a.Hk, DK), Q(a.q, a.qe, tok + 16 * b, n - 16 * b, a.Hk, DK);
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                if (b == W) kw[s] = K.raw(at, 32 * s);
-                else if (need_k(b)) kb[b][s] = K.raw(at, 32 * s);
-                if (MODE == FWD && b == X) xw[s] = Q.raw(at, 32 * s);
-                if (SW && b == X) xw[s] = K.raw(at, 32 * s);
-                if (SW && kq_tile(b)) qb[b][s] = Q.raw(at, 32 * s);
-            }
+        for (int s = 0; s < KS; ++s) {
+            kw[s] = K.raw(at, 32 * s);
+            if (MODE != KEEP) qx[s] = Q.raw(at, 32 * s);
         }
         const int row = ptid / 4, cv = col + (ptid % 4) * (4 * NC);
         if constexpr (SW) {
@@ -157,8 +148,8 @@ struct Producer {
         for (int i = 0; i < 3; ++i) reinterpret_cast<u32x2 *>(&t[i][lane])[side] = p[i];
     }
 
-    // builds the stage; `next` requests the chunk after it once the
-    // registers of this one are free
+    // builds the stage; `next` requests the chunk after it once this one's
+    // rows are in the stage
     template <typename F>
     __device__ __forceinline__ void build(St &st, float (*gp)[C], const Eye &eye, float scale,
                                           int ln, int lg, int ptid, F next)
@@ -177,30 +168,14 @@ struct Producer {
             st.beta[lane] = beta;
             if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
         }
-        // K and Q blocks to the stage, tile products
-        f32x4 kk[4] = {}, kq[4] = {};
+        // K and Q blocks and the values to the stage
+        bf16x8 kf[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int c = 32 * s + 8 * lg;
-            const bf16x8 kf = R::bf(kw[s]);
-            *reinterpret_cast<bf16x8 *>(&st.K[16 * W + ln][c]) = kf;
-            bf16x8 xf = {};
-            if constexpr (MODE != KEEP) xf = R::bf(xw[s]);
-            if constexpr (MODE == FWD) *reinterpret_cast<bf16x8 *>(&st.Q[16 * X + ln][c]) = xf;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                bf16x8 bf = {};
-                if (need_k(b)) bf = b == W ? kf : R::bf(kb[b][s]);
-                if (kk_tile(b)) kk[b] = mma(bf, kf, kk[b]);
-                if constexpr (SW) {
-                    if (kq_tile(b)) {
-                        const bf16x8 qf = R::bf(qb[b][s]);
-                        kq[b] = mma(qf, xf, kq[b]);
-                        if (b == X) *reinterpret_cast<bf16x8 *>(&st.Q[16 * X + ln][c]) = qf;
-                    }
-                } else if (kq_tile(b))
-                    kq[b] = mma(bf, xf, kq[b]);
-            }
+            kf[s] = R::bf(kw[s]);
+            *reinterpret_cast<bf16x8 *>(&st.K[16 * W + ln][c]) = kf[s];
+            if constexpr (MODE != KEEP) *reinterpret_cast<bf16x8 *>(&st.Q[16 * X + ln][c]) = R::bf(qx[s]);
         }
         {
             const int row = ptid / 4, c = (ptid % 4) * (4 * NC);
@@ -208,7 +183,24 @@ struct Producer {
             for (int i = 0; i < VL; ++i)
                 *reinterpret_cast<bf16x8 *>(&st.V[row][c + 8 * i]) = SW ? Rows<bf16>::bf(v[i]) : R::bf(v8[i]);
         }
+        __syncthreads();                 // rows of the chunk are in the stage
         next();
+        // tile products
+        f32x4 kk[4] = {}, kq[4] = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int c = 32 * s + 8 * lg;
+            bf16x8 xf = {};
+            if constexpr (MODE == FWD) xf = lds8(&st.Q[16 * X + ln][c]);
+            if constexpr (SW) xf = lds8(&st.K[16 * X + ln][c]);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                bf16x8 bf = {};
+                if (kk_tile(b) || (!SW && kq_tile(b))) bf = b == W ? kf[s] : lds8(&st.K[16 * b + ln][c]);
+                if (kk_tile(b)) kk[b] = mma(bf, kf[s], kk[b]);
+                if (kq_tile(b)) kq[b] = mma(SW ? lds8(&st.Q[16 * b + ln][c]) : bf, xf, kq[b]);
+            }
+        }
         // tiles: lane token x, row tokens y = 16 b + 4 lg + e; x is the later
         // one in the forward, the earlier one in the sweep
         const int xk = 16 * W + ln, xq = 16 * X + ln;
@@ -318,22 +310,29 @@ struct Producer {
 // eight channels of one 16-byte operand read
 __device__ __forceinline__ int channel(int t, int lg, int e) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1) + e; }
 
-__device__ __forceinline__ f32x4 mul_block(const Block &t, int lane, const Half &b, f32x4 c)
+// left operands in registers
+struct BlockRegs {
+    u32x2 h, m, l;
+    __device__ __forceinline__ BlockRegs(const Block &t, int lane) : h(t.p[0][lane]), m(t.p[1][lane]), l(t.p[2][lane]) {}
+};
+struct PairRegs {
+    bf16x8 h, m, l;
+    __device__ __forceinline__ PairRegs(const bf16x8 (*t)[WAVE], int lane) : h(t[0][lane]), m(t[1][lane]), l(t[2][lane]) {}
+};
+__device__ __forceinline__ f32x4 mul_block(const BlockRegs &t, const Half &b, f32x4 c)
 {
-    const u32x2 h = t.p[0][lane], m = t.p[1][lane], l = t.p[2][lane];
-    c = mma(join(h, l), b.lh, c);
-    c = mma(join(m, m), b.hm, c);
-    return mma(join(h, h), b.hm, c);
+    c = mma(join(t.h, t.l), b.lh, c);
+    c = mma(join(t.m, t.m), b.hm, c);
+    return mma(join(t.h, t.h), b.hm, c);
 }
-__device__ __forceinline__ f32x4 mul_pair(const bf16x8 (*t)[WAVE], int lane, const Parts<3> &b, f32x4 c)
+__device__ __forceinline__ f32x4 mul_pair(const PairRegs &t, const Parts<3> &b, f32x4 c)
 {
-    const bf16x8 h = t[0][lane], m = t[1][lane], l = t[2][lane];
-    c = mma(h, b.p[2], c);
-    c = mma(l, b.p[0], c);
-    c = mma(m, b.p[1], c);
-    c = mma(m, b.p[0], c);
-    c = mma(h, b.p[1], c);
-    return mma(h, b.p[0], c);
+    c = mma(t.h, b.p[2], c);
+    c = mma(t.l, b.p[0], c);
+    c = mma(t.m, b.p[1], c);
+    c = mma(t.m, b.p[0], c);
+    c = mma(t.h, b.p[1], c);
+    return mma(t.h, b.p[0], c);
 }
 
 template <typename TI, int DK, int NC, int MODE>
@@ -349,19 +348,33 @@ struct Consumer {
         return join(lds_tr(&X[r][c]), lds_tr(&X[r + 16][c]));
     }
 
-    // S += K^T (or Q^T) u over the tokens 32 s .. of the chunk
-    __device__ __forceinline__ void update(const bf16 (*M)[Stage<DK, NC, MODE>::LK], const Parts<3> &u, int s, int ln, int lg)
+    // row tiles t0 .. t1 of S += K^T (or Q^T) u over the tokens 32 s .. of the chunk
+    __device__ __forceinline__ void update(const bf16 (*M)[Stage<DK, NC, MODE>::LK], const Parts<3> &u, int s, int t0, int t1,
+                                           int ln, int lg)
     {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) S[t] = mma_parts<3>(transposed(M, t, s, ln, lg), u, S[t]);
+        for (int t = 0; t < RT; ++t)
+            if (t >= t0 && t < t1) S[t] = mma_parts<3>(transposed(M, t, s, ln, lg), u, S[t]);
     }
 
     // out: buffer of the chunk's rows of o (R); off: this lane's byte in row 4 lg
     __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Eye &eye, float scale, int w, int ln, int lg,
-                                            rsrc_t out, int row_bytes, int off)
+                                            rsrc_t out, int row_bytes, int off, bool more)
     {
         const int lane = ln + 16 * lg;
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        // Operands are requested a phase ahead: the phases are dependent
+        // chains of one wave, and the LDS latency would stand in each of
+        // their steps (scheduling barriers keep the requests where they are).
+        u32x2 vt[4];
+        f32x4 eg[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            vt[t] = lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
+            eg[t] = ld4f(&st.eG[16 * t + 4 * lg]);
+        }
+        const BlockRegs T0(st.T[0], lane), A10(st.Aone[0], lane), T1(st.T[1], lane);
+        __builtin_amdgcn_sched_barrier(0);
         f32x4 X[4] = {}, O[4] = {}, R[4];
         Parts<3> p[KS];
 #pragma unroll
@@ -369,12 +382,14 @@ struct Consumer {
             p[s] = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
 #pragma unroll
             for (int t = 0; t < 4; ++t) X[t] = mma_parts<3>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], X[t]);
+            if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }
+        const PairRegs A2(st.Apair[0], lane), A3(st.Apair[1], lane);
+        const float gam = st.gamma;
+        const f32x4 er0 = ld4f(&st.eR[4 * lg]), er1 = ld4f(&st.eR[16 + 4 * lg]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f32x4 v = widen(lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]));
-            R[t] = v - ld4f(&st.eG[16 * t + 4 * lg]) * X[t];
-        }
+        for (int t = 0; t < 4; ++t) R[t] = widen(vt[t]) - eg[t] * X[t];
         // the substitution is one long dependent chain: products that do not
         // wait for it stand between its steps
         const auto qs = [&](int s) {
@@ -386,26 +401,28 @@ struct Consumer {
         u32x2 h, m, l;
         Half x = split_half(R[0], eye, h, m, l);
         qs(0);
-        R[0] = mul_block(st.T[0], lane, x, zero);
+        R[0] = mul_block(T0, x, zero);
         qs(1);
         x = split_half(R[0], eye, h, m, l);
-        R[1] = mul_block(st.Aone[0], lane, x, R[1]);
+        R[1] = mul_block(A10, x, R[1]);
         qs(2);
         x = split_half(R[1], eye, h, m, l);
         qs(3);
-        R[1] = mul_block(st.T[1], lane, x, zero);
-        const float gam = st.gamma;
+        R[1] = mul_block(T1, x, zero);
+        const BlockRegs T2(st.T[2], lane), A32(st.Aone[1], lane), T3(st.T[3], lane);
+        const f32x4 er2 = ld4f(&st.eR[32 + 4 * lg]), er3 = ld4f(&st.eR[48 + 4 * lg]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < RT; ++t) S[t] *= gam;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) O[t] *= ld4f(&st.eG[16 * t + 4 * lg]);
+        for (int t = 0; t < 4; ++t) O[t] *= eg[t];
         const Parts<3> r01 = split_pair<3>(R[0], R[1], eye);
-        R[2] = mul_pair(st.Apair[0], lane, r01, R[2]);
-        R[3] = mul_pair(st.Apair[1], lane, r01, R[3]);
-        const Parts<3> u0 = split_pair<3>(ld4f(&st.eR[4 * lg]) * R[0], ld4f(&st.eR[16 + 4 * lg]) * R[1], eye);
+        R[2] = mul_pair(A2, r01, R[2]);
+        R[3] = mul_pair(A3, r01, R[3]);
+        const Parts<3> u0 = split_pair<3>(er0 * R[0], er1 * R[1], eye);
         x = split_half(R[2], eye, h, m, l);
-        update(st.K, u0, 0, ln, lg);
-        R[2] = mul_block(st.T[2], lane, x, zero);
+        update(st.K, u0, 0, 0, RT / 2, ln, lg);
+        R[2] = mul_block(T2, x, zero);
         // operands 0, 1, 2a, 2b, 3a, 3b: rows 0, 1, 2, 2, 3, 3 against tokens
         // 0-31 (2b, 3b: 32-63)
         const auto pr = [&](int i, int t, bf16x8 rh, bf16x8 rm) {
@@ -420,11 +437,12 @@ struct Consumer {
         pr(1, 1, r01.p[0], r01.p[1]);
         x = split_half(R[2], eye, h, m, l);
         pr(2, 2, r01.p[0], r01.p[1]);
-        R[3] = mul_block(st.Aone[1], lane, x, R[3]);
+        R[3] = mul_block(A32, x, R[3]);
         pr(4, 3, r01.p[0], r01.p[1]);
         x = split_half(R[3], eye, h, m, l);
-        R[3] = mul_block(st.T[3], lane, x, zero);
-        const Parts<3> u1 = split_pair<3>(ld4f(&st.eR[32 + 4 * lg]) * R[2], ld4f(&st.eR[48 + 4 * lg]) * R[3], eye);
+        update(st.K, u0, 0, RT / 2, RT, ln, lg);
+        R[3] = mul_block(T3, x, zero);
+        const Parts<3> u1 = split_pair<3>(er2 * R[2], er3 * R[3], eye);
         const Parts<2> r23 = split_pair<2>(R[2], R[3], eye);
         pr(3, 2, r23.p[0], r23.p[1]);
         pr(5, 3, r23.p[0], r23.p[1]);
@@ -438,7 +456,7 @@ struct Consumer {
                 else
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(R[t][e]), out, off + so, 0, 0);
             }
-        update(st.K, u1, 1, ln, lg);
+        update(st.K, u1, 1, 0, RT, ln, lg);
     }
 };
 
@@ -515,6 +533,7 @@ void gdr_chunk_kernel(Args a)
     load_state<DK / 16>(q.S, a.S0 ? a.S0 + st : nullptr, a.dv, lg);
     constexpr int es = MODE == FWD ? 2 : 4;
     const int rb = a.Hv * a.dv * es, off = 4 * lg * rb + (hv * a.dv + col + 16 * wave + ln) * es;
+    if (chunks > 0) __syncthreads();                     // rows of chunk 0
     for (int c = 0; c < chunks; ++c) {
         __syncthreads();
         int64_t tok;
@@ -525,7 +544,8 @@ void gdr_chunk_kernel(Args a)
             const int64_t slot = bos / C + n + c;
             store_state<DK / 16>(q.S, a.Sc + (slot * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln, a.dv, lg);
         }
-        q.forward(sm.st[c & 1], eye, a.scale, wave, ln, lg, make_rsrc(base + tok * rb, nrow * rb), rb, off);
+        q.forward(sm.st[c & 1], eye, a.scale, wave, ln, lg, make_rsrc(base + tok * rb, nrow * rb), rb, off,
+                  c + 1 < chunks);
     }
     if (MODE == FWD && a.S_T) store_state<DK / 16>(q.S, a.S_T + st, a.dv, lg);
 }
