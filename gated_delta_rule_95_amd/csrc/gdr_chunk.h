@@ -83,6 +83,15 @@ __device__ __forceinline__ f32x4 mma_parts(bf16x8 a, const Parts<NS> &b, f32x4 c
     return c;
 }
 
+// acc + (parts of a) * b: the transposed product, result column = b's row
+template <int NS>
+__device__ __forceinline__ f32x4 mma_by_parts(const Parts<NS> &a, bf16x8 b, f32x4 c)
+{
+#pragma unroll
+    for (int i = NS - 1; i >= 0; --i) c = mma(a.p[i], b, c);
+    return c;
+}
+
 // Products over 16 rows with both operands in three parts: the six products
 // of at least 2^-24 fill three 32-slot products,
 //   [Ah | Al] [Bl | Bh],  [Am | Am] [Bh | Bm],  [Ah | Ah] [Bh | Bm].

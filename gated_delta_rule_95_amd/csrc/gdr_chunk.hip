@@ -45,6 +45,7 @@ struct Stage {
     bf16x8 Apair[2][3][WAVE];                    // a block of rows against two of columns
     Block Aone[2], T[4];                         // block against block; inverted diagonal blocks
     float eG[C], eR[C];                          // e^G; b e^{G_C - G} (sweep: e^{G_C - G})
+    float eGs[C];                                // scale e^G
     float beta[C];
     float gamma;
 };
@@ -163,7 +164,9 @@ struct Producer {
         gp[2][lane] = beta;
         if constexpr (W == 0) {
             const float er = kda::fast_exp2((float)(Gend - G));
-            st.eG[lane] = kda::fast_exp2(gh);
+            const float eg = kda::fast_exp2(gh);
+            st.eG[lane] = eg;
+            st.eGs[lane] = scale * eg;
             st.eR[lane] = SW ? er : er * beta;
             st.beta[lane] = beta;
             if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
@@ -209,7 +212,7 @@ struct Producer {
         for (int b = 0; b < 4; ++b) {
             if (!kk_tile(b) && !kq_tile(b)) continue;
             const int y = 16 * b + 4 * lg;
-            const f32x4 yh = ld4f(&gp[0][y]), yl = ld4f(&gp[1][y]), yb = ld4f(&gp[2][y]);
+            const f32x4 yh = ld4f(&gp[0][y]), yl = ld4f(&gp[1][y]), yb = ld4f(&gp[2][y]), sb = scale * yb;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (kk_tile(b)) {
@@ -219,7 +222,7 @@ struct Producer {
                 }
                 if (kq_tile(b)) {
                     const float d = (ghq - yh[e]) + (glq - yl[e]);
-                    kq[b][e] = kda::fast_exp2(SW ? -d : d) * ((SW ? scale : yb[e]) * kq[b][e]);
+                    kq[b][e] = kda::fast_exp2(SW ? -d : d) * ((SW ? scale : sb[e]) * kq[b][e]);
                     if (b == X && !(SW ? y + e >= xq : y + e <= xq)) kq[b][e] = 0.f;
                 }
             }
@@ -357,8 +360,8 @@ struct Consumer {
             if (t >= t0 && t < t1) S[t] = mma_parts<3>(transposed(M, t, s, ln, lg), u, S[t]);
     }
 
-    // out: buffer of the chunk's rows of o (R); off: this lane's byte in row 4 lg
-    __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Eye &eye, float scale, int w, int ln, int lg,
+    // out: buffer of the chunk's rows of o (R); off: this lane's byte in block 0
+    __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Eye &eye, int w, int ln, int lg,
                                             rsrc_t out, int row_bytes, int off, bool more)
     {
         const int lane = ln + 16 * lg;
@@ -376,12 +379,12 @@ struct Consumer {
         const BlockRegs T0(st.T[0], lane), A10(st.Aone[0], lane), T1(st.T[1], lane);
         __builtin_amdgcn_sched_barrier(0);
         f32x4 X[4] = {}, O[4] = {}, R[4];
-        Parts<3> p[KS];
+        Parts<2> p[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            p[s] = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
+            p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = mma_parts<3>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], X[t]);
+            for (int t = 0; t < 4; ++t) X[t] = mma_parts<2>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], X[t]);
             if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }
         const PairRegs A2(st.Apair[0], lane), A3(st.Apair[1], lane);
@@ -390,13 +393,15 @@ struct Consumer {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < 4; ++t) R[t] = widen(vt[t]) - eg[t] * X[t];
-        // the substitution is one long dependent chain: products that do not
-        // wait for it stand between its steps
+        // The substitution is one long dependent chain: products that do not
+        // wait for it stand between its steps.  O is formed transposed (the
+        // operands of a product trade places), so that a lane holds four
+        // columns of one token and o goes out 8 bytes at a time.
         const auto qs = [&](int s) {
             if (MODE == FWD && s < KS)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    O[t] = mma_parts<2>(lds8(&st.Q[16 * t + ln][32 * s + 8 * lg]), Parts<2>{{p[s].p[0], p[s].p[1]}}, O[t]);
+                    O[t] = mma_by_parts(p[s], lds8(&st.Q[16 * t + ln][32 * s + 8 * lg]), O[t]);
         };
         u32x2 h, m, l;
         Half x = split_half(R[0], eye, h, m, l);
@@ -415,7 +420,7 @@ struct Consumer {
 #pragma unroll
         for (int t = 0; t < RT; ++t) S[t] *= gam;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) O[t] *= eg[t];
+        for (int t = 0; t < 4; ++t) O[t] *= st.eGs[16 * t + ln];
         const Parts<3> r01 = split_pair<3>(R[0], R[1], eye);
         R[2] = mul_pair(A2, r01, R[2]);
         R[3] = mul_pair(A3, r01, R[3]);
@@ -428,9 +433,9 @@ struct Consumer {
         const auto pr = [&](int i, int t, bf16x8 rh, bf16x8 rm) {
             if constexpr (MODE == FWD) {
                 const bf16x8 ph = st.P[0][i][lane], pm = st.P[1][i][lane];
-                O[t] = mma(pm, rh, O[t]);
-                O[t] = mma(ph, rm, O[t]);
-                O[t] = mma(ph, rh, O[t]);
+                O[t] = mma(rh, pm, O[t]);
+                O[t] = mma(rm, ph, O[t]);
+                O[t] = mma(rh, ph, O[t]);
             }
         };
         pr(0, 0, r01.p[0], r01.p[1]);
@@ -447,15 +452,13 @@ struct Consumer {
         pr(3, 2, r23.p[0], r23.p[1]);
         pr(5, 3, r23.p[0], r23.p[1]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (MODE == FWD) __builtin_amdgcn_raw_buffer_store_b64(pack4(O[t]), out, off + 16 * t * row_bytes, 0, 0);
+            else
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int so = (16 * t + e) * row_bytes;
-                if constexpr (MODE == FWD)
-                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)(scale * O[t][e])), out, off + so, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(R[t][e]), out, off + so, 0, 0);
-            }
+                for (int e = 0; e < 4; ++e)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(R[t][e]), out, off + (16 * t + e) * row_bytes, 0, 0);
+        }
         update(st.K, u1, 1, 0, RT, ln, lg);
     }
 };
@@ -532,7 +535,9 @@ void gdr_chunk_kernel(Args a)
     const int64_t st = ((int64_t)n * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln;
     load_state<DK / 16>(q.S, a.S0 ? a.S0 + st : nullptr, a.dv, lg);
     constexpr int es = MODE == FWD ? 2 : 4;
-    const int rb = a.Hv * a.dv * es, off = 4 * lg * rb + (hv * a.dv + col + 16 * wave + ln) * es;
+    // o: this lane's token and columns; R: its rows and column
+    const int rb = a.Hv * a.dv * es;
+    const int off = MODE == FWD ? ln * rb + (hv * a.dv + col + 16 * wave + 4 * lg) * es : 4 * lg * rb + (hv * a.dv + col + 16 * wave + ln) * es;
     if (chunks > 0) __syncthreads();                     // rows of chunk 0
     for (int c = 0; c < chunks; ++c) {
         __syncthreads();
@@ -544,7 +549,7 @@ void gdr_chunk_kernel(Args a)
             const int64_t slot = bos / C + n + c;
             store_state<DK / 16>(q.S, a.Sc + (slot * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln, a.dv, lg);
         }
-        q.forward(sm.st[c & 1], eye, a.scale, wave, ln, lg, make_rsrc(base + tok * rb, nrow * rb), rb, off,
+        q.forward(sm.st[c & 1], eye, wave, ln, lg, make_rsrc(base + tok * rb, nrow * rb), rb, off,
                   c + 1 < chunks);
     }
     if (MODE == FWD && a.S_T) store_state<DK / 16>(q.S, a.S_T + st, a.dv, lg);
