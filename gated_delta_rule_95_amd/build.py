@@ -23,7 +23,7 @@ ARCH = "gfx950"
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill.hip", "kda_noalloc.hip",
            "kda_spec.hip", "kda_backward.hip",
            "gdr_api.cpp", "gdr_decode.hip", "gdr_recurrent.hip", "gdr_grad.hip",
-           "gdr_chunk.hip", "gdr_save8.hip"]
+           "gdr_chunk.hip", "gdr_grad_chunk.hip", "gdr_save8.hip"]
 
 
 def hipcc() -> str:

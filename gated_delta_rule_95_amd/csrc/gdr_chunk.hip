@@ -45,7 +45,7 @@ struct Stage {
     bf16x8 Apair[2][3][WAVE];                    // a block of rows against two of columns
     Block Aone[2], T[4];                         // block against block; inverted diagonal blocks
     float eG[C], eR[C];                          // e^G; b e^{G_C - G} (sweep: e^{G_C - G})
-    float eGs[C];                                // scale e^G
+    float eGs[C], eGb[C];                        // scale e^G; (sweep) b e^G
     float beta[C];
     float gamma;
 };
@@ -167,6 +167,7 @@ struct Producer {
             const float eg = kda::fast_exp2(gh);
             st.eG[lane] = eg;
             st.eGs[lane] = scale * eg;
+            st.eGb[lane] = beta * eg;
             st.eR[lane] = SW ? er : er * beta;
             st.beta[lane] = beta;
             if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
@@ -352,17 +353,51 @@ struct Consumer {
     }
 
     // row tiles t0 .. t1 of S += K^T (or Q^T) u over the tokens 32 s .. of the chunk
-    __device__ __forceinline__ void update(const bf16 (*M)[Stage<DK, NC, MODE>::LK], const Parts<3> &u, int s, int t0, int t1,
-                                           int ln, int lg)
+    template <int NS>
+    __device__ __forceinline__ void update(const bf16 (*M)[Stage<DK, NC, MODE>::LK], const Parts<NS> &u, int s, int t0,
+                                           int t1, int ln, int lg)
     {
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-            if (t >= t0 && t < t1) S[t] = mma_parts<3>(transposed(M, t, s, ln, lg), u, S[t]);
+            if (t >= t0 && t < t1) S[t] = mma_parts<NS>(transposed(M, t, s, ln, lg), u, S[t]);
     }
 
-    // out: buffer of the chunk's rows of o (R); off: this lane's byte in block 0
+    // Two blocks of 16 rows in fp32, from their three parts: a product with
+    // the identity transposes a part exactly, and a lane stores four columns
+    // of one row.  off: this lane's byte in the first block.
+    static __device__ __forceinline__ void put_rows(const Parts<3> &r, const Eye &eye, rsrc_t out, int off, int row_bytes)
+    {
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        const f32x4 x = -mma_by_parts(r, eye.a, zero), y = -mma_by_parts(r, eye.b, zero);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), out, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, off + 16 * row_bytes, 0, 0);
+    }
+
+    // The state's two parts at a chunk border, as the gradient kernel's
+    // operands: [part][16 channels][32 columns] tiles of 1 KiB in lane order,
+    // lane (channel, lg) holding columns 8 lg .. 8 lg + 7.  dst: the head's
+    // tiles; cw: this wave's first column.
+    static __device__ __forceinline__ void put_parts(const Parts<2> *p, const Eye &eye, bf16x8 *dst, int dv, int cw, int ln,
+                                                     int lg)
+    {
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        const int ks = dv / 32, lane = 8 * ((ln >> 2) & 1) + (ln & 3) + 16 * (((cw >> 4) & 1) * 2 + (lg >> 1));
+        u32x2 *d = reinterpret_cast<u32x2 *>(dst + ((ln >> 3) * ks + cw / 32) * WAVE + lane) + (lg & 1);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                u32x2 *at = d + 2 * WAVE * ks * (i * RT + 2 * s);
+                __builtin_nontemporal_store(pack4(-mma(p[s].p[i], eye.a, zero)), at);
+                __builtin_nontemporal_store(pack4(-mma(p[s].p[i], eye.b, zero)), at + 8);
+            }
+    }
+
+    // out: buffer of the chunk's rows of o (R); off: this lane's byte in block
+    // 0; keep: where the entry state goes (KEEP)
     __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Eye &eye, int w, int ln, int lg,
-                                            rsrc_t out, int row_bytes, int off, bool more)
+                                            rsrc_t out, int row_bytes, int off, bf16x8 *keep, int dv, int cw,
+                                            bool more)
     {
         const int lane = ln + 16 * lg;
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -387,6 +422,7 @@ struct Consumer {
             for (int t = 0; t < 4; ++t) X[t] = mma_parts<2>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], X[t]);
             if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }
+        if constexpr (MODE == KEEP) put_parts(p, eye, keep, dv, cw, ln, lg);
         const PairRegs A2(st.Apair[0], lane), A3(st.Apair[1], lane);
         const float gam = st.gamma;
         const f32x4 er0 = ld4f(&st.eR[4 * lg]), er1 = ld4f(&st.eR[16 + 4 * lg]);
@@ -448,18 +484,109 @@ struct Consumer {
         update(st.K, u0, 0, RT / 2, RT, ln, lg);
         R[3] = mul_block(T3, x, zero);
         const Parts<3> u1 = split_pair<3>(er2 * R[2], er3 * R[3], eye);
-        const Parts<2> r23 = split_pair<2>(R[2], R[3], eye);
+        const Parts<2> r23 = MODE == FWD ? split_pair<2>(R[2], R[3], eye) : Parts<2>{};
         pr(3, 2, r23.p[0], r23.p[1]);
         pr(5, 3, r23.p[0], r23.p[1]);
+        if constexpr (MODE == FWD) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if constexpr (MODE == FWD) __builtin_amdgcn_raw_buffer_store_b64(pack4(O[t]), out, off + 16 * t * row_bytes, 0, 0);
-            else
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(R[t][e]), out, off + (16 * t + e) * row_bytes, 0, 0);
+            for (int t = 0; t < 4; ++t)
+                __builtin_amdgcn_raw_buffer_store_b64(pack4(O[t]), out, off + 16 * t * row_bytes, 0, 0);
+        } else {
+            put_rows(r01, eye, out, off, row_bytes);
+            put_rows(split_pair<3>(R[2], R[3], eye), eye, out, off + 32 * row_bytes, row_bytes);
         }
         update(st.K, u1, 1, 0, RT, ln, lg);
+    }
+
+    // out: buffer of the chunk's rows of Ub; offs: this lane's byte in block
+    // 0 of it and of dv; keep: where the exit cotangent goes
+    __device__ __forceinline__ void sweep(const Stage<DK, NC, MODE> &st, const Eye &eye, int w, int ln, int lg, rsrc_t out,
+                                          int row_bytes, int off, rsrc_t dval, int vrow_bytes, int voff, bf16x8 *keep, int dv,
+                                          int cw, bool more)
+    {
+        const int lane = ln + 16 * lg;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        u32x2 d[4];
+        f32x4 er[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            d[t] = lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
+            er[t] = ld4f(&st.eR[16 * t + 4 * lg]);
+        }
+        const BlockRegs T3(st.T[3], lane), A23(st.Aone[0], lane), T2(st.T[2], lane);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 F[4] = {};
+        Parts<2> p[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) F[t] = mma_parts<2>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], F[t]);
+            if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
+        }
+        put_parts(p, eye, keep, dv, cw, ln, lg);
+        const PairRegs A1(st.Apair[0], lane), A0(st.Apair[1], lane);
+        const float gam = st.gamma;
+        f32x4 eg[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) eg[t] = ld4f(&st.eGs[16 * t + 4 * lg]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) F[t] *= er[t];
+        const bf16x8 d01 = join(d[0], d[1]), d23 = join(d[2], d[3]);
+        // operands 0a, 0b, 1a, 1b, 2, 3: rows 0, 0, 1, 1, 2, 3 against tokens
+        // 32-63 (0a, 1a: 0-31)
+        const auto pd = [&](int i, int t, bf16x8 x) {
+            F[t] = mma(st.P[1][i][lane], x, F[t]);
+            F[t] = mma(st.P[0][i][lane], x, F[t]);
+        };
+        pd(5, 3, d23);
+        pd(4, 2, d23);
+        u32x2 h, m, l;
+        Half x = split_half(F[3], eye, h, m, l);
+        pd(3, 1, d23);
+        F[3] = mul_block(T3, x, zero);
+        pd(1, 0, d23);
+        x = split_half(F[3], eye, h, m, l);
+        pd(2, 1, d01);
+        F[2] = mul_block(A23, x, F[2]);
+        pd(0, 0, d01);
+        x = split_half(F[2], eye, h, m, l);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) S[t] *= gam;
+        const Parts<2> w01 = split_pair<2>(eg[0] * widen(d[0]), eg[1] * widen(d[1]), eye);
+        const Parts<2> w23 = split_pair<2>(eg[2] * widen(d[2]), eg[3] * widen(d[3]), eye);
+        F[2] = mul_block(T2, x, zero);
+        const BlockRegs T1(st.T[1], lane), A01(st.Aone[1], lane), T0(st.T[0], lane);
+        f32x4 eb[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) eb[t] = ld4f(&st.eGb[16 * t + 4 * lg]);
+        __builtin_amdgcn_sched_barrier(0);
+        const Parts<3> u23 = split_pair<3>(F[2], F[3], eye);
+        F[1] = mul_pair(A1, u23, F[1]);
+        F[0] = mul_pair(A0, u23, F[0]);
+        const Parts<3> y23 = split_pair<3>(-eb[2] * F[2], -eb[3] * F[3], eye);
+        x = split_half(F[1], eye, h, m, l);
+        update(st.Q, w01, 0, 0, RT, ln, lg);
+        F[1] = mul_block(T1, x, zero);
+        update(st.Q, w23, 1, 0, RT / 2, ln, lg);
+        x = split_half(F[1], eye, h, m, l);
+        update(st.Q, w23, 1, RT / 2, RT, ln, lg);
+        F[0] = mul_block(A01, x, F[0]);
+        update(st.K, y23, 1, 0, RT / 2, ln, lg);
+        x = split_half(F[0], eye, h, m, l);
+        update(st.K, y23, 1, RT / 2, RT, ln, lg);
+        F[0] = mul_block(T0, x, zero);
+        const Parts<3> u01 = split_pair<3>(F[0], F[1], eye);
+        const Parts<3> y01 = split_pair<3>(-eb[0] * F[0], -eb[1] * F[1], eye);
+        // dv = beta Ub, from the transposed rows
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f32x4 u = -mma_by_parts(t < 2 ? u01 : u23, t & 1 ? eye.b : eye.a, zero);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, u), out, off + 16 * t * row_bytes, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(pack4(st.beta[16 * t + ln] * u), dval, voff + 16 * t * vrow_bytes, 0, 0);
+        }
+        update(st.K, y01, 0, 0, RT, ln, lg);
     }
 };
 
@@ -516,9 +643,11 @@ void gdr_chunk_kernel(Args a)
         (&sm.st[1].P[0][0][0])[i] = bf16x8{};
     }
     __syncthreads();
+    // step c of the chain is chunk c, or from the last one on in the sweep
     const auto where = [&](int c, int64_t &tok, int &nrow) {
-        tok = bos + (int64_t)c * C;
-        nrow = len - c * C < C ? len - c * C : C;
+        const int i = MODE == SWEEP ? chunks - 1 - c : c;
+        tok = bos + (int64_t)i * C;
+        nrow = len - i * C < C ? len - i * C : C;
     };
     if (wave >= NC) {
         const int w = wave - NC, ptid = tid - NC * WAVE;
@@ -533,26 +662,31 @@ void gdr_chunk_kernel(Args a)
     const Eye eye = make_eye(lane);
     Consumer<TI, DK, NC, MODE> q;
     const int64_t st = ((int64_t)n * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln;
-    load_state<DK / 16>(q.S, a.S0 ? a.S0 + st : nullptr, a.dv, lg);
+    const float *init = MODE == SWEEP ? a.dS_T : a.S0;
+    load_state<DK / 16>(q.S, init ? init + st : nullptr, a.dv, lg);
+    // a lane's place in rows of o, R, Ub and dv: its token and four columns
+    const int cw = col + 16 * wave, e0 = (ln * a.Hv + hv) * a.dv + cw + 4 * lg;
     constexpr int es = MODE == FWD ? 2 : 4;
-    // o: this lane's token and columns; R: its rows and column
     const int rb = a.Hv * a.dv * es;
-    const int off = MODE == FWD ? ln * rb + (hv * a.dv + col + 16 * wave + 4 * lg) * es : 4 * lg * rb + (hv * a.dv + col + 16 * wave + ln) * es;
+    float *border = MODE == SWEEP ? a.Lc : a.Sc;
     if (chunks > 0) __syncthreads();                     // rows of chunk 0
     for (int c = 0; c < chunks; ++c) {
         __syncthreads();
         int64_t tok;
         int nrow;
         where(c, tok, nrow);
-        const char *base = MODE == FWD ? static_cast<const char *>(a.o) : reinterpret_cast<const char *>(a.R);
-        if constexpr (MODE == KEEP) {
-            const int64_t slot = bos / C + n + c;
-            store_state<DK / 16>(q.S, a.Sc + (slot * a.Hv + hv) * DK * a.dv + col + 16 * wave + ln, a.dv, lg);
-        }
-        q.forward(sm.st[c & 1], eye, wave, ln, lg, make_rsrc(base + tok * rb, nrow * rb), rb, off,
-                  c + 1 < chunks);
+        const char *base = MODE == FWD ? static_cast<const char *>(a.o) : reinterpret_cast<const char *>(MODE == KEEP ? a.R : a.Ub);
+        const rsrc_t out = make_rsrc(base + tok * rb, nrow * rb);
+        const int64_t slot = bos / C + n + (MODE == SWEEP ? chunks - 1 - c : c);
+        bf16x8 *keep = reinterpret_cast<bf16x8 *>(border + (slot * a.Hv + hv) * DK * a.dv);
+        if constexpr (MODE == SWEEP) {
+            const rsrc_t dval = make_rsrc(static_cast<char *>(a.dval) + tok * (rb / 2), nrow * (rb / 2));
+            q.sweep(sm.st[c & 1], eye, wave, ln, lg, out, rb, e0 * 4, dval, rb / 2, e0 * 2, keep, a.dv, cw, c + 1 < chunks);
+        } else
+            q.forward(sm.st[c & 1], eye, wave, ln, lg, out, rb, e0 * es, keep, a.dv, cw, c + 1 < chunks);
     }
-    if (MODE == FWD && a.S_T) store_state<DK / 16>(q.S, a.S_T + st, a.dv, lg);
+    float *fin = MODE == FWD ? a.S_T : MODE == SWEEP ? a.dS0 : nullptr;
+    if (fin) store_state<DK / 16>(q.S, fin + st, a.dv, lg);
 }
 
 template <typename TI, int DK, int NC, int MODE>
@@ -573,6 +707,19 @@ hipError_t launch_t(const Args &a)
 hipError_t launch_chunk_fwd(const Args &a)
 {
     return a.dk == 128 ? launch_t<bf16, 128, 4, FWD>(a) : launch_t<bf16, 64, 4, FWD>(a);
+}
+
+template <typename TI>
+static hipError_t keep_and_sweep(const Args &a)
+{
+    const hipError_t e = a.dk == 128 ? launch_t<TI, 128, 4, KEEP>(a) : launch_t<TI, 64, 4, KEEP>(a);
+    if (e != hipSuccess) return e;
+    return a.dk == 128 ? launch_t<TI, 128, 4, SWEEP>(a) : launch_t<TI, 64, 4, SWEEP>(a);
+}
+
+hipError_t launch_chunk_keep_sweep(const Args &a)
+{
+    return a.in == In::BF16 ? keep_and_sweep<bf16>(a) : keep_and_sweep<e4m3>(a);
 }
 
 }  // namespace gdr

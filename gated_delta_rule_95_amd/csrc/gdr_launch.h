@@ -35,7 +35,8 @@ struct Args {
     const float *dS_T;
     void *dq, *dkey, *dval;
     float *dg, *dbeta, *dS0;
-    float *Sc, *Lc;                      // [slots, Hv, dk, dv] chunk-entry states, exit cotangents
+    float *Sc, *Lc;                      // [slots, Hv, dk * dv] chunk-entry states, exit cotangents (in the
+                                         // form's own order, 4 bytes an element)
     float *R, *Ub;                       // [n_tokens, Hv, dv]
     hipStream_t stream;
 };
@@ -67,6 +68,8 @@ hipError_t launch_recurrent_keep(const Args &a, int C);
 hipError_t launch_recurrent_sweep(const Args &a, int C);
 hipError_t launch_grad32(const Args &a);
 hipError_t launch_chunk_fwd(const Args &a);
+hipError_t launch_chunk_keep_sweep(const Args &a);
+hipError_t launch_chunk_grad(const Args &a);
 hipError_t launch_decode(const DecodeArgs &a);
 hipError_t launch_save8(const void *x, int64_t rows, int d, uint8_t *x8, uint8_t *xe, hipStream_t s);
 hipError_t launch_load8(const uint8_t *x8, const uint8_t *xe, int64_t rows, int d, void *x,
