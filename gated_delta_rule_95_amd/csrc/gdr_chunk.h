@@ -113,6 +113,18 @@ __device__ __forceinline__ Half split_half(f32x4 x, const Eye &eye, u32x2 &h, u3
 
 __device__ __forceinline__ bf16x8 lds8(const void *p) { return *static_cast<const bf16x8 *>(p); }
 
+// Rows of 2 D bytes with their 16-byte pieces exchanged by row, so that 16
+// lanes reading one piece of 16 rows touch every bank once.
+template <int D>
+struct Swz {
+    static constexpr int NP = D / 8;             // pieces a row
+    static __device__ __forceinline__ int at(int row, int c)
+    {
+        const int x = NP >= 16 ? row & 15 : (row >> 1) & 7;
+        return row * D + (((c >> 3) ^ x) << 3) + (c & 7);
+    }
+};
+
 // Transposing LDS read: lane (ln, lg) gets four rows of one column, given the
 // address of row (ln / 4) of its group's four rows, columns 4 (ln % 4) ..
 __device__ __forceinline__ u32x2 lds_tr(const bf16 *p)

@@ -37,11 +37,11 @@ struct Block {
 
 template <int DK, int NC, int MODE>
 struct Stage {
-    static constexpr int LK = DK + 16;           // odd multiples of 32 bytes: no bank conflicts
-    static constexpr int LV = 16 * NC + 16;
-    bf16 K[C][LK], Q[C][LK], V[C][LV];           // V: v, or dO in the sweep
+    static constexpr int LV = 16 * NC + 8;
+    static constexpr int PP = MODE == SWEEP ? 3 : 2;
+    bf16 K[C * DK], Q[C * DK], V[C][LV];         // K, Q by Swz; V: v, or dO in the sweep
     // operands of 1 KiB in lane order
-    bf16x8 P[2][MODE == KEEP ? 1 : 6][WAVE];   // [part][0, 1, 2a, 2b, 3a, 3b]
+    bf16x8 P[PP][MODE == KEEP ? 1 : 6][WAVE];   // [part][0, 1, 2a, 2b, 3a, 3b]
     bf16x8 Apair[2][3][WAVE];                    // a block of rows against two of columns
     Block Aone[2], T[4];                         // block against block; inverted diagonal blocks
     float eG[C], eR[C];                          // e^G; b e^{G_C - G} (sweep: e^{G_C - G})
@@ -178,8 +178,8 @@ struct Producer {
         for (int s = 0; s < KS; ++s) {
             const int c = 32 * s + 8 * lg;
             kf[s] = R::bf(kw[s]);
-            *reinterpret_cast<bf16x8 *>(&st.K[16 * W + ln][c]) = kf[s];
-            if constexpr (MODE != KEEP) *reinterpret_cast<bf16x8 *>(&st.Q[16 * X + ln][c]) = R::bf(qx[s]);
+            *reinterpret_cast<bf16x8 *>(&st.K[Swz<DK>::at(16 * W + ln, c)]) = kf[s];
+            if constexpr (MODE != KEEP) *reinterpret_cast<bf16x8 *>(&st.Q[Swz<DK>::at(16 * X + ln, c)]) = R::bf(qx[s]);
         }
         {
             const int row = ptid / 4, c = (ptid % 4) * (4 * NC);
@@ -195,14 +195,14 @@ struct Producer {
         for (int s = 0; s < KS; ++s) {
             const int c = 32 * s + 8 * lg;
             bf16x8 xf = {};
-            if constexpr (MODE == FWD) xf = lds8(&st.Q[16 * X + ln][c]);
-            if constexpr (SW) xf = lds8(&st.K[16 * X + ln][c]);
+            if constexpr (MODE == FWD) xf = lds8(&st.Q[Swz<DK>::at(16 * X + ln, c)]);
+            if constexpr (SW) xf = lds8(&st.K[Swz<DK>::at(16 * X + ln, c)]);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 bf16x8 bf = {};
-                if (kk_tile(b) || (!SW && kq_tile(b))) bf = b == W ? kf[s] : lds8(&st.K[16 * b + ln][c]);
+                if (kk_tile(b) || (!SW && kq_tile(b))) bf = b == W ? kf[s] : lds8(&st.K[Swz<DK>::at(16 * b + ln, c)]);
                 if (kk_tile(b)) kk[b] = mma(bf, kf[s], kk[b]);
-                if (kq_tile(b)) kq[b] = mma(SW ? lds8(&st.Q[16 * b + ln][c]) : bf, xf, kq[b]);
+                if (kq_tile(b)) kq[b] = mma(SW ? lds8(&st.Q[Swz<DK>::at(16 * b + ln, c)]) : bf, xf, kq[b]);
             }
         }
         // tiles: lane token x, row tokens y = 16 b + 4 lg + e; x is the later
@@ -242,10 +242,13 @@ struct Producer {
             if (kq_tile(b)) {
                 constexpr int r = X;
                 const int op = SW ? (r < 2 ? 2 * r + (b >> 1) : r + 2) : (r < 2 ? r : 2 * r - 2 + (b >> 1));
-                const u32x2 h = pack4(kq[b]);
-                const f32x4 rest = mma(eye.a, join(h, h), kq[b]);
-                reinterpret_cast<u32x2 *>(&st.P[0][op][lane])[b & 1] = h;
-                reinterpret_cast<u32x2 *>(&st.P[1][op][lane])[b & 1] = pack4(rest);
+                f32x4 x = kq[b];
+#pragma unroll
+                for (int i = 0; i < St::PP; ++i) {
+                    const u32x2 h = pack4(x);
+                    reinterpret_cast<u32x2 *>(&st.P[i][op][lane])[b & 1] = h;
+                    if (i + 1 < St::PP) x = mma(eye.a, join(h, h), x);
+                }
             }
         }
         // (I + A)^-1 of the diagonal block by rows: lane row i = ln solves
@@ -346,15 +349,16 @@ struct Consumer {
     f32x4 S[RT];
 
     // K^T or Q^T operand: channels of row tile ct against tokens 32 s ..
-    static __device__ __forceinline__ bf16x8 transposed(const bf16 (*X)[Stage<DK, NC, MODE>::LK], int ct, int s, int ln, int lg)
+    static __device__ __forceinline__ bf16x8 transposed(const bf16 *X, int ct, int s, int ln, int lg)
     {
         const int c = 32 * (ct >> 1) + 8 * (ln & 3) + 4 * (ct & 1), r = 32 * s + 4 * lg + (ln >> 2);
-        return join(lds_tr(&X[r][c]), lds_tr(&X[r + 16][c]));
+        const bf16 *p = X + Swz<DK>::at(r, c);           // row + 16: the same exchange of pieces
+        return join(lds_tr(p), lds_tr(p + 16 * DK));
     }
 
     // row tiles t0 .. t1 of S += K^T (or Q^T) u over the tokens 32 s .. of the chunk
     template <int NS>
-    __device__ __forceinline__ void update(const bf16 (*M)[Stage<DK, NC, MODE>::LK], const Parts<NS> &u, int s, int t0,
+    __device__ __forceinline__ void update(const bf16 *M, const Parts<NS> &u, int s, int t0,
                                            int t1, int ln, int lg)
     {
 #pragma unroll
@@ -373,30 +377,25 @@ struct Consumer {
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, off + 16 * row_bytes, 0, 0);
     }
 
-    // The state's two parts at a chunk border, as the gradient kernel's
-    // operands: [part][16 channels][32 columns] tiles of 1 KiB in lane order,
-    // lane (channel, lg) holding columns 8 lg .. 8 lg + 7.  dst: the head's
-    // tiles; cw: this wave's first column.
-    static __device__ __forceinline__ void put_parts(const Parts<2> *p, const Eye &eye, bf16x8 *dst, int dv, int cw, int ln,
-                                                     int lg)
+    // The state at a chunk border in fp32, in the order of the gradient
+    // kernel's operands: tiles [16 channels][32 columns], each as two halves of
+    // 1 KiB in lane order, lane (channel, lg) holding the columns 8 lg ..
+    // 8 lg + 3 in the first and the next four in the second.  dst: the head's
+    // tiles; cw: this wave's first column; row tiles 2 s and 2 s + 1.
+    static __device__ __forceinline__ void put_state(const Parts<3> &p, int s, const Eye &eye, float *dst, int dv, int cw,
+                                                     int ln, int lg)
     {
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         const int ks = dv / 32, lane = 8 * ((ln >> 2) & 1) + (ln & 3) + 16 * (((cw >> 4) & 1) * 2 + (lg >> 1));
-        u32x2 *d = reinterpret_cast<u32x2 *>(dst + ((ln >> 3) * ks + cw / 32) * WAVE + lane) + (lg & 1);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                u32x2 *at = d + 2 * WAVE * ks * (i * RT + 2 * s);
-                __builtin_nontemporal_store(pack4(-mma(p[s].p[i], eye.a, zero)), at);
-                __builtin_nontemporal_store(pack4(-mma(p[s].p[i], eye.b, zero)), at + 8);
-            }
+        f32x4 *d = reinterpret_cast<f32x4 *>(dst) + (((2 * s + (ln >> 3)) * ks + cw / 32) * 2 + (lg & 1)) * WAVE + lane;
+        __builtin_nontemporal_store(-mma_by_parts(p, eye.a, zero), d);
+        __builtin_nontemporal_store(-mma_by_parts(p, eye.b, zero), d + 4);
     }
 
     // out: buffer of the chunk's rows of o (R); off: this lane's byte in block
     // 0; keep: where the entry state goes (KEEP)
     __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Eye &eye, int w, int ln, int lg,
-                                            rsrc_t out, int row_bytes, int off, bf16x8 *keep, int dv, int cw,
+                                            rsrc_t out, int row_bytes, int off, float *keep, int dv, int cw,
                                             bool more)
     {
         const int lane = ln + 16 * lg;
@@ -417,12 +416,16 @@ struct Consumer {
         Parts<2> p[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
+            if constexpr (MODE == KEEP) {
+                const Parts<3> x = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
+                p[s] = Parts<2>{{x.p[0], x.p[1]}};
+                put_state(x, s, eye, keep, dv, cw, ln, lg);
+            } else
+                p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = mma_parts<2>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], X[t]);
+            for (int t = 0; t < 4; ++t) X[t] = mma_parts<2>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p[s], X[t]);
             if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }
-        if constexpr (MODE == KEEP) put_parts(p, eye, keep, dv, cw, ln, lg);
         const PairRegs A2(st.Apair[0], lane), A3(st.Apair[1], lane);
         const float gam = st.gamma;
         const f32x4 er0 = ld4f(&st.eR[4 * lg]), er1 = ld4f(&st.eR[16 + 4 * lg]);
@@ -437,7 +440,7 @@ struct Consumer {
             if (MODE == FWD && s < KS)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    O[t] = mma_by_parts(p[s], lds8(&st.Q[16 * t + ln][32 * s + 8 * lg]), O[t]);
+                    O[t] = mma_by_parts(p[s], lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
         };
         u32x2 h, m, l;
         Half x = split_half(R[0], eye, h, m, l);
@@ -501,7 +504,7 @@ struct Consumer {
     // out: buffer of the chunk's rows of Ub; offs: this lane's byte in block
     // 0 of it and of dv; keep: where the exit cotangent goes
     __device__ __forceinline__ void sweep(const Stage<DK, NC, MODE> &st, const Eye &eye, int w, int ln, int lg, rsrc_t out,
-                                          int row_bytes, int off, rsrc_t dval, int vrow_bytes, int voff, bf16x8 *keep, int dv,
+                                          int row_bytes, int off, rsrc_t dval, int vrow_bytes, int voff, float *keep, int dv,
                                           int cw, bool more)
     {
         const int lane = ln + 16 * lg;
@@ -516,15 +519,14 @@ struct Consumer {
         const BlockRegs T3(st.T[3], lane), A23(st.Aone[0], lane), T2(st.T[2], lane);
         __builtin_amdgcn_sched_barrier(0);
         f32x4 F[4] = {};
-        Parts<2> p[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
+            const Parts<3> p = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
+            put_state(p, s, eye, keep, dv, cw, ln, lg);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) F[t] = mma_parts<2>(lds8(&st.K[16 * t + ln][32 * s + 8 * lg]), p[s], F[t]);
+            for (int t = 0; t < 4; ++t) F[t] = mma_parts<3>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p, F[t]);
             if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }
-        put_parts(p, eye, keep, dv, cw, ln, lg);
         const PairRegs A1(st.Apair[0], lane), A0(st.Apair[1], lane);
         const float gam = st.gamma;
         f32x4 eg[4];
@@ -537,6 +539,7 @@ struct Consumer {
         // operands 0a, 0b, 1a, 1b, 2, 3: rows 0, 0, 1, 1, 2, 3 against tokens
         // 32-63 (0a, 1a: 0-31)
         const auto pd = [&](int i, int t, bf16x8 x) {
+            F[t] = mma(st.P[2][i][lane], x, F[t]);
             F[t] = mma(st.P[1][i][lane], x, F[t]);
             F[t] = mma(st.P[0][i][lane], x, F[t]);
         };
@@ -554,8 +557,8 @@ struct Consumer {
         x = split_half(F[2], eye, h, m, l);
 #pragma unroll
         for (int t = 0; t < RT; ++t) S[t] *= gam;
-        const Parts<2> w01 = split_pair<2>(eg[0] * widen(d[0]), eg[1] * widen(d[1]), eye);
-        const Parts<2> w23 = split_pair<2>(eg[2] * widen(d[2]), eg[3] * widen(d[3]), eye);
+        const Parts<3> w01 = split_pair<3>(eg[0] * widen(d[0]), eg[1] * widen(d[1]), eye);
+        const Parts<3> w23 = split_pair<3>(eg[2] * widen(d[2]), eg[3] * widen(d[3]), eye);
         F[2] = mul_block(T2, x, zero);
         const BlockRegs T1(st.T[1], lane), A01(st.Aone[1], lane), T0(st.T[0], lane);
         f32x4 eb[4];
@@ -678,7 +681,7 @@ void gdr_chunk_kernel(Args a)
         const char *base = MODE == FWD ? static_cast<const char *>(a.o) : reinterpret_cast<const char *>(MODE == KEEP ? a.R : a.Ub);
         const rsrc_t out = make_rsrc(base + tok * rb, nrow * rb);
         const int64_t slot = bos / C + n + (MODE == SWEEP ? chunks - 1 - c : c);
-        bf16x8 *keep = reinterpret_cast<bf16x8 *>(border + (slot * a.Hv + hv) * DK * a.dv);
+        float *keep = border + (slot * a.Hv + hv) * DK * a.dv;
         if constexpr (MODE == SWEEP) {
             const rsrc_t dval = make_rsrc(static_cast<char *>(a.dval) + tok * (rb / 2), nrow * (rb / 2));
             q.sweep(sm.st[c & 1], eye, wave, ln, lg, out, rb, e0 * 4, dval, rb / 2, e0 * 2, keep, a.dv, cw, c + 1 < chunks);

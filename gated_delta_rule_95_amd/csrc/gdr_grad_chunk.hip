@@ -7,26 +7,18 @@
 // order; each of its d_k / 16 waves owns 16 key channels of dq and dk.  Everything is formed transposed, result rows = key channels and
 // columns = tokens: the state's operands come straight from memory in the
 // order the sweeps left them, decays and masks are per-lane scalars, and dq,
-// dk go out 8 bytes at a time.  fp32 operands are held in two bf16 parts
-// (16 bits), products of two such operands without the smallest of the four.
+// dk go out 8 bytes at a time.
+//
+// Operands of the products that dg depends on are held in three bf16 parts
+// and multiplied without the parts' products below 2^-24 (with two parts dg
+// was off by 4e-6 of its norm, with three by 6e-7: sums in fp32 are little
+// better); dP and dN, which only dq and dk see, in two.
 #include "gdr_chunk.h"
 
 namespace gdr {
 namespace {
 
 constexpr int C = 64;
-
-// Rows of 2 D bytes with their 16-byte pieces exchanged by row, so that 16
-// lanes reading one piece of 16 rows touch every bank once.
-template <int D>
-struct Swz {
-    static constexpr int NP = D / 8;             // pieces a row
-    static __device__ __forceinline__ int at(int row, int c)
-    {
-        const int x = NP >= 16 ? row & 15 : (row >> 1) & 7;
-        return row * D + (((c >> 3) ^ x) << 3) + (c & 7);
-    }
-};
 
 // waves, and value columns staged at a time
 template <int DK, int DV>
@@ -40,7 +32,7 @@ struct alignas(16) GradSmem {
     static constexpr int NW = Shape<DK, DV>::NW, SW = Shape<DK, DV>::SW;
     bf16 q[C * DK], k[C * DK];
     union {
-        bf16 rows[5][C * SW];                    // dO, U hi, U lo, Yb hi, Yb lo
+        bf16 rows[7][C * SW];                    // dO; U, Yb in three parts each
         bf16 mat[4][C * C];                      // dP hi, dP lo, dN + dN^T hi, lo   [i][j]
     };
     float G[2][C], a[NW][C], b[NW][C], e[8][C], rev[C], ls[NW];
@@ -113,12 +105,30 @@ __device__ __forceinline__ T scan_step(T x)
         return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, ROWS, 0xf, false));
 }
 
-// hi and lo parts of eight values
-__device__ __forceinline__ void split8(const f32x4 x, const f32x4 y, bf16x8 &h, bf16x8 &l)
+// the three parts of eight values
+__device__ __forceinline__ Parts<3> split8(f32x4 x, f32x4 y)
 {
-    const u32x2 hx = pack4(x), hy = pack4(y);
-    h = join(hx, hy);
-    l = join(pack4(x - widen(hx)), pack4(y - widen(hy)));
+    Parts<3> r;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const u32x2 hx = pack4(x), hy = pack4(y);
+        r.p[i] = join(hx, hy);
+        if (i < 2) {
+            x -= widen(hx);
+            y -= widen(hy);
+        }
+    }
+    return r;
+}
+// a b + c, both in three parts
+__device__ __forceinline__ f32x4 mma33(const Parts<3> &a, const Parts<3> &b, f32x4 c)
+{
+    c = mma(a.p[0], b.p[2], c);
+    c = mma(a.p[2], b.p[0], c);
+    c = mma(a.p[1], b.p[1], c);
+    c = mma(a.p[0], b.p[1], c);
+    c = mma(a.p[1], b.p[0], c);
+    return mma(a.p[0], b.p[0], c);
 }
 
 template <typename TI, int DK, int DV>
@@ -180,10 +190,8 @@ void gdr_grad_chunk_kernel(Args a)
         const int row = tid / TPR, cc = CPT * (tid % TPR);
         const float be = gate(rbe, row);
         float db = 0.f;
-        const int64_t st = (slot * a.Hv + hv) * (int64_t)(DK * DV / 4);      // in bf16x8: two parts
-        const bf16x8 *Sc = reinterpret_cast<const bf16x8 *>(a.Sc) + st + wave * VS * WAVE + lane;
-        const bf16x8 *Lc = reinterpret_cast<const bf16x8 *>(a.Lc) + st + wave * VS * WAVE + lane;
-        constexpr int PART = (DK / 16) * VS * WAVE;
+        const int64_t st = (slot * a.Hv + hv) * (int64_t)(DK * DV / 4) + wave * VS * 2 * WAVE + lane;     // in f32x4
+        const f32x4 *Sc = reinterpret_cast<const f32x4 *>(a.Sc) + st, *Lc = reinterpret_cast<const f32x4 *>(a.Lc) + st;
 #pragma unroll 1
         for (int v0 = 0; v0 < DV; v0 += SW) {
             const Rows<bf16> O(a.dO, nullptr, tok, nt, a.Hv, DV);
@@ -206,59 +214,46 @@ void gdr_grad_chunk_kernel(Args a)
                 const int at = Swz<SW>::at(row, cc + 8 * i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) db += r[2 * i][j] * u[2 * i][j] + r[2 * i + 1][j] * u[2 * i + 1][j];
-                bf16x8 hi, lo;
                 *reinterpret_cast<bf16x8 *>(&s.rows[0][at]) = Rows<bf16>::bf(o[i]);
-                split8(be * r[2 * i], be * r[2 * i + 1], hi, lo);
-                *reinterpret_cast<bf16x8 *>(&s.rows[1][at]) = hi;
-                *reinterpret_cast<bf16x8 *>(&s.rows[2][at]) = lo;
-                split8(be * u[2 * i], be * u[2 * i + 1], hi, lo);
-                *reinterpret_cast<bf16x8 *>(&s.rows[3][at]) = hi;
-                *reinterpret_cast<bf16x8 *>(&s.rows[4][at]) = lo;
+                const Parts<3> U = split8(be * r[2 * i], be * r[2 * i + 1]), Y = split8(be * u[2 * i], be * u[2 * i + 1]);
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    *reinterpret_cast<bf16x8 *>(&s.rows[1 + j][at]) = U.p[j];
+                    *reinterpret_cast<bf16x8 *>(&s.rows[4 + j][at]) = Y.p[j];
+                }
             }
             __syncthreads();
 #pragma unroll 1
             for (int ks = 0; ks < SW / 32; ++ks) {
-                const int vc = 32 * ks + 8 * lg, t0 = (v0 / 32 + ks) * WAVE;
-                const bf16x8 sh = __builtin_nontemporal_load(Sc + t0), sl = __builtin_nontemporal_load(Sc + t0 + PART);
-                const bf16x8 lh = __builtin_nontemporal_load(Lc + t0), ll = __builtin_nontemporal_load(Lc + t0 + PART);
+                const int vc = 32 * ks + 8 * lg, t0 = (v0 / 32 + ks) * 2 * WAVE;
+                const auto rows3 = [&](int first, int row) {
+                    const int at = Swz<SW>::at(row, vc);
+                    return Parts<3>{{lds8(&s.rows[first][at]), lds8(&s.rows[first + 1][at]), lds8(&s.rows[first + 2][at])}};
+                };
+                const Parts<3> S = split8(__builtin_nontemporal_load(Sc + t0), __builtin_nontemporal_load(Sc + t0 + WAVE));
+                const Parts<3> L = split8(__builtin_nontemporal_load(Lc + t0), __builtin_nontemporal_load(Lc + t0 + WAVE));
 #pragma unroll
                 for (int i = 0; i < NKD; ++i) {
                     const int own = 16 * block_of(i) + ln;
                     if (kind_of(i) == 0) {
                         const bf16x8 x = row8<SW>(s.rows[0], own, vc);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            mat[i][b] = mma(row8<SW>(s.rows[2], 16 * b + ln, vc), x, mat[i][b]);
-                            mat[i][b] = mma(row8<SW>(s.rows[1], 16 * b + ln, vc), x, mat[i][b]);
-                        }
+                        for (int b = 0; b < 4; ++b) mat[i][b] = mma_by_parts<3>(rows3(1, 16 * b + ln), x, mat[i][b]);
                     } else {
-                        const bf16x8 xh = row8<SW>(s.rows[3], own, vc), xl = row8<SW>(s.rows[4], own, vc);
+                        const Parts<3> x = rows3(4, own);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const bf16x8 uh = row8<SW>(s.rows[1], 16 * b + ln, vc);
-                            mat[i][b] = mma(row8<SW>(s.rows[2], 16 * b + ln, vc), xh, mat[i][b]);
-                            mat[i][b] = mma(uh, xl, mat[i][b]);
-                            mat[i][b] = mma(uh, xh, mat[i][b]);
-                        }
+                        for (int b = 0; b < 4; ++b) mat[i][b] = mma33(rows3(1, 16 * b + ln), x, mat[i][b]);
                     }
                 }
-                // the diagonal of S L^T
-                ls = mma(sl, lh, ls);
-                ls = mma(sh, ll, ls);
-                ls = mma(sh, lh, ls);
+                ls = mma33(S, L, ls);            // its diagonal is wanted
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const int at = Swz<SW>::at(16 * t + ln, vc);
-                    const bf16x8 ot = lds8(&s.rows[0][at]), uh = lds8(&s.rows[1][at]), ul = lds8(&s.rows[2][at]);
-                    const bf16x8 yh = lds8(&s.rows[3][at]), yl = lds8(&s.rows[4][at]);
-                    x1[t] = mma(sl, ot, x1[t]);
-                    x2[t] = mma(sl, yh, x2[t]);
-                    x3[t] = mma(ll, uh, x3[t]);
-                    x2[t] = mma(sh, yl, x2[t]);
-                    x3[t] = mma(lh, ul, x3[t]);
-                    x1[t] = mma(sh, ot, x1[t]);
-                    x2[t] = mma(sh, yh, x2[t]);
-                    x3[t] = mma(lh, uh, x3[t]);
+                    x1[t] = mma_by_parts<3>(S, row8<SW>(s.rows[0], 16 * t + ln, vc), x1[t]);
+                    x2[t] = mma33(S, rows3(4, 16 * t + ln), x2[t]);
+                    x3[t] = mma33(L, rows3(1, 16 * t + ln), x3[t]);
+                    // keeps the reads of all blocks from being hoisted into registers at once
+                    if (t == 1) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
