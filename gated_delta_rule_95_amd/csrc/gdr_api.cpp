@@ -318,6 +318,17 @@ kda_status check8(const void *q, const void *k, const void *v, const uint8_t *q8
     return check_bufs(bufs, 9);
 }
 
+gdr::Kept8 kept8(const void *q, const void *k, const void *v, const uint8_t *q8, const uint8_t *qe,
+                 const uint8_t *k8, const uint8_t *ke, const uint8_t *v8, const uint8_t *ve,
+                 int64_t n_tokens, int32_t Hk, int32_t Hv, int32_t dk, int32_t dv)
+{
+    const auto mut = [](const uint8_t *p) { return const_cast<uint8_t *>(p); };     // read only when loading
+    const int64_t rk = n_tokens * Hk * dk / 8, rv = n_tokens * Hv * dv / 8;
+    const int lk = dk < 32 ? dk / 8 : 4, lv = dv < 32 ? dv / 8 : 4;
+    return gdr::Kept8{{q, k, v}, {mut(q8), mut(k8), mut(v8)}, {mut(qe), mut(ke), mut(ve)},
+                      {rk, rk, rv}, {lk, lk, lv}, {}};
+}
+
 }  // namespace
 
 GDR_API kda_status gdr_save8(const void *q, const void *k, const void *v, int64_t n_tokens,
@@ -327,11 +338,8 @@ GDR_API kda_status gdr_save8(const void *q, const void *k, const void *v, int64_
 {
     kda_status s = check8(q, k, v, q8, qe, k8, ke, v8, ve, n_tokens, H_k, H_v, d_k, d_v, true);
     if (s != KDA_OK || n_tokens == 0) return s;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = gdr::launch_save8(q, n_tokens * H_k, d_k, q8, qe, st);
-    if (e == hipSuccess) e = gdr::launch_save8(k, n_tokens * H_k, d_k, k8, ke, st);
-    if (e == hipSuccess) e = gdr::launch_save8(v, n_tokens * H_v, d_v, v8, ve, st);
-    return hip_status(e, "gdr_save8 launch");
+    return hip_status(gdr::launch_save8(kept8(q, k, v, q8, qe, k8, ke, v8, ve, n_tokens, H_k, H_v, d_k, d_v),
+                                        static_cast<hipStream_t>(stream)), "gdr_save8 launch");
 }
 
 GDR_API kda_status gdr_load8(const uint8_t *q8, const uint8_t *qe, const uint8_t *k8,
@@ -341,9 +349,6 @@ GDR_API kda_status gdr_load8(const uint8_t *q8, const uint8_t *qe, const uint8_t
 {
     kda_status s = check8(q, k, v, q8, qe, k8, ke, v8, ve, n_tokens, H_k, H_v, d_k, d_v, false);
     if (s != KDA_OK || n_tokens == 0) return s;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = gdr::launch_load8(q8, qe, n_tokens * H_k, d_k, q, st);
-    if (e == hipSuccess) e = gdr::launch_load8(k8, ke, n_tokens * H_k, d_k, k, st);
-    if (e == hipSuccess) e = gdr::launch_load8(v8, ve, n_tokens * H_v, d_v, v, st);
-    return hip_status(e, "gdr_load8 launch");
+    return hip_status(gdr::launch_load8(kept8(q, k, v, q8, qe, k8, ke, v8, ve, n_tokens, H_k, H_v, d_k, d_v),
+                                        static_cast<hipStream_t>(stream)), "gdr_load8 launch");
 }

@@ -87,6 +87,17 @@ __device__ __forceinline__ double last_lane(double x)
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// Cuts what follows loose from the lane indices before it: addresses and masks
+// made of them are then formed where they are used, and not kept in registers
+// across the chunks.  With twelve waves (168 registers each) 2 registers are
+// spilled in place of 213; with eight there is room, and forming them again
+// would cost 9%.
+template <bool ON>
+__device__ __forceinline__ void loosen(int &ln, int &lg)
+{
+    if constexpr (ON) asm volatile("" : "+v"(ln), "+v"(lg));
+}
+
 // Producer W of four.  Its tiles pair the lane tokens of block W (K K^T) and
 // of block 3 - W (K Q^T) with the row tokens of the blocks b before and at
 // them (forward) or at and behind them (sweep).
@@ -155,7 +166,7 @@ struct Producer {
     __device__ __forceinline__ void build(St &st, float (*gp)[C], const Eye &eye, float scale,
                                           int ln, int lg, int ptid, F next)
     {
-        const int lane = ln + 16 * lg;
+        int lane = ln + 16 * lg;
         // cumulative log2-decay in double, held as two floats
         const double G = scan64((double)floor_g(g) * (double)LOG2E), Gend = last_lane(G);
         const float gh = (float)G;
@@ -190,6 +201,7 @@ struct Producer {
         __syncthreads();                 // rows of the chunk are in the stage
         next();
         // tile products
+        loosen<NC == 8>(ln, lg);
         f32x4 kk[4] = {}, kq[4] = {};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -205,6 +217,8 @@ struct Producer {
                 if (kq_tile(b)) kq[b] = mma(SW ? lds8(&st.Q[Swz<DK>::at(16 * b + ln, c)]) : bf, xf, kq[b]);
             }
         }
+        loosen<NC == 8>(ln, lg);
+        lane = ln + 16 * lg;
         // tiles: lane token x, row tokens y = 16 b + 4 lg + e; x is the later
         // one in the forward, the earlier one in the sweep
         const int xk = 16 * W + ln, xq = 16 * X + ln;
@@ -290,7 +304,7 @@ struct Producer {
     static __device__ __forceinline__ void run(const Args &a, Smem<DK, NC, MODE> &sm, int chunks, Tok where, int hk, int hv,
                                                int col, int lane, int ptid)
     {
-        const int ln = lane % 16, lg = lane / 16;
+        int ln = lane % 16, lg = lane / 16;
         const Eye eye = make_eye(lane);
         Producer p;
         const auto request = [&](int c) {
@@ -303,6 +317,7 @@ struct Producer {
         };
         request(0);
         for (int c = 0; c < chunks; ++c) {
+            loosen<NC == 8>(ln, lg);
             p.build(sm.st[c & 1], sm.G[W], eye, a.scale, ln, lg, ptid, [&] { request(c + 1); });
             __syncthreads();
         }
@@ -345,7 +360,9 @@ __device__ __forceinline__ f32x4 mul_pair(const PairRegs &t, const Parts<3> &b, 
 template <typename TI, int DK, int NC, int MODE>
 struct Consumer {
     static constexpr int RT = DK / 16, KS = DK / 32;
-    using TO = bf16;
+    // eight consumers: a third of the registers, and another consumer on the
+    // same SIMD to run while one waits
+    static constexpr bool LEAN = NC == 8;
     f32x4 S[RT];
 
     // K^T or Q^T operand: channels of row tile ct against tokens 32 s ..
@@ -403,6 +420,9 @@ struct Consumer {
         // Operands are requested a phase ahead: the phases are dependent
         // chains of one wave, and the LDS latency would stand in each of
         // their steps (scheduling barriers keep the requests where they are).
+        const auto pin = [] {
+            if constexpr (!LEAN) __builtin_amdgcn_sched_barrier(0);
+        };
         u32x2 vt[4];
         f32x4 eg[4];
 #pragma unroll
@@ -411,7 +431,7 @@ struct Consumer {
             eg[t] = ld4f(&st.eG[16 * t + 4 * lg]);
         }
         const BlockRegs T0(st.T[0], lane), A10(st.Aone[0], lane), T1(st.T[1], lane);
-        __builtin_amdgcn_sched_barrier(0);
+        pin();
         f32x4 X[4] = {}, O[4] = {}, R[4];
         Parts<2> p[KS];
 #pragma unroll
@@ -424,12 +444,16 @@ struct Consumer {
                 p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
 #pragma unroll
             for (int t = 0; t < 4; ++t) X[t] = mma_parts<2>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p[s], X[t]);
+            if constexpr (MODE == FWD && LEAN) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) O[t] = mma_by_parts(p[s], lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
+            }
             if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }
         const PairRegs A2(st.Apair[0], lane), A3(st.Apair[1], lane);
         const float gam = st.gamma;
         const f32x4 er0 = ld4f(&st.eR[4 * lg]), er1 = ld4f(&st.eR[16 + 4 * lg]);
-        __builtin_amdgcn_sched_barrier(0);
+        pin();
 #pragma unroll
         for (int t = 0; t < 4; ++t) R[t] = widen(vt[t]) - eg[t] * X[t];
         // The substitution is one long dependent chain: products that do not
@@ -437,7 +461,7 @@ struct Consumer {
         // operands of a product trade places), so that a lane holds four
         // columns of one token and o goes out 8 bytes at a time.
         const auto qs = [&](int s) {
-            if (MODE == FWD && s < KS)
+            if (MODE == FWD && s < KS && !LEAN)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     O[t] = mma_by_parts(p[s], lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
@@ -455,7 +479,7 @@ struct Consumer {
         R[1] = mul_block(T1, x, zero);
         const BlockRegs T2(st.T[2], lane), A32(st.Aone[1], lane), T3(st.T[3], lane);
         const f32x4 er2 = ld4f(&st.eR[32 + 4 * lg]), er3 = ld4f(&st.eR[48 + 4 * lg]);
-        __builtin_amdgcn_sched_barrier(0);
+        pin();
 #pragma unroll
         for (int t = 0; t < RT; ++t) S[t] *= gam;
 #pragma unroll
@@ -613,8 +637,12 @@ __device__ __forceinline__ void store_state(const f32x4 *S, float *p, int dv, in
 
 // Workgroups of one key head (its value heads' column blocks) share q and k:
 // unit u of them runs on XCD u % 8 (workgroups go round the XCDs in order), so
-// that the second and later reads hit that XCD's L2.
-__device__ __forceinline__ bool my_chain(const Args &a, int per_unit, int &n, int &hk, int &j)
+// that the second and later reads hit that XCD's L2.  Units are dealt out with
+// the longest sequences first (up to 128 of them): a long chain that starts
+// last would run alone at the end.
+constexpr int kSorted = 128;
+__device__ __forceinline__ bool my_chain(const Args &a, int per_unit, int *lens, int tid, int nthreads, int &n, int &hk,
+                                         int &j)
 {
     const int64_t b = blockIdx.x, slot = b / 8;
     const int64_t u = (slot / per_unit) * 8 + b % 8;
@@ -622,6 +650,20 @@ __device__ __forceinline__ bool my_chain(const Args &a, int per_unit, int &n, in
     if (u >= (int64_t)a.seq.n_seqs * a.Hk) return false;
     n = (int)(u / a.Hk);
     hk = (int)(u % a.Hk);
+    const int ns = a.seq.n_seqs;
+    if (a.seq.cu_seqlens && ns > 1 && ns <= kSorted) {
+        for (int i = tid; i < ns; i += nthreads) lens[i] = seq_of(a.seq, i).len;
+        __syncthreads();
+        if (tid < ns) {
+            const int mine = lens[tid];
+            int rank = 0;
+            for (int i = 0; i < ns; ++i) rank += lens[i] > mine || (lens[i] == mine && i < tid);
+            if (rank == n) lens[kSorted] = tid;
+        }
+        __syncthreads();
+        n = __builtin_amdgcn_readfirstlane(lens[kSorted]);
+        __syncthreads();                         // before the place is used for something else
+    }
     return true;
 }
 
@@ -633,9 +675,10 @@ void gdr_chunk_kernel(Args a)
     constexpr int BV = 16 * NC;
     const int CB = a.dv / BV, grp = a.Hv / a.Hk;
     int n, hk, j;
-    if (!my_chain(a, grp * CB, n, hk, j)) return;
+    const int tid = threadIdx.x;
+    if (!my_chain(a, grp * CB, reinterpret_cast<int *>(sm.G), tid, (NC + 4) * WAVE, n, hk, j)) return;
     const int hv = hk * grp + j / CB, col = (j % CB) * BV;
-    const int tid = threadIdx.x, lane = tid % WAVE, ln = lane % 16, lg = lane / 16;
+    const int lane = tid % WAVE, ln = lane % 16, lg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const Seq sq = seq_of(a.seq, n);
     const int bos = __builtin_amdgcn_readfirstlane(sq.bos), len = __builtin_amdgcn_readfirstlane(sq.len);
@@ -707,8 +750,17 @@ hipError_t launch_t(const Args &a)
 
 }  // namespace
 
+// Eight consumers (one workgroup a chain of 128 columns) or four (two): with
+// both halves of every chain running at once, four are faster (281 against
+// 367 us, 128 chains of 64 chunks on 256 compute units); with more chains than
+// half the compute units the halves would queue, and eight do the work of two
+// workgroups in 1.3 times the time of one.
+constexpr int64_t kWide = 129;
+
 hipError_t launch_chunk_fwd(const Args &a)
 {
+    if (a.dv == 128 && (int64_t)a.seq.n_seqs * a.Hv >= kWide)
+        return a.dk == 128 ? launch_t<bf16, 128, 8, FWD>(a) : launch_t<bf16, 64, 8, FWD>(a);
     return a.dk == 128 ? launch_t<bf16, 128, 4, FWD>(a) : launch_t<bf16, 64, 4, FWD>(a);
 }
 

@@ -71,8 +71,16 @@ hipError_t launch_chunk_fwd(const Args &a);
 hipError_t launch_chunk_keep_sweep(const Args &a);
 hipError_t launch_chunk_grad(const Args &a);
 hipError_t launch_decode(const DecodeArgs &a);
-hipError_t launch_save8(const void *x, int64_t rows, int d, uint8_t *x8, uint8_t *xe, hipStream_t s);
-hipError_t launch_load8(const uint8_t *x8, const uint8_t *xe, int64_t rows, int d, void *x,
-                        hipStream_t s);
+
+// q, k, v (bf16) and their 8-bit form
+struct Kept8 {
+    const void *x[3];
+    uint8_t *x8[3], *xe[3];
+    int64_t n8[3];                       // groups of eight elements
+    int lanes[3];                        // groups a block
+    int first[4];                        // first workgroups (filled in at launch)
+};
+hipError_t launch_save8(Kept8 a, hipStream_t s);
+hipError_t launch_load8(Kept8 a, hipStream_t s);
 
 }  // namespace gdr

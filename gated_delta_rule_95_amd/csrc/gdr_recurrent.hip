@@ -121,7 +121,8 @@ void gdr_recurrent_kernel(Args a, int C)
                     for (int e = 0; e < 4; ++e)
                         a.Lc[cst + (int64_t)(16 * m + 4 * r + e) * DV] = S[m][e];
             }
-            float pk = 0.f, pq = 0.f;
+            // four partial sums each: one would be a chain of d_k / 4 dependent adds
+            f32x4 pk4 = {0.f, 0.f, 0.f, 0.f}, pq4 = pk4;
 #pragma unroll
             for (int m = 0; m < RT; ++m) {
                 const f32x4 kk = *reinterpret_cast<const f32x4 *>(&s_k[t][16 * m + 4 * r]);
@@ -130,11 +131,11 @@ void gdr_recurrent_kernel(Args a, int C)
                 for (int e = 0; e < 4; ++e) {
                     if (MODE == SWEEP) S[m][e] += (a.scale * x) * qq[e];
                     else S[m][e] *= al;
-                    pk += S[m][e] * kk[e];
-                    if (MODE == FWD) pq += S[m][e] * qq[e];
+                    pk4[e] += S[m][e] * kk[e];
+                    if (MODE == FWD) pq4[e] += S[m][e] * qq[e];
                 }
             }
-            pk = sum_groups(pk);
+            const float pk = sum_groups((pk4[0] + pk4[1]) + (pk4[2] + pk4[3]));
             float u;
             if (MODE == SWEEP) {
                 u = -be * pk;
@@ -148,7 +149,7 @@ void gdr_recurrent_kernel(Args a, int C)
                 if (MODE == KEEP && r == 0) a.R[row * DV + col] = res;
             }
             if (MODE == FWD) {
-                pq = sum_groups(pq);
+                const float pq = sum_groups((pq4[0] + pq4[1]) + (pq4[2] + pq4[3]));
                 if (r == 0)
                     kda::Elem<TO>::st((TO *)a.o + row * DV + col, a.scale * (pq + u * s_kq[t]));
             }

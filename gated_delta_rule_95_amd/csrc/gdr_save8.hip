@@ -15,14 +15,22 @@
 namespace gdr {
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 __global__ __launch_bounds__(256)
-void gdr_save8_kernel(const uint32_t *__restrict__ x, int64_t n8, int lanes,
-                      uint32_t *__restrict__ x8, uint8_t *__restrict__ xe)
+void gdr_save8_kernel(Kept8 a)
 {
+    // q, k and v in one launch: a workgroup's part is that of its index
+    const int t = blockIdx.x < a.first[1] ? 0 : blockIdx.x < a.first[2] ? 1 : 2;
+    const u32x4 *__restrict__ x = static_cast<const u32x4 *>(a.x[t]);
+    const int64_t n8 = a.n8[t], stride = (a.first[t + 1] - a.first[t]) * 256ll;
+    const int lanes = a.lanes[t];
+    u32x2 *__restrict__ x8 = reinterpret_cast<u32x2 *>(a.x8[t]);
+    uint8_t *__restrict__ xe = a.xe[t];
     // every lane of a block is in or out together: blocks do not straddle n8
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n8; i += gridDim.x * 256ll) {
-        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x) + i);
+    for (int64_t i = (blockIdx.x - a.first[t]) * 256ll + threadIdx.x; i < n8; i += stride) {
+        const u32x4 w = __builtin_nontemporal_load(x + i);
         float f[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -52,26 +60,28 @@ void gdr_save8_kernel(const uint32_t *__restrict__ x, int64_t n8, int lanes,
             const bool fin = (__float_as_uint(f[j]) & 0x7fffffffu) < 0x7f800000u;
             y[j] = fin ? fminf(fmaxf(z, -448.f), 448.f) : __uint_as_float(0x7fc00000u);
         }
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         u32x2 b;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j], y[4 * j + 1], 0, false);
             b[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j + 2], y[4 * j + 3], p, true);
         }
-        reinterpret_cast<u32x2 *>(x8)[i] = b;
+        x8[i] = b;
         if (threadIdx.x % lanes == 0) xe[i / lanes] = (uint8_t)e;
     }
 }
 
 __global__ __launch_bounds__(256)
-void gdr_load8_kernel(const uint32_t *__restrict__ x8, const uint8_t *__restrict__ xe, int64_t n8,
-                      int lanes, uint32_t *__restrict__ x)
+void gdr_load8_kernel(Kept8 a)
 {
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n8; i += gridDim.x * 256ll) {
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-        const u32x2 b = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(x8) + i);
+    const int t = blockIdx.x < a.first[1] ? 0 : blockIdx.x < a.first[2] ? 1 : 2;
+    u32x4 *__restrict__ x = static_cast<u32x4 *>(const_cast<void *>(a.x[t]));
+    const int64_t n8 = a.n8[t], stride = (a.first[t + 1] - a.first[t]) * 256ll;
+    const int lanes = a.lanes[t];
+    const u32x2 *__restrict__ x8 = reinterpret_cast<const u32x2 *>(a.x8[t]);
+    const uint8_t *__restrict__ xe = a.xe[t];
+    for (int64_t i = (blockIdx.x - a.first[t]) * 256ll + threadIdx.x; i < n8; i += stride) {
+        const u32x2 b = __builtin_nontemporal_load(x8 + i);
         const float f = __uint_as_float((uint32_t)xe[i / lanes] << 23);
         u32x4 w;
 #pragma unroll
@@ -83,36 +93,38 @@ void gdr_load8_kernel(const uint32_t *__restrict__ x8, const uint8_t *__restrict
             w[2 * j] = (__float_as_uint(p0) >> 16) | (__float_as_uint(p1) & 0xffff0000u);
             w[2 * j + 1] = (__float_as_uint(r0) >> 16) | (__float_as_uint(r1) & 0xffff0000u);
         }
-        __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(x) + i);
+        __builtin_nontemporal_store(w, x + i);
     }
 }
 
-unsigned grid_for(int64_t n8)
+// fills in the workgroups' ranges; the number of them, or 0
+int plan(Kept8 &a)
 {
-    const int64_t b = (n8 + 255) / 256;
-    return (unsigned)(b < 8192 ? b : 8192);
+    int at = 0;
+    for (int t = 0; t < 3; ++t) {
+        a.first[t] = at;
+        const int64_t b = (a.n8[t] + 255) / 256;
+        at += (int)(b < 65536 ? b : 65536);
+    }
+    a.first[3] = at;
+    return at;
 }
 
 }  // namespace
 
-hipError_t launch_save8(const void *x, int64_t rows, int d, uint8_t *x8, uint8_t *xe, hipStream_t s)
+hipError_t launch_save8(Kept8 a, hipStream_t s)
 {
-    const int64_t n8 = rows * d / 8;
-    if (n8 == 0) return hipSuccess;
-    hipLaunchKernelGGL(gdr_save8_kernel, dim3(grid_for(n8)), dim3(256), 0, s,
-                       static_cast<const uint32_t *>(x), n8, d < 32 ? d / 8 : 4,
-                       reinterpret_cast<uint32_t *>(x8), xe);
+    const int blocks = plan(a);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(gdr_save8_kernel, dim3(blocks), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
-hipError_t launch_load8(const uint8_t *x8, const uint8_t *xe, int64_t rows, int d, void *x,
-                        hipStream_t s)
+hipError_t launch_load8(Kept8 a, hipStream_t s)
 {
-    const int64_t n8 = rows * d / 8;
-    if (n8 == 0) return hipSuccess;
-    hipLaunchKernelGGL(gdr_load8_kernel, dim3(grid_for(n8)), dim3(256), 0, s,
-                       reinterpret_cast<const uint32_t *>(x8), xe, n8, d < 32 ? d / 8 : 4,
-                       static_cast<uint32_t *>(x));
+    const int blocks = plan(a);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(gdr_load8_kernel, dim3(blocks), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
