@@ -14,7 +14,7 @@ namespace gdr {
 // everything else token by token in fp32.
 static bool chunked(int dk, int dv, bool bf16) { return bf16 && dk >= 64 && dv >= 64; }
 
-int bwd_chunk(int dk, int dv, bool bf16) { return chunked(dk, dv, bf16) ? 64 : 32; }
+int bwd_chunk(int dk, int dv, bool bf16) { return chunked(dk, dv, bf16) ? 64 : kRecurrentChunk; }
 
 static hipError_t launch_fwd(const Args &a)
 {
@@ -29,9 +29,8 @@ static hipError_t launch_bwd(const Args &a)
         if ((e = launch_chunk_keep_sweep(a)) != hipSuccess || a.seq.n_tokens == 0) return e;
         return launch_chunk_grad(a);
     }
-    const int C = bwd_chunk(a.dk, a.dv, bf16);
-    if ((e = launch_recurrent_keep(a, C)) != hipSuccess) return e;
-    if ((e = launch_recurrent_sweep(a, C)) != hipSuccess || a.seq.n_tokens == 0) return e;
+    if ((e = launch_recurrent_keep(a)) != hipSuccess) return e;
+    if ((e = launch_recurrent_sweep(a)) != hipSuccess || a.seq.n_tokens == 0) return e;
     return launch_grad32(a);
 }
 

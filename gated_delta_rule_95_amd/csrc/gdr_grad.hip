@@ -40,7 +40,8 @@ __device__ __forceinline__ bool find_chunk(const SeqArgs &s, int64_t slot, int C
 // fp32 on the fp32 matrix cores (16x16x4): lane (n, g) = (lane % 16, lane / 16)
 // takes contraction index 4 g + i at step i, so both operands of a product
 // of row-major tiles are 16-byte reads of a row.
-constexpr int C32 = 32;
+constexpr int C32 = kRecurrentChunk;
+static_assert(C32 == 32, "the lane layouts below");
 
 template <typename TI, int DK, int DV>
 struct alignas(16) GradSmem {
@@ -100,12 +101,14 @@ void gdr_grad_kernel(Args a)
             *reinterpret_cast<f32x4 *>(&s.U[t][x]) = u;
             *reinterpret_cast<f32x4 *>(&s.Yb[t][x]) = y;
         }
-        if (tid == 0) {
-            double x = 0.0;
-            for (int t = 0; t < C; ++t) {
-                if (t < nt) x += (double)floor_g(a.g[(int64_t)(tok + t) * a.Hv + hv]);
-                s.G[t] = x;
+        if (tid < C) {
+            double x = tid < nt ? (double)floor_g(a.g[(int64_t)(tok + tid) * a.Hv + hv]) : 0.0;
+#pragma unroll
+            for (int m = 1; m < C; m *= 2) {
+                const double y = __shfl_up(x, m);
+                if (tid >= m) x += y;
             }
+            s.G[tid] = x;
         }
         __syncthreads();
         if (tid < C) {
@@ -238,13 +241,23 @@ void gdr_grad_kernel(Args a)
         for (int m = 1; m < 64; m *= 2) ls += __shfl_xor(ls, m);
         if (lane == 0) s.ls[wave] = ls;
         __syncthreads();
-        if (tid < nt) {
-            float x = kda::fast_exp2((float)(s.G[C - 1] * LOG2E)) * (s.ls[0] + s.ls[1] + s.ls[2] + s.ls[3]);
-            for (int i = 0; i < C; ++i)
-                for (int w = 0; w < 4; ++w) x += i >= tid ? s.a[w][i] : s.b[w][i];
-            for (int i = tid; i < C; ++i)
-                for (int j = 0; j < tid; ++j) x += s.qk[i][j];
-            a.dg[(int64_t)(tok + tid) * a.Hv + hv] = x;
+        {
+            // eight threads a token, each every eighth row
+            const int t = tid / 8;
+            float x = 0.f;
+#pragma unroll
+            for (int i0 = 0; i0 < C; i0 += 8) {
+                const int i = i0 + tid % 8;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) x += i >= t ? s.a[w][i] : s.b[w][i];
+                if (i >= t)
+                    for (int j = 0; j < t; ++j) x += s.qk[i][j];
+            }
+#pragma unroll
+            for (int m = 1; m < 8; m *= 2) x += __shfl_xor(x, m);
+            if (tid % 8 == 0 && t < nt)
+                a.dg[(int64_t)(tok + t) * a.Hv + hv] =
+                    x + kda::fast_exp2((float)(s.G[C - 1] * LOG2E)) * (s.ls[0] + s.ls[1] + s.ls[2] + s.ls[3]);
         }
     }
 #pragma unroll

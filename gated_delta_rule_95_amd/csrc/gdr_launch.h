@@ -53,7 +53,9 @@ struct DecodeArgs {
     hipStream_t stream;
 };
 
-// tokens between two kept states of the backward
+// tokens between two kept states of the backward, token by token
+constexpr int kRecurrentChunk = 32;
+// ... and in either form
 int bwd_chunk(int dk, int dv, bool bf16);
 // chunk slots cu_seqlens[n] / C + n + c of a batch: an upper bound on every slot + 1
 inline int64_t bwd_slots(int32_t n_seqs, int64_t n_tokens, int C)
@@ -64,8 +66,8 @@ inline int64_t bwd_slots(int32_t n_seqs, int64_t n_tokens, int C)
 // the kernels behind launch_fwd and launch_bwd (gdr_api.cpp), by form: token
 // by token in fp32, or chunks of 64 on the matrix cores
 hipError_t launch_recurrent_fwd(const Args &a);
-hipError_t launch_recurrent_keep(const Args &a, int C);
-hipError_t launch_recurrent_sweep(const Args &a, int C);
+hipError_t launch_recurrent_keep(const Args &a);
+hipError_t launch_recurrent_sweep(const Args &a);
 hipError_t launch_grad32(const Args &a);
 hipError_t launch_chunk_fwd(const Args &a);
 hipError_t launch_chunk_keep_sweep(const Args &a);

@@ -2,11 +2,17 @@
 // keeps states for the backward, and the reverse sweep.  Right for every
 // type and head size.
 //
-// Columns of the state evolve independently, so a wave owns 16 columns and
-// all rows of S in registers: lane (c, r) = (lane % 16, lane / 16) holds rows
-// 16 t + 4 r + e of column c.  Per token the two column sums S'^T k and
-// S'^T q are taken together (o = S'^T q + u (k . q)), each over a lane's own
-// rows and then over the four row groups by two register swaps.
+// Columns of the state evolve independently, so a wave owns GC columns and
+// all rows of S in registers: lane (c, r) = (lane % GC, lane / GC) holds rows
+// 4 (NG m + r) + e of column c, NG = 64 / GC.  Per token the two column sums
+// S'^T k and S'^T q are taken together (o = S'^T q + u (k . q)), each over a
+// lane's own rows and then over the row groups by moves between lanes.
+//
+// Bound by the chain of tokens: a token is some 4 d_k / NG vector operations, a
+// sum over lanes and their latencies, so with few chains a wave takes fewer
+// columns and more lanes share one (GC 4 in place of 16).  A token's operands
+// are read from the LDS one token ahead and a tile's from memory one tile
+// ahead.
 #include "gdr_device.h"
 
 namespace gdr {
@@ -16,12 +22,31 @@ constexpr int TT = 16;               // tokens staged at a time
 
 enum { FWD = 0, KEEP = 1, SWEEP = 2 };
 
-template <typename TI, int DK, int DV>
+constexpr int64_t kFew = 8192, kSome = 32768;
+
+template <int DK, int DV, int GC>
 struct Shape {
-    static constexpr int NW = DV / 16 < 4 ? DV / 16 : 4;
+    static constexpr int NG = WAVE / GC;
+    static constexpr int NW = DV / GC < 4 ? DV / GC : 4;
     static constexpr int NT = NW * WAVE;
-    static constexpr int BV = 16 * NW;
+    static constexpr int BV = GC * NW;
+    static constexpr int RM = DK / (4 * NG);     // four-row pieces a lane
+    static_assert(RM >= 1, "row groups");
 };
+
+// sum over the lanes of equal lane % GC
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x)
+{
+    return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+template <int GC>
+__device__ __forceinline__ float sum_rows(float x)
+{
+    if constexpr (GC <= 4) x = dpp_add<0x124>(x);        // row_ror 4
+    if constexpr (GC <= 8) x = dpp_add<0x128>(x);        // row_ror 8
+    return sum_groups(x);
+}
 
 // MODE FWD: writes o and S_T.  KEEP: the state before every token of index
 // 0, C, 2C, ... of its sequence to Sc[slot], and R_t = v_t - S'^T k_t.
@@ -29,172 +54,219 @@ struct Shape {
 //     L += scale q_t dO_t^T;  Ub_t = L^T k_t;  L = exp(g_t) (L - k_t (beta_t Ub_t)^T),
 // writing dv = beta Ub, Ub, L behind the last token of every chunk (Lc) and
 // dS0.
-template <typename TI, int DK, int DV, int MODE>
-__global__ __launch_bounds__((Shape<TI, DK, DV>::NT))
-void gdr_recurrent_kernel(Args a, int C)
+template <typename TI, int DK, int DV, int GC, int MODE>
+__global__ __launch_bounds__((Shape<DK, DV, GC>::NT))
+void gdr_recurrent_kernel(Args a)
 {
-    using Sh = Shape<TI, DK, DV>;
+    constexpr int C = kRecurrentChunk;
+    using Sh = Shape<DK, DV, GC>;
     using TO = typename OutOf<TI>::type;
-    constexpr int RT = DK / 16;      // row tiles: four rows of each per lane
-    constexpr int CB = DV / Sh::BV;
-    __shared__ __align__(16) float s_k[TT][DK], s_q[TT][DK], s_v[TT][Sh::BV];
-    __shared__ float s_a[TT], s_b[TT], s_kq[TT];
-    const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
-    const int c = lane % 16, r = lane / 16;
+    constexpr int RM = Sh::RM, NG = Sh::NG, NT = Sh::NT, BV = Sh::BV;
+    constexpr int CB = DV / BV;
+    struct Tile {
+        float k[TT][DK], q[TT][DK], v[TT][BV], a[TT], b[TT], kq[TT];
+    };
+    __shared__ __align__(16) Tile s_t[2];
+    const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int c = lane % GC, r = lane / GC;
     const int64_t chain = blockIdx.x / CB;
     const int cb = blockIdx.x % CB;
     const int n = (int)(chain / a.Hv), hv = (int)(chain % a.Hv), hk = hv / (a.Hv / a.Hk);
-    const Seq sq = seq_of(a.seq, n);
-    const int col = cb * Sh::BV + 16 * wave + c;
+    Seq sq = seq_of(a.seq, n);
+    sq.bos = __builtin_amdgcn_readfirstlane(sq.bos);      // addresses of rows are scalar arithmetic
+    sq.len = __builtin_amdgcn_readfirstlane(sq.len);
+    const int col = cb * BV + GC * wave + c;
     const auto Q = src<TI>(a.q, a.qe), K = src<TI>(a.k, a.ke), V = src<TI>(a.v, a.ve);
     const auto G = src<TO>(a.dO, nullptr);
     const int64_t st = (chain * DK) * DV + col;
     const float *init = MODE == SWEEP ? a.dS_T : a.S0;
-    f32x4 S[RT];
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    const auto row_of = [&](int m, int e) { return 4 * (NG * m + r) + e; };
+    f32x4 S[RM];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int m = 0; m < RM; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            S[t][e] = init ? init[st + (int64_t)(16 * t + 4 * r + e) * DV] : 0.f;
+        for (int e = 0; e < 4; ++e) S[m][e] = init ? init[st + (int64_t)row_of(m, e) * DV] : 0.f;
 
     const int tiles = (sq.len + TT - 1) / TT;
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int t0 = (MODE == SWEEP ? tiles - 1 - tile : tile) * TT;
-        const int nt = sq.len - t0 < TT ? sq.len - t0 : TT;
-        __syncthreads();
-        for (int i = tid; i < TT * DK / 4; i += Sh::NT) {
-            const int t = i / (DK / 4), ch = 4 * (i % (DK / 4));
-            f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qq = kk;
+    // a tile's rows: from memory to registers, from there to the LDS
+    constexpr int NK = (TT * DK / 4 + NT - 1) / NT, NV = (TT * BV / 4 + NT - 1) / NT;
+    f32x4 rk[NK], rq[NK], rv[NV];
+    float ra = 0.f, rb = 0.f;
+    const auto first = [&](int tile) { return (MODE == SWEEP ? tiles - 1 - tile : tile) * TT; };
+    const auto request = [&](int tile) {
+        const int t0 = first(tile), nt = sq.len - t0 < TT ? sq.len - t0 : TT;
+#pragma unroll
+        for (int x = 0; x < NK; ++x) {
+            const int i = tid + x * NT, t = i / (DK / 4), ch = 4 * (i % (DK / 4));
+            rk[x] = rq[x] = zero;
             if (t < nt) {
                 const int64_t row = (int64_t)(sq.bos + t0 + t) * a.Hk + hk;
-                kk = K.ld4(row, DK, ch);
-                if (MODE != KEEP) qq = Q.ld4(row, DK, ch);
+                rk[x] = K.ld4(row, DK, ch);
+                if (MODE != KEEP) rq[x] = Q.ld4(row, DK, ch);
             }
-            *reinterpret_cast<f32x4 *>(&s_k[t][ch]) = kk;
-            *reinterpret_cast<f32x4 *>(&s_q[t][ch]) = qq;
         }
-        for (int i = tid; i < TT * Sh::BV / 4; i += Sh::NT) {
-            const int t = i / (Sh::BV / 4), x = 4 * (i % (Sh::BV / 4));
-            f32x4 vv = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int i = tid + x * NT, t = i / (BV / 4), y = 4 * (i % (BV / 4));
+            rv[x] = zero;
             if (t < nt) {
                 const int64_t row = (int64_t)(sq.bos + t0 + t) * a.Hv + hv;
-                if constexpr (MODE == SWEEP) vv = G.ld4(row, DV, cb * Sh::BV + x);
-                else vv = V.ld4(row, DV, cb * Sh::BV + x);
+                if constexpr (MODE == SWEEP) rv[x] = G.ld4(row, DV, cb * BV + y);
+                else rv[x] = V.ld4(row, DV, cb * BV + y);
             }
-            *reinterpret_cast<f32x4 *>(&s_v[t][x]) = vv;
         }
         if (tid < TT) {
             const bool in = tid < nt;
             const int64_t row = (int64_t)(sq.bos + t0 + (in ? tid : 0)) * a.Hv + hv;
-            s_a[tid] = in ? kda::fast_exp2(floor_g(a.g[row]) * LOG2E) : 1.f;
-            s_b[tid] = in ? a.beta[row] : 0.f;
+            ra = in ? a.g[row] : 0.f;
+            rb = in ? a.beta[row] : 0.f;
         }
-        __syncthreads();
-        if (MODE == FWD) {           // k . q of every token: 16 lanes a token
-            for (int t = tid / 16; t < TT; t += Sh::NT / 16) {
-                float x = 0.f;
-                for (int i = tid % 16; i < DK; i += 16) x += s_k[t][i] * s_q[t][i];
+    };
+    if (tiles > 0) request(0);
+    for (int tile = 0; tile < tiles; ++tile) {
+        Tile &s = s_t[tile & 1];
+        const int t0 = first(tile), nt = sq.len - t0 < TT ? sq.len - t0 : TT;
 #pragma unroll
-                for (int m = 1; m < 16; m *= 2) x += __shfl_xor(x, m);
-                if (tid % 16 == 0) s_kq[t] = x;
+        for (int x = 0; x < NK; ++x) {
+            const int i = tid + x * NT, t = i / (DK / 4), ch = 4 * (i % (DK / 4));
+            if (NK * NT == TT * DK / 4 || t < TT) {
+                *reinterpret_cast<f32x4 *>(&s.k[t][ch]) = rk[x];
+                if (MODE != KEEP) *reinterpret_cast<f32x4 *>(&s.q[t][ch]) = rq[x];
             }
-            __syncthreads();
+            if (MODE == FWD) {       // k . q of every token: DK / 4 neighbouring lanes a token
+                float y = rk[x][0] * rq[x][0] + rk[x][1] * rq[x][1] + rk[x][2] * rq[x][2] + rk[x][3] * rq[x][3];
+#pragma unroll
+                for (int m = 1; m < DK / 4; m *= 2) y += __shfl_xor(y, m);
+                if (t < TT && ch == 0) s.kq[t] = y;
+            }
         }
-        for (int i = 0; i < nt; ++i) {
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int i = tid + x * NT, t = i / (BV / 4), y = 4 * (i % (BV / 4));
+            if (t < TT) *reinterpret_cast<f32x4 *>(&s.v[t][y]) = rv[x];
+        }
+        if (tid < TT) {
+            s.a[tid] = kda::fast_exp2(floor_g(ra) * LOG2E);
+            s.b[tid] = rb;
+        }
+        // the other half of the LDS was last read before the barrier of the
+        // tile before, so one barrier a tile is enough
+        __syncthreads();
+        if (tile + 1 < tiles) request(tile + 1);
+        struct Tok {
+            f32x4 k[RM], q[RM];
+            float al, be, x, kq;
+        };
+        const auto read = [&](int i) {
+            const int t = MODE == SWEEP ? nt - 1 - i : i;
+            Tok y;
+#pragma unroll
+            for (int m = 0; m < RM; ++m) {
+                y.k[m] = *reinterpret_cast<const f32x4 *>(&s.k[t][row_of(m, 0)]);
+                if (MODE != KEEP) y.q[m] = *reinterpret_cast<const f32x4 *>(&s.q[t][row_of(m, 0)]);
+            }
+            y.al = s.a[t];
+            y.be = s.b[t];
+            y.x = s.v[t][GC * wave + c];
+            y.kq = MODE == FWD ? s.kq[t] : 0.f;
+            return y;
+        };
+        const auto step = [&](const Tok &y, int i) {
             const int t = MODE == SWEEP ? nt - 1 - i : i;
             const int pos = t0 + t;
-            const int64_t row = (int64_t)(sq.bos + pos) * a.Hv + hv;
-            const float al = s_a[t], be = s_b[t], x = s_v[t][16 * wave + c];
-            const int64_t slot = sq.bos / C + n + pos / C;
-            const int64_t cst = ((slot * a.Hv + hv) * DK) * DV + col;
-            if (MODE == KEEP && pos % C == 0) {
+            const int64_t at = ((int64_t)(sq.bos + pos) * a.Hv + hv) * DV;
+            if (MODE == KEEP ? pos % C == 0 : MODE == SWEEP && (pos % C == C - 1 || pos == sq.len - 1)) {
+                const int64_t slot = sq.bos / C + n + pos / C;
+                float *dst = (MODE == KEEP ? a.Sc : a.Lc) + ((slot * a.Hv + hv) * DK) * DV + col;
 #pragma unroll
-                for (int m = 0; m < RT; ++m)
+                for (int m = 0; m < RM; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        a.Sc[cst + (int64_t)(16 * m + 4 * r + e) * DV] = S[m][e];
+                    for (int e = 0; e < 4; ++e) dst[(int64_t)row_of(m, e) * DV] = S[m][e];
             }
-            if (MODE == SWEEP && (pos % C == C - 1 || pos == sq.len - 1)) {
+            // four partial sums each: one would be a chain of dependent adds
+            f32x4 pk4 = zero, pq4 = zero;
 #pragma unroll
-                for (int m = 0; m < RT; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        a.Lc[cst + (int64_t)(16 * m + 4 * r + e) * DV] = S[m][e];
+            for (int m = 0; m < RM; ++m) {
+                if (MODE == SWEEP) S[m] += (a.scale * y.x) * y.q[m];
+                else S[m] *= y.al;
+                pk4 += S[m] * y.k[m];
+                if (MODE == FWD) pq4 += S[m] * y.q[m];
             }
-            // four partial sums each: one would be a chain of d_k / 4 dependent adds
-            f32x4 pk4 = {0.f, 0.f, 0.f, 0.f}, pq4 = pk4;
+            const float pk = sum_rows<GC>((pk4[0] + pk4[1]) + (pk4[2] + pk4[3]));
+            const float pq = MODE == FWD ? sum_rows<GC>((pq4[0] + pq4[1]) + (pq4[2] + pq4[3])) : 0.f;
+            const float res = MODE == SWEEP ? pk : y.x - pk;
+            const float u = MODE == SWEEP ? -y.be * pk : y.be * res;
 #pragma unroll
-            for (int m = 0; m < RT; ++m) {
-                const f32x4 kk = *reinterpret_cast<const f32x4 *>(&s_k[t][16 * m + 4 * r]);
-                const f32x4 qq = *reinterpret_cast<const f32x4 *>(&s_q[t][16 * m + 4 * r]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (MODE == SWEEP) S[m][e] += (a.scale * x) * qq[e];
-                    else S[m][e] *= al;
-                    pk4[e] += S[m][e] * kk[e];
-                    if (MODE == FWD) pq4[e] += S[m][e] * qq[e];
+            for (int m = 0; m < RM; ++m) {
+                S[m] += y.k[m] * u;
+                if (MODE == SWEEP) S[m] *= y.al;
+            }
+            if (r == 0) {
+                if (MODE == FWD) kda::Elem<TO>::st((TO *)a.o + at + col, a.scale * (pq + u * y.kq));
+                if (MODE == KEEP) (a.R + at)[col] = res;
+                if (MODE == SWEEP) {
+                    kda::Elem<TO>::st((TO *)a.dval + at + col, -u);
+                    (a.Ub + at)[col] = pk;
                 }
             }
-            const float pk = sum_groups((pk4[0] + pk4[1]) + (pk4[2] + pk4[3]));
-            float u;
-            if (MODE == SWEEP) {
-                u = -be * pk;
-                if (r == 0) {
-                    kda::Elem<TO>::st((TO *)a.dval + row * DV + col, be * pk);
-                    a.Ub[row * DV + col] = pk;
-                }
-            } else {
-                const float res = x - pk;
-                u = be * res;
-                if (MODE == KEEP && r == 0) a.R[row * DV + col] = res;
-            }
-            if (MODE == FWD) {
-                const float pq = sum_groups((pq4[0] + pq4[1]) + (pq4[2] + pq4[3]));
-                if (r == 0)
-                    kda::Elem<TO>::st((TO *)a.o + row * DV + col, a.scale * (pq + u * s_kq[t]));
-            }
-#pragma unroll
-            for (int m = 0; m < RT; ++m) {
-                const f32x4 kk = *reinterpret_cast<const f32x4 *>(&s_k[t][16 * m + 4 * r]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    S[m][e] += kk[e] * u;
-                    if (MODE == SWEEP) S[m][e] *= al;
-                }
+        };
+        // a token ahead, two sets of registers in turn
+        Tok x = read(0);
+        for (int i = 0; i < nt; i += 2) {
+            const Tok y = read(i + 1 < nt ? i + 1 : i);
+            step(x, i);
+            if (i + 1 < nt) {
+                x = read(i + 2 < nt ? i + 2 : i + 1);
+                step(y, i + 1);
             }
         }
     }
     float *out = MODE == FWD ? a.S_T : MODE == SWEEP ? a.dS0 : nullptr;
     if (out) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+        for (int m = 0; m < RM; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                out[st + (int64_t)(16 * t + 4 * r + e) * DV] = S[t][e];
+            for (int e = 0; e < 4; ++e) out[st + (int64_t)row_of(m, e) * DV] = S[m][e];
     }
 }
 
-template <typename TI, int DK, int DV>
-hipError_t launch_t(const Args &a, int mode, int C)
+template <typename TI, int DK, int DV, int GC>
+hipError_t launch_gc(const Args &a, int mode)
 {
-    using Sh = Shape<TI, DK, DV>;
+    using Sh = Shape<DK, DV, GC>;
     const int64_t blocks = (int64_t)a.seq.n_seqs * a.Hv * (DV / Sh::BV);
     if (blocks * Sh::NT >= ((int64_t)1 << 32)) return hipErrorInvalidValue;   // grid size limit
     const dim3 grid((unsigned)blocks), block(Sh::NT);
     if (mode == FWD) {
         if constexpr (std::is_same<TI, e4m3>::value) return hipErrorInvalidValue;
-        else hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, FWD>), grid, block, 0, a.stream, a, C);
+        else hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, FWD>), grid, block, 0, a.stream, a);
     } else if (mode == KEEP)
-        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, KEEP>), grid, block, 0, a.stream, a, C);
+        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, KEEP>), grid, block, 0, a.stream, a);
     else
-        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, SWEEP>), grid, block, 0, a.stream, a, C);
+        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, SWEEP>), grid, block, 0, a.stream, a);
     return hipGetLastError();
 }
 
-template <typename TI>
-hipError_t dispatch(const Args &a, int mode, int C)
+template <typename TI, int DK, int DV>
+hipError_t launch_t(const Args &a, int mode)
 {
-#define GDR_CASE(DK_, DV_) if (a.dk == DK_ && a.dv == DV_) return launch_t<TI, DK_, DV_>(a, mode, C);
+    // Sixteen columns a wave do the least work in all; eight (four) give twice
+    // (four times) the waves, each with a shorter step.  Forward, fp32, d = 128,
+    // 4 / 8 / 16 columns a wave: 32 chains of 1024 tokens 0.28 / 0.34 / 0.48 ms;
+    // 128 chains 0.47 / 0.42 / 0.49 ms; 512 chains 1.72 / 1.33 / 1.18 ms.
+    const int64_t columns = (int64_t)a.seq.n_seqs * a.Hv * DV;
+    if constexpr (DK >= 64)
+        if (columns < kFew) return launch_gc<TI, DK, DV, 4>(a, mode);
+    if constexpr (DK >= 32)
+        if (columns < kSome) return launch_gc<TI, DK, DV, 8>(a, mode);
+    return launch_gc<TI, DK, DV, 16>(a, mode);
+}
+
+template <typename TI>
+hipError_t dispatch(const Args &a, int mode)
+{
+#define GDR_CASE(DK_, DV_) if (a.dk == DK_ && a.dv == DV_) return launch_t<TI, DK_, DV_>(a, mode);
 #define GDR_ROW(DK_) GDR_CASE(DK_, 16) GDR_CASE(DK_, 32) GDR_CASE(DK_, 64) GDR_CASE(DK_, 128)
     GDR_ROW(16) GDR_ROW(32) GDR_ROW(64) GDR_ROW(128)
 #undef GDR_ROW
@@ -202,17 +274,17 @@ hipError_t dispatch(const Args &a, int mode, int C)
     return hipErrorInvalidValue;
 }
 
-hipError_t run(const Args &a, int mode, int C)
+hipError_t run(const Args &a, int mode)
 {
-    if (a.in == In::F32) return dispatch<float>(a, mode, C);
-    if (a.in == In::BF16) return dispatch<bf16>(a, mode, C);
-    return dispatch<e4m3>(a, mode, C);
+    if (a.in == In::F32) return dispatch<float>(a, mode);
+    if (a.in == In::BF16) return dispatch<bf16>(a, mode);
+    return dispatch<e4m3>(a, mode);
 }
 
 }  // namespace
 
-hipError_t launch_recurrent_fwd(const Args &a) { return run(a, FWD, 1 << 30); }
-hipError_t launch_recurrent_keep(const Args &a, int C) { return run(a, KEEP, C); }
-hipError_t launch_recurrent_sweep(const Args &a, int C) { return run(a, SWEEP, C); }
+hipError_t launch_recurrent_fwd(const Args &a) { return run(a, FWD); }
+hipError_t launch_recurrent_keep(const Args &a) { return run(a, KEEP); }
+hipError_t launch_recurrent_sweep(const Args &a) { return run(a, SWEEP); }
 
 }  // namespace gdr
