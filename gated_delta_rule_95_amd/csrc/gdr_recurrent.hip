@@ -20,6 +20,13 @@ namespace {
 
 constexpr int TT = 16;               // tokens staged at a time
 
+// raw buffer resource: stores at or past `bytes` are dropped
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void *base, int bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
 enum { FWD = 0, KEEP = 1, SWEEP = 2 };
 
 constexpr int64_t kFew = 8192, kSome = 32768;
@@ -64,9 +71,11 @@ void gdr_recurrent_kernel(Args a)
     constexpr int RM = Sh::RM, NG = Sh::NG, NT = Sh::NT, BV = Sh::BV;
     constexpr int CB = DV / BV;
     struct Tile {
-        float k[TT][DK], q[TT][DK], v[TT][BV], a[TT], b[TT], kq[TT];
+        float k[TT][DK], q[TT][DK], v[TT][BV];
+        float gate[TT][4];           // e^g, beta, k . q (written by different threads)
     };
     __shared__ __align__(16) Tile s_t[2];
+    static_assert(sizeof(Tile) % 16 == 0, "16-byte reads");
     const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int c = lane % GC, r = lane / GC;
     const int64_t chain = blockIdx.x / CB;
@@ -138,7 +147,7 @@ void gdr_recurrent_kernel(Args a)
                 float y = rk[x][0] * rq[x][0] + rk[x][1] * rq[x][1] + rk[x][2] * rq[x][2] + rk[x][3] * rq[x][3];
 #pragma unroll
                 for (int m = 1; m < DK / 4; m *= 2) y += __shfl_xor(y, m);
-                if (t < TT && ch == 0) s.kq[t] = y;
+                if (t < TT && ch == 0) s.gate[t][2] = y;
             }
         }
 #pragma unroll
@@ -147,79 +156,85 @@ void gdr_recurrent_kernel(Args a)
             if (t < TT) *reinterpret_cast<f32x4 *>(&s.v[t][y]) = rv[x];
         }
         if (tid < TT) {
-            s.a[tid] = kda::fast_exp2(floor_g(ra) * LOG2E);
-            s.b[tid] = rb;
+            s.gate[tid][0] = kda::fast_exp2(floor_g(ra) * LOG2E);
+            s.gate[tid][1] = rb;
         }
         // the other half of the LDS was last read before the barrier of the
         // tile before, so one barrier a tile is enough
         __syncthreads();
         if (tile + 1 < tiles) request(tile + 1);
+        // states at the chunks' borders, which are tiles' borders
+        if (MODE == KEEP ? t0 % C == 0 : MODE == SWEEP && (tile == 0 || (t0 + TT) % C == 0)) {
+            const int64_t slot = sq.bos / C + n + t0 / C;
+            float *dst = (MODE == KEEP ? a.Sc : a.Lc) + ((slot * a.Hv + hv) * DK) * DV + col;
+#pragma unroll
+            for (int m = 0; m < RM; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[(int64_t)row_of(m, e) * DV] = S[m][e];
+        }
+        // One lane of a column stores; the others' places, and those of the
+        // rows behind the sequence (whole tiles are run: rows of zeros with
+        // e^g = 1 change nothing), are past the buffers' ends and dropped.
+        const int64_t tok = (int64_t)(sq.bos + t0) * a.Hv * DV;
+        const int rowe = a.Hv * DV, place = r == 0 ? hv * DV + col : 0x10000000;
+        const rsrc_t out0 = make_rsrc(MODE == FWD ? (const void *)((TO *)a.o + tok) : (const void *)((MODE == KEEP ? a.R : a.Ub) + tok),
+                                      nt * rowe * (MODE == FWD ? (int)sizeof(TO) : 4));
+        const rsrc_t out1 = make_rsrc((TO *)a.dval + tok, MODE == SWEEP ? nt * rowe * (int)sizeof(TO) : 0);
+        const auto put = [](rsrc_t r, int at, float x, auto type) {
+            if constexpr (sizeof(type) == 2)
+                __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)x), r, 2 * at, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, 4 * at, 0, 0);
+        };
         struct Tok {
-            f32x4 k[RM], q[RM];
-            float al, be, x, kq;
+            f32x4 k[RM], q[RM], gate;
+            float x;
         };
         const auto read = [&](int i) {
-            const int t = MODE == SWEEP ? nt - 1 - i : i;
+            const int t = MODE == SWEEP ? TT - 1 - i : i;
             Tok y;
 #pragma unroll
             for (int m = 0; m < RM; ++m) {
                 y.k[m] = *reinterpret_cast<const f32x4 *>(&s.k[t][row_of(m, 0)]);
                 if (MODE != KEEP) y.q[m] = *reinterpret_cast<const f32x4 *>(&s.q[t][row_of(m, 0)]);
             }
-            y.al = s.a[t];
-            y.be = s.b[t];
+            y.gate = *reinterpret_cast<const f32x4 *>(s.gate[t]);
             y.x = s.v[t][GC * wave + c];
-            y.kq = MODE == FWD ? s.kq[t] : 0.f;
             return y;
         };
         const auto step = [&](const Tok &y, int i) {
-            const int t = MODE == SWEEP ? nt - 1 - i : i;
-            const int pos = t0 + t;
-            const int64_t at = ((int64_t)(sq.bos + pos) * a.Hv + hv) * DV;
-            if (MODE == KEEP ? pos % C == 0 : MODE == SWEEP && (pos % C == C - 1 || pos == sq.len - 1)) {
-                const int64_t slot = sq.bos / C + n + pos / C;
-                float *dst = (MODE == KEEP ? a.Sc : a.Lc) + ((slot * a.Hv + hv) * DK) * DV + col;
-#pragma unroll
-                for (int m = 0; m < RM; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dst[(int64_t)row_of(m, e) * DV] = S[m][e];
-            }
+            const int at = place + (MODE == SWEEP ? TT - 1 - i : i) * rowe;
+            const float al = y.gate[0], be = y.gate[1];
             // four partial sums each: one would be a chain of dependent adds
             f32x4 pk4 = zero, pq4 = zero;
 #pragma unroll
             for (int m = 0; m < RM; ++m) {
                 if (MODE == SWEEP) S[m] += (a.scale * y.x) * y.q[m];
-                else S[m] *= y.al;
+                else S[m] *= al;
                 pk4 += S[m] * y.k[m];
                 if (MODE == FWD) pq4 += S[m] * y.q[m];
             }
             const float pk = sum_rows<GC>((pk4[0] + pk4[1]) + (pk4[2] + pk4[3]));
             const float pq = MODE == FWD ? sum_rows<GC>((pq4[0] + pq4[1]) + (pq4[2] + pq4[3])) : 0.f;
             const float res = MODE == SWEEP ? pk : y.x - pk;
-            const float u = MODE == SWEEP ? -y.be * pk : y.be * res;
+            const float u = MODE == SWEEP ? -be * pk : be * res;
 #pragma unroll
             for (int m = 0; m < RM; ++m) {
                 S[m] += y.k[m] * u;
-                if (MODE == SWEEP) S[m] *= y.al;
+                if (MODE == SWEEP) S[m] *= al;
             }
-            if (r == 0) {
-                if (MODE == FWD) kda::Elem<TO>::st((TO *)a.o + at + col, a.scale * (pq + u * y.kq));
-                if (MODE == KEEP) (a.R + at)[col] = res;
-                if (MODE == SWEEP) {
-                    kda::Elem<TO>::st((TO *)a.dval + at + col, -u);
-                    (a.Ub + at)[col] = pk;
-                }
-            }
+            if (MODE == FWD) put(out0, at, a.scale * (pq + u * y.gate[2]), TO());
+            if (MODE != FWD) put(out0, at, res, 0.f);
+            if (MODE == SWEEP) put(out1, at, -u, TO());
         };
         // a token ahead, two sets of registers in turn
         Tok x = read(0);
-        for (int i = 0; i < nt; i += 2) {
-            const Tok y = read(i + 1 < nt ? i + 1 : i);
+#pragma unroll 2
+        for (int i = 0; i < TT; i += 2) {
+            const Tok y = read(i + 1);
             step(x, i);
-            if (i + 1 < nt) {
-                x = read(i + 2 < nt ? i + 2 : i + 1);
-                step(y, i + 1);
-            }
+            x = read((i + 2) % TT);
+            step(y, i + 1);
         }
     }
     float *out = MODE == FWD ? a.S_T : MODE == SWEEP ? a.dS0 : nullptr;
