@@ -29,8 +29,7 @@ static hipError_t launch_bwd(const Args &a)
         if ((e = launch_chunk_keep_sweep(a)) != hipSuccess || a.seq.n_tokens == 0) return e;
         return launch_chunk_grad(a);
     }
-    if ((e = launch_recurrent_keep(a)) != hipSuccess) return e;
-    if ((e = launch_recurrent_sweep(a)) != hipSuccess || a.seq.n_tokens == 0) return e;
+    if ((e = launch_recurrent_keep_sweep(a)) != hipSuccess || a.seq.n_tokens == 0) return e;
     return launch_grad32(a);
 }
 

@@ -641,10 +641,10 @@ __device__ __forceinline__ void store_state(const f32x4 *S, float *p, int dv, in
 // the longest sequences first (up to 128 of them): a long chain that starts
 // last would run alone at the end.
 constexpr int kSorted = 128;
-__device__ __forceinline__ bool my_chain(const Args &a, int per_unit, int *lens, int tid, int nthreads, int &n, int &hk,
+__device__ __forceinline__ bool my_chain(const Args &a, int64_t b, int per_unit, int *lens, int tid, int nthreads, int &n, int &hk,
                                          int &j)
 {
-    const int64_t b = blockIdx.x, slot = b / 8;
+    const int64_t slot = b / 8;
     const int64_t u = (slot / per_unit) * 8 + b % 8;
     j = (int)(slot % per_unit);
     if (u >= (int64_t)a.seq.n_seqs * a.Hk) return false;
@@ -667,16 +667,15 @@ __device__ __forceinline__ bool my_chain(const Args &a, int per_unit, int *lens,
     return true;
 }
 
+// workgroup `block` of a pass over all chains
 template <typename TI, int DK, int NC, int MODE>
-__global__ __launch_bounds__((NC + 4) * WAVE)
-void gdr_chunk_kernel(Args a)
+__device__ __forceinline__ void chain_pass(const Args &a, Smem<DK, NC, MODE> &sm, int64_t block)
 {
-    __shared__ Smem<DK, NC, MODE> sm;
     constexpr int BV = 16 * NC;
     const int CB = a.dv / BV, grp = a.Hv / a.Hk;
     int n, hk, j;
     const int tid = threadIdx.x;
-    if (!my_chain(a, grp * CB, reinterpret_cast<int *>(sm.G), tid, (NC + 4) * WAVE, n, hk, j)) return;
+    if (!my_chain(a, block, grp * CB, reinterpret_cast<int *>(sm.G), tid, (NC + 4) * WAVE, n, hk, j)) return;
     const int hv = hk * grp + j / CB, col = (j % CB) * BV;
     const int lane = tid % WAVE, ln = lane % 16, lg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -735,16 +734,56 @@ void gdr_chunk_kernel(Args a)
     if (fin) store_state<DK / 16>(q.S, fin + st, a.dv, lg);
 }
 
-template <typename TI, int DK, int NC, int MODE>
-hipError_t launch_t(const Args &a)
+template <int DK, int NC>
+__global__ __launch_bounds__((NC + 4) * WAVE)
+void gdr_chunk_fwd_kernel(Args a)
+{
+    __shared__ Smem<DK, NC, FWD> sm;
+    static_assert(sizeof(sm) <= 160 * 1024, "LDS");
+    chain_pass<bf16, DK, NC, FWD>(a, sm, blockIdx.x);
+}
+
+// The backward's two passes over the chains do not wait for each other: one
+// launch has the sweep's workgroups (the longer ones) and then the keeping
+// forward's, which share the compute units where either alone leaves some
+// idle.
+template <typename TI, int DK, int NC>
+__global__ __launch_bounds__((NC + 4) * WAVE)
+void gdr_chunk_bwd_kernel(Args a, int64_t half)
+{
+    using Sweep = Smem<DK, NC, SWEEP>;
+    using Keep = Smem<DK, NC, KEEP>;
+    static_assert(sizeof(Keep) <= sizeof(Sweep) && sizeof(Sweep) <= 160 * 1024, "LDS");
+    __shared__ __align__(16) char raw[sizeof(Sweep)];
+    if (blockIdx.x < half) chain_pass<TI, DK, NC, SWEEP>(a, *reinterpret_cast<Sweep *>(raw), blockIdx.x);
+    else chain_pass<TI, DK, NC, KEEP>(a, *reinterpret_cast<Keep *>(raw), blockIdx.x - half);
+}
+
+// workgroups of one pass: units of a key head, padded to whole rounds of XCDs
+template <int NC>
+int64_t pass_blocks(const Args &a)
 {
     const int64_t units = (int64_t)a.seq.n_seqs * a.Hk;
-    const int64_t blocks = (units + 7) / 8 * 8 * (a.Hv / a.Hk) * (a.dv / (16 * NC));
+    return (units + 7) / 8 * 8 * (a.Hv / a.Hk) * (a.dv / (16 * NC));
+}
+
+template <int DK, int NC>
+hipError_t launch_fwd_t(const Args &a)
+{
+    const int64_t blocks = pass_blocks<NC>(a);
     constexpr int NT = (NC + 4) * WAVE;
     if (blocks * NT >= ((int64_t)1 << 32)) return hipErrorInvalidValue;   // grid size limit
-    static_assert(sizeof(Smem<DK, NC, MODE>) <= 160 * 1024, "LDS");
-    hipLaunchKernelGGL((gdr_chunk_kernel<TI, DK, NC, MODE>), dim3((unsigned)blocks), dim3(NT), 0,
-                       a.stream, a);
+    hipLaunchKernelGGL((gdr_chunk_fwd_kernel<DK, NC>), dim3((unsigned)blocks), dim3(NT), 0, a.stream, a);
+    return hipGetLastError();
+}
+
+template <typename TI, int DK>
+hipError_t launch_bwd_t(const Args &a)
+{
+    const int64_t half = pass_blocks<4>(a);
+    constexpr int NT = 8 * WAVE;
+    if (2 * half * NT >= ((int64_t)1 << 32)) return hipErrorInvalidValue;   // grid size limit
+    hipLaunchKernelGGL((gdr_chunk_bwd_kernel<TI, DK, 4>), dim3((unsigned)(2 * half)), dim3(NT), 0, a.stream, a, half);
     return hipGetLastError();
 }
 
@@ -760,21 +799,14 @@ constexpr int64_t kWide = 129;
 hipError_t launch_chunk_fwd(const Args &a)
 {
     if (a.dv == 128 && (int64_t)a.seq.n_seqs * a.Hv >= kWide)
-        return a.dk == 128 ? launch_t<bf16, 128, 8, FWD>(a) : launch_t<bf16, 64, 8, FWD>(a);
-    return a.dk == 128 ? launch_t<bf16, 128, 4, FWD>(a) : launch_t<bf16, 64, 4, FWD>(a);
-}
-
-template <typename TI>
-static hipError_t keep_and_sweep(const Args &a)
-{
-    const hipError_t e = a.dk == 128 ? launch_t<TI, 128, 4, KEEP>(a) : launch_t<TI, 64, 4, KEEP>(a);
-    if (e != hipSuccess) return e;
-    return a.dk == 128 ? launch_t<TI, 128, 4, SWEEP>(a) : launch_t<TI, 64, 4, SWEEP>(a);
+        return a.dk == 128 ? launch_fwd_t<128, 8>(a) : launch_fwd_t<64, 8>(a);
+    return a.dk == 128 ? launch_fwd_t<128, 4>(a) : launch_fwd_t<64, 4>(a);
 }
 
 hipError_t launch_chunk_keep_sweep(const Args &a)
 {
-    return a.in == In::BF16 ? keep_and_sweep<bf16>(a) : keep_and_sweep<e4m3>(a);
+    if (a.in == In::BF16) return a.dk == 128 ? launch_bwd_t<bf16, 128>(a) : launch_bwd_t<bf16, 64>(a);
+    return a.dk == 128 ? launch_bwd_t<e4m3, 128>(a) : launch_bwd_t<e4m3, 64>(a);
 }
 
 }  // namespace gdr

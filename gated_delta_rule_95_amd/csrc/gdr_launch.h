@@ -66,8 +66,7 @@ inline int64_t bwd_slots(int32_t n_seqs, int64_t n_tokens, int C)
 // the kernels behind launch_fwd and launch_bwd (gdr_api.cpp), by form: token
 // by token in fp32, or chunks of 64 on the matrix cores
 hipError_t launch_recurrent_fwd(const Args &a);
-hipError_t launch_recurrent_keep(const Args &a);
-hipError_t launch_recurrent_sweep(const Args &a);
+hipError_t launch_recurrent_keep_sweep(const Args &a);
 hipError_t launch_grad32(const Args &a);
 hipError_t launch_chunk_fwd(const Args &a);
 hipError_t launch_chunk_keep_sweep(const Args &a);

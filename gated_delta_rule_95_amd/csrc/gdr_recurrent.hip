@@ -61,25 +61,25 @@ __device__ __forceinline__ float sum_rows(float x)
 //     L += scale q_t dO_t^T;  Ub_t = L^T k_t;  L = exp(g_t) (L - k_t (beta_t Ub_t)^T),
 // writing dv = beta Ub, Ub, L behind the last token of every chunk (Lc) and
 // dS0.
+template <int DK, int DV, int GC>
+struct Tile {
+    float k[TT][DK], q[TT][DK], v[TT][Shape<DK, DV, GC>::BV];
+    float gate[TT][4];           // e^g, beta, k . q (written by different threads)
+};
+
 template <typename TI, int DK, int DV, int GC, int MODE>
-__global__ __launch_bounds__((Shape<DK, DV, GC>::NT))
-void gdr_recurrent_kernel(Args a)
+__device__ __forceinline__ void token_pass(const Args &a, Tile<DK, DV, GC> *s_t, int64_t block)
 {
     constexpr int C = kRecurrentChunk;
     using Sh = Shape<DK, DV, GC>;
     using TO = typename OutOf<TI>::type;
     constexpr int RM = Sh::RM, NG = Sh::NG, NT = Sh::NT, BV = Sh::BV;
     constexpr int CB = DV / BV;
-    struct Tile {
-        float k[TT][DK], q[TT][DK], v[TT][BV];
-        float gate[TT][4];           // e^g, beta, k . q (written by different threads)
-    };
-    __shared__ __align__(16) Tile s_t[2];
-    static_assert(sizeof(Tile) % 16 == 0, "16-byte reads");
+    static_assert(sizeof(Tile<DK, DV, GC>) % 16 == 0, "16-byte reads");
     const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int c = lane % GC, r = lane / GC;
-    const int64_t chain = blockIdx.x / CB;
-    const int cb = blockIdx.x % CB;
+    const int64_t chain = block / CB;
+    const int cb = (int)(block % CB);
     const int n = (int)(chain / a.Hv), hv = (int)(chain % a.Hv), hk = hv / (a.Hv / a.Hk);
     Seq sq = seq_of(a.seq, n);
     sq.bos = __builtin_amdgcn_readfirstlane(sq.bos);      // addresses of rows are scalar arithmetic
@@ -134,7 +134,7 @@ void gdr_recurrent_kernel(Args a)
     };
     if (tiles > 0) request(0);
     for (int tile = 0; tile < tiles; ++tile) {
-        Tile &s = s_t[tile & 1];
+        Tile<DK, DV, GC> &s = s_t[tile & 1];
         const int t0 = first(tile), nt = sq.len - t0 < TT ? sq.len - t0 : TT;
 #pragma unroll
         for (int x = 0; x < NK; ++x) {
@@ -246,25 +246,38 @@ void gdr_recurrent_kernel(Args a)
     }
 }
 
+// the forward, or the backward's two passes (which do not wait for each other)
+// in one launch: the sweep's workgroups, then the keeping forward's
+template <typename TI, int DK, int DV, int GC, bool BWD>
+__global__ __launch_bounds__((Shape<DK, DV, GC>::NT))
+void gdr_recurrent_kernel(Args a, int64_t half)
+{
+    __shared__ __align__(16) Tile<DK, DV, GC> tiles[2];
+    if constexpr (BWD) {
+        if (blockIdx.x < half) token_pass<TI, DK, DV, GC, SWEEP>(a, tiles, blockIdx.x);
+        else token_pass<TI, DK, DV, GC, KEEP>(a, tiles, blockIdx.x - half);
+    } else
+        token_pass<TI, DK, DV, GC, FWD>(a, tiles, blockIdx.x);
+}
+
 template <typename TI, int DK, int DV, int GC>
-hipError_t launch_gc(const Args &a, int mode)
+hipError_t launch_gc(const Args &a, bool bwd)
 {
     using Sh = Shape<DK, DV, GC>;
-    const int64_t blocks = (int64_t)a.seq.n_seqs * a.Hv * (DV / Sh::BV);
+    const int64_t half = (int64_t)a.seq.n_seqs * a.Hv * (DV / Sh::BV), blocks = bwd ? 2 * half : half;
     if (blocks * Sh::NT >= ((int64_t)1 << 32)) return hipErrorInvalidValue;   // grid size limit
     const dim3 grid((unsigned)blocks), block(Sh::NT);
-    if (mode == FWD) {
-        if constexpr (std::is_same<TI, e4m3>::value) return hipErrorInvalidValue;
-        else hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, FWD>), grid, block, 0, a.stream, a);
-    } else if (mode == KEEP)
-        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, KEEP>), grid, block, 0, a.stream, a);
+    if (bwd)
+        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, true>), grid, block, 0, a.stream, a, half);
+    else if constexpr (!std::is_same<TI, e4m3>::value)
+        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, false>), grid, block, 0, a.stream, a, half);
     else
-        hipLaunchKernelGGL((gdr_recurrent_kernel<TI, DK, DV, GC, SWEEP>), grid, block, 0, a.stream, a);
+        return hipErrorInvalidValue;
     return hipGetLastError();
 }
 
 template <typename TI, int DK, int DV>
-hipError_t launch_t(const Args &a, int mode)
+hipError_t launch_t(const Args &a, bool bwd)
 {
     // Sixteen columns a wave do the least work in all; eight (four) give twice
     // (four times) the waves, each with a shorter step.  Forward, fp32, d = 128,
@@ -272,16 +285,16 @@ hipError_t launch_t(const Args &a, int mode)
     // 128 chains 0.47 / 0.42 / 0.49 ms; 512 chains 1.72 / 1.33 / 1.18 ms.
     const int64_t columns = (int64_t)a.seq.n_seqs * a.Hv * DV;
     if constexpr (DK >= 64)
-        if (columns < kFew) return launch_gc<TI, DK, DV, 4>(a, mode);
+        if (columns < kFew) return launch_gc<TI, DK, DV, 4>(a, bwd);
     if constexpr (DK >= 32)
-        if (columns < kSome) return launch_gc<TI, DK, DV, 8>(a, mode);
-    return launch_gc<TI, DK, DV, 16>(a, mode);
+        if (columns < kSome) return launch_gc<TI, DK, DV, 8>(a, bwd);
+    return launch_gc<TI, DK, DV, 16>(a, bwd);
 }
 
 template <typename TI>
-hipError_t dispatch(const Args &a, int mode)
+hipError_t dispatch(const Args &a, bool bwd)
 {
-#define GDR_CASE(DK_, DV_) if (a.dk == DK_ && a.dv == DV_) return launch_t<TI, DK_, DV_>(a, mode);
+#define GDR_CASE(DK_, DV_) if (a.dk == DK_ && a.dv == DV_) return launch_t<TI, DK_, DV_>(a, bwd);
 #define GDR_ROW(DK_) GDR_CASE(DK_, 16) GDR_CASE(DK_, 32) GDR_CASE(DK_, 64) GDR_CASE(DK_, 128)
     GDR_ROW(16) GDR_ROW(32) GDR_ROW(64) GDR_ROW(128)
 #undef GDR_ROW
@@ -289,17 +302,16 @@ hipError_t dispatch(const Args &a, int mode)
     return hipErrorInvalidValue;
 }
 
-hipError_t run(const Args &a, int mode)
+hipError_t run(const Args &a, bool bwd)
 {
-    if (a.in == In::F32) return dispatch<float>(a, mode);
-    if (a.in == In::BF16) return dispatch<bf16>(a, mode);
-    return dispatch<e4m3>(a, mode);
+    if (a.in == In::F32) return dispatch<float>(a, bwd);
+    if (a.in == In::BF16) return dispatch<bf16>(a, bwd);
+    return dispatch<e4m3>(a, bwd);
 }
 
 }  // namespace
 
-hipError_t launch_recurrent_fwd(const Args &a) { return run(a, FWD); }
-hipError_t launch_recurrent_keep(const Args &a) { return run(a, KEEP); }
-hipError_t launch_recurrent_sweep(const Args &a) { return run(a, SWEEP); }
+hipError_t launch_recurrent_fwd(const Args &a) { return run(a, false); }
+hipError_t launch_recurrent_keep_sweep(const Args &a) { return run(a, true); }
 
 }  // namespace gdr
