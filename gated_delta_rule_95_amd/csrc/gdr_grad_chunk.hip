@@ -33,7 +33,7 @@ struct alignas(16) GradSmem {
     bf16 q[C * DK], k[C * DK];
     union {
         bf16 rows[7][C * SW];                    // dO; U, Yb in three parts each
-        bf16 mat[4][C * C];                      // dP hi, dP lo, dN + dN^T hi, lo   [i][j]
+        bf16 mat[4][C * C];                      // dP hi, dP lo, dN hi, dN lo   [i][j]
     };
     float G[2][C], a[NW][C], b[NW][C], e[8][C], rev[C], ls[NW];
 };
@@ -160,6 +160,31 @@ void gdr_grad_chunk_kernel(Args a)
     const auto block_of = [&](int i) { return kind_of(i) ? 3 - (wave & 3) : wave & 3; };
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     const Eye eye = make_eye(lane);
+    // rows of dO, R and Ub for one stage of value columns of one head, a
+    // thread's part; requested a stage ahead
+    constexpr int TPR = NT / C, CPT = SW / TPR;          // threads a row, columns a thread (a multiple of 8)
+    const int row = tid / TPR, cc = CPT * (tid % TPR);
+    u32x4 ro[CPT / 8];
+    f32x4 rr[CPT / 4], ru[CPT / 4];
+    float rbeta = 0.f, rgate = 0.f;
+    const auto request = [&](int hv, int v0) {
+        const Rows<bf16> O(a.dO, nullptr, tok, nt, a.Hv, DV);
+        const int rb = a.Hv * DV * 4;
+        const rsrc_t br = make_rsrc(reinterpret_cast<const char *>(a.R) + tok * rb, nt * rb);
+        const rsrc_t bu = make_rsrc(reinterpret_cast<const char *>(a.Ub) + tok * rb, nt * rb);
+        const rsrc_t bb = make_rsrc(a.beta + tok * a.Hv, nt * a.Hv * 4), bg = make_rsrc(a.g + tok * a.Hv, nt * a.Hv * 4);
+        const int e = ((row * a.Hv + hv) * DV + v0 + cc) * 4;
+#pragma unroll
+        for (int i = 0; i < CPT / 8; ++i) ro[i] = O.raw(e / 2, 8 * i);
+#pragma unroll
+        for (int i = 0; i < CPT / 4; ++i) {
+            rr[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(br, e + 16 * i, 0, 0));
+            ru[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(bu, e + 16 * i, 0, 0));
+        }
+        rbeta = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bb, (row * a.Hv + hv) * 4, 0, 0));
+        if (v0 == 0) rgate = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bg, (lane * a.Hv + hv) * 4, 0, 0));
+    };
+    request(hk * grp, 0);
     {
         const Rows<TI> Q(a.q, a.qe, tok, nt, a.Hk, DK), K(a.k, a.ke, tok, nt, a.Hk, DK);
 #pragma unroll
@@ -174,48 +199,28 @@ void gdr_grad_chunk_kernel(Args a)
     for (int h = 0; h < grp; ++h) {
         const int hv = hk * grp + h;
         fresh();
-        const rsrc_t rg = make_rsrc(a.g + tok * a.Hv, nt * a.Hv * 4), rbe = make_rsrc(a.beta + tok * a.Hv, nt * a.Hv * 4);
-        const auto gate = [&](rsrc_t r, int row) {
-            return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (row * a.Hv + hv) * 4, 0, 0));
-        };
         if (wave == 0) {
-            const double G = scan64<double>((double)floor_g(gate(rg, lane)) * (double)LOG2E);
+            const double G = scan64<double>((double)floor_g(rgate) * (double)LOG2E);
             const float gh = (float)G;
             s.G[0][lane] = gh;
             s.G[1][lane] = (float)(G - (double)gh);
         }
         // products over the value columns
         f32x4 mat[NKD][4] = {}, x1[4] = {}, x2[4] = {}, x3[4] = {}, ls = zero;
-        constexpr int TPR = NT / C, CPT = SW / TPR;      // threads a row, columns a thread (a multiple of 8)
-        const int row = tid / TPR, cc = CPT * (tid % TPR);
-        const float be = gate(rbe, row);
         float db = 0.f;
         const int64_t st = (slot * a.Hv + hv) * (int64_t)(DK * DV / 4) + wave * VS * 2 * WAVE + lane;     // in f32x4
         const f32x4 *Sc = reinterpret_cast<const f32x4 *>(a.Sc) + st, *Lc = reinterpret_cast<const f32x4 *>(a.Lc) + st;
 #pragma unroll 1
         for (int v0 = 0; v0 < DV; v0 += SW) {
-            const Rows<bf16> O(a.dO, nullptr, tok, nt, a.Hv, DV);
-            const int rb = a.Hv * DV * 4;
-            const rsrc_t rr = make_rsrc(reinterpret_cast<const char *>(a.R) + tok * rb, nt * rb);
-            const rsrc_t ru = make_rsrc(reinterpret_cast<const char *>(a.Ub) + tok * rb, nt * rb);
-            const int e = ((row * a.Hv + hv) * DV + v0 + cc) * 4;
-            u32x4 o[CPT / 8];
-            f32x4 r[CPT / 4], u[CPT / 4];
-#pragma unroll
-            for (int i = 0; i < CPT / 8; ++i) o[i] = O.raw(e / 2, 8 * i);
-#pragma unroll
-            for (int i = 0; i < CPT / 4; ++i) {
-                r[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, e + 16 * i, 0, 0));
-                u[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ru, e + 16 * i, 0, 0));
-            }
             __syncthreads();                     // what lies here has been read
 #pragma unroll
             for (int i = 0; i < CPT / 8; ++i) {
                 const int at = Swz<SW>::at(row, cc + 8 * i);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) db += r[2 * i][j] * u[2 * i][j] + r[2 * i + 1][j] * u[2 * i + 1][j];
-                *reinterpret_cast<bf16x8 *>(&s.rows[0][at]) = Rows<bf16>::bf(o[i]);
-                const Parts<3> U = split8(be * r[2 * i], be * r[2 * i + 1]), Y = split8(be * u[2 * i], be * u[2 * i + 1]);
+                for (int j = 0; j < 4; ++j) db += rr[2 * i][j] * ru[2 * i][j] + rr[2 * i + 1][j] * ru[2 * i + 1][j];
+                *reinterpret_cast<bf16x8 *>(&s.rows[0][at]) = Rows<bf16>::bf(ro[i]);
+                const Parts<3> U = split8(rbeta * rr[2 * i], rbeta * rr[2 * i + 1]);
+                const Parts<3> Y = split8(rbeta * ru[2 * i], rbeta * ru[2 * i + 1]);
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
                     *reinterpret_cast<bf16x8 *>(&s.rows[1 + j][at]) = U.p[j];
@@ -225,13 +230,12 @@ void gdr_grad_chunk_kernel(Args a)
             __syncthreads();
 #pragma unroll 1
             for (int ks = 0; ks < SW / 32; ++ks) {
-                const int vc = 32 * ks + 8 * lg, t0 = (v0 / 32 + ks) * 2 * WAVE;
+                const int vc = 32 * ks + 8 * lg;
                 const auto rows3 = [&](int first, int row) {
                     const int at = Swz<SW>::at(row, vc);
                     return Parts<3>{{lds8(&s.rows[first][at]), lds8(&s.rows[first + 1][at]), lds8(&s.rows[first + 2][at])}};
                 };
-                const Parts<3> S = split8(__builtin_nontemporal_load(Sc + t0), __builtin_nontemporal_load(Sc + t0 + WAVE));
-                const Parts<3> L = split8(__builtin_nontemporal_load(Lc + t0), __builtin_nontemporal_load(Lc + t0 + WAVE));
+                const int t0=(v0/32+ks)*2*WAVE; const Parts<3> S = split8(__builtin_nontemporal_load(Sc + t0), __builtin_nontemporal_load(Sc + t0 + WAVE)), L = split8(__builtin_nontemporal_load(Lc + t0), __builtin_nontemporal_load(Lc + t0 + WAVE));
 #pragma unroll
                 for (int i = 0; i < NKD; ++i) {
                     const int own = 16 * block_of(i) + ln;
@@ -256,6 +260,8 @@ void gdr_grad_chunk_kernel(Args a)
                     if (t == 1) __builtin_amdgcn_sched_barrier(0);
                 }
             }
+            if (v0 + SW < DV) request(hv, v0 + SW);
+            else if (h + 1 < grp) request(hv + 1, 0);
         }
 #pragma unroll
         for (int m = 1; m < TPR; m *= 2) db += __shfl_xor(db, m);
@@ -320,23 +326,8 @@ void gdr_grad_chunk_kernel(Args a)
                 }
                 const u32x2 vh = pack4(v), vl = pack4(v - widen(vh));
                 const int at = Swz<C>::at(i, j);
-                bf16 *mh = s.mat[2 * kind], *ml = s.mat[2 * kind + 1];
-                if (kind == 0) {
-                    *reinterpret_cast<u32x2 *>(&mh[at]) = vh;
-                    *reinterpret_cast<u32x2 *>(&ml[at]) = vl;
-                } else {
-                    // both triangles, each entry with its mirror image
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j + e <= i) {
-                            const uint16_t hb = (uint16_t)(vh[e / 2] >> (16 * (e % 2))), lb = (uint16_t)(vl[e / 2] >> (16 * (e % 2)));
-                            const int mirror = Swz<C>::at(j + e, i);
-                            reinterpret_cast<uint16_t *>(mh)[at + e] = hb;
-                            reinterpret_cast<uint16_t *>(ml)[at + e] = lb;
-                            reinterpret_cast<uint16_t *>(mh)[mirror] = hb;
-                            reinterpret_cast<uint16_t *>(ml)[mirror] = lb;
-                        }
-                }
+                *reinterpret_cast<u32x2 *>(&s.mat[2 * kind][at]) = vh;
+                *reinterpret_cast<u32x2 *>(&s.mat[2 * kind + 1][at]) = vl;
             }
             // sum over j < t <= i of E_ij: [j < t] E by products with zeros
             // and ones, then the rows i >= t
@@ -372,9 +363,14 @@ void gdr_grad_chunk_kernel(Args a)
                 const int at = Swz<C>::at(16 * t + ln, 32 * x + 8 * lg);
 #pragma unroll
                 for (int part = 1; part >= 0; --part) {
-                    if (x <= t / 2) dq[t] = mma(kt, lds8(&s.mat[part][at]), dq[t]);
-                    if (x >= t / 2) dk[t] = mma(qt, tr8<C>(s.mat[part], 32 * x, 16 * t, ln, lg), dk[t]);
-                    dk[t] = mma(kt, lds8(&s.mat[2 + part][at]), dk[t]);
+                    if (x <= t / 2) {
+                        dq[t] = mma(kt, lds8(&s.mat[part][at]), dq[t]);
+                        dk[t] = mma(kt, lds8(&s.mat[2 + part][at]), dk[t]);
+                    }
+                    if (x >= t / 2) {
+                        dk[t] = mma(qt, tr8<C>(s.mat[part], 32 * x, 16 * t, ln, lg), dk[t]);
+                        dk[t] = mma(kt, tr8<C>(s.mat[2 + part], 32 * x, 16 * t, ln, lg), dk[t]);
+                    }
                 }
             }
         }
