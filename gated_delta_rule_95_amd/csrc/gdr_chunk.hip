@@ -14,13 +14,12 @@
 // consumer waves hold 16 columns of S (L) each in registers, in the matrix
 // cores' result layout, and never exchange anything: every operand they
 // multiply from the right is one of their own results.  The triangular system
-// is solved by substitution over four blocks of 16 tokens with the diagonal
-// blocks inverted (so it is as stable as substitution is: keys may repeat).
-// Four producer waves build the next chunk's left operands in the other half
-// of the LDS meanwhile; one barrier a chunk.  Producer w forms row w of the
-// tiles of K K^T and row 3 - w of K Q^T straight from global loads in operand
-// layout, five tiles each, and inverts diagonal block w by itself: no
-// exchange among producers either.
+// is solved by substitution over two blocks of 32 tokens with the diagonal
+// blocks inverted: 16 by 16 by substitution too, joined by one product (so it
+// is as stable as substitution is: keys may repeat).  Four producer waves
+// build the next chunk's left operands in the other half of the LDS meanwhile,
+// two barriers a chunk: two of them form and invert a diagonal block of 32
+// each, two the rest of K K^T and K Q^T, without a word among them.
 #include "gdr_chunk.h"
 
 namespace gdr {
@@ -43,7 +42,9 @@ struct Stage {
     // operands of 1 KiB in lane order
     bf16x8 P[PP][MODE == KEEP ? 1 : 6][WAVE];   // [part][0, 1, 2a, 2b, 3a, 3b]
     bf16x8 Apair[2][3][WAVE];                    // a block of rows against two of columns
-    Block Aone[2], T[4];                         // block against block; inverted diagonal blocks
+    // inverted diagonal blocks of 32: the rows with one block of 16, those with two
+    Block Tone[2];
+    bf16x8 Tpair[2][3][WAVE];
     float eG[C], eR[C];                          // e^G; b e^{G_C - G} (sweep: e^{G_C - G})
     float eGs[C], eGb[C];                        // scale e^G; (sweep) b e^G
     float beta[C];
@@ -98,9 +99,9 @@ __device__ __forceinline__ void loosen(int &ln, int &lg)
     if constexpr (ON) asm volatile("" : "+v"(ln), "+v"(lg));
 }
 
-// Producer W of four.  Its tiles pair the lane tokens of block W (K K^T) and
-// of block 3 - W (K Q^T) with the row tokens of the blocks b before and at
-// them (forward) or at and behind them (sweep).
+// Producer W of four.  A tile pairs the lane tokens of one block of 16 with the
+// row tokens of another, the lane's the later ones in the forward and the
+// earlier ones in the sweep.
 template <typename TI, int DK, int NC, int MODE, int W>
 struct Producer {
     using R = Rows<TI>;
@@ -108,10 +109,15 @@ struct Producer {
     static constexpr int KS = DK / 32;
     static constexpr int VL = NC / 2;            // 16-byte loads of V a thread
     static constexpr bool SW = MODE == SWEEP;
-    static constexpr int X = 3 - W;
-    static constexpr bool kk_tile(int b) { return SW ? b >= W : b <= W; }
-    static constexpr bool kq_tile(int b) { return MODE != KEEP && (SW ? b >= X : b <= X); }
-    typename R::raw_t kw[KS], qx[KS];            // rows of K block W and of Q block X
+    static constexpr int PR = W / 2;             // odd waves: the diagonal block of 32 it inverts
+    // odd waves: the blocks of 16 the off-diagonal tile pairs
+    static constexpr int OL = SW ? 2 * PR : 2 * PR + 1, OR = SW ? 2 * PR + 1 : 2 * PR;
+    // even waves: lane block and first row block of its half of the corner
+    // (rows 2, 3 against 0, 1; sweep: 0, 1 against 2, 3), lane blocks of K Q^T
+    static constexpr int CL = SW ? PR : 2 + PR, CR = SW ? 2 : 0;
+    static constexpr int L0 = SW ? PR : 3 - PR, L1 = 3 - L0;
+    static constexpr bool reaches(int lane, int row) { return SW ? row >= lane : row <= lane; }
+    typename R::raw_t kw[KS], qw[KS];            // rows of K and Q, block W
     u32x4 v[VL];
     typename R::raw_t v8[VL];
     float g, beta;
@@ -121,11 +127,11 @@ struct Producer {
                                          int ln, int lg, int ptid)
     {
         const typename R::at_t at = R::at(ln, a.Hk, hk, DK, 8 * lg);
-        const R K(a.k, a.ke, tok + 16 * W, n - 16 * W, a.Hk, DK), Q(a.q, a.qe, tok + 16 * X, n - 16 * X, a.Hk, DK);
+        const R K(a.k, a.ke, tok + 16 * W, n - 16 * W, a.Hk, DK), Q(a.q, a.qe, tok + 16 * W, n - 16 * W, a.Hk, DK);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             kw[s] = K.raw(at, 32 * s);
-            if (MODE != KEEP) qx[s] = Q.raw(at, 32 * s);
+            if (MODE != KEEP) qw[s] = Q.raw(at, 32 * s);
         }
         const int row = ptid / 4, cv = col + (ptid % 4) * (4 * NC);
         if constexpr (SW) {
@@ -143,7 +149,7 @@ struct Producer {
         beta = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb, (lane * a.Hv + hv) * 4, 0, 0));
     }
 
-    // A operands in three parts from a lane's four values of one tile
+    // left operands in three parts from a lane's four values of one tile
     static __device__ __forceinline__ void put_block(Block &t, int lane, f32x4 x, const Eye &eye)
     {
         u32x2 h, m, l;
@@ -158,6 +164,87 @@ struct Producer {
         split_half(x, eye, p[0], p[1], p[2]);
 #pragma unroll
         for (int i = 0; i < 3; ++i) reinterpret_cast<u32x2 *>(&t[i][lane])[side] = p[i];
+    }
+    // decays between lane token x and the row tokens y .. y + 3, times w
+    static __device__ __forceinline__ f32x4 decays(const float (*gp)[C], int x, int y, f32x4 w)
+    {
+        const float gh = gp[0][x], gl = gp[1][x];
+        const f32x4 yh = ld4f(&gp[0][y]), yl = ld4f(&gp[1][y]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float d = (gh - yh[e]) + (gl - yl[e]);
+            w[e] *= kda::fast_exp2(SW ? -d : d);
+        }
+        return w;
+    }
+
+    // (I + A)^-1 of a diagonal block of 32 from its tiles, into the stage
+    static __device__ __forceinline__ void invert(St &st, f32x4 d0, f32x4 d1, f32x4 off, const Eye &eye, int ln, int lg)
+    {
+        const int lane = ln + 16 * lg;
+        // three tiles of 16 x 16 floats where the operands go later
+        float *sc = reinterpret_cast<float *>(st.Tpair[PR]), *s0 = sc, *s1 = sc + 256, *so = sc + 512;
+        *reinterpret_cast<f32x4 *>(&s0[16 * ln + 4 * lg]) = d0;
+        *reinterpret_cast<f32x4 *>(&s1[16 * ln + 4 * lg]) = d1;
+        *reinterpret_cast<f32x4 *>(&so[16 * ln + 4 * lg]) = off;
+        __builtin_amdgcn_wave_barrier();
+        // Both blocks of 16 at once, one a half wave: lane row i = ln solves
+        // t (I + A) = e_i, each entry when final taken out of those left (from
+        // the last to the first; sweep: A is upper triangular, from the first
+        // on).  Row j is read a step ahead.
+        float *mine = sc + 256 * (lg >> 1);
+        float t[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) t[j] = ln == j ? 1.f : 0.f;
+        f32x4 av[4];
+        const auto row = [&](int j, f32x4 *x) {
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4)
+                if (SW ? 4 * k4 + 3 > j : 4 * k4 < j) x[k4] = ld4f(&mine[16 * j + 4 * k4]);
+        };
+        row(SW ? 0 : 15, av);
+#pragma unroll
+        for (int jj = 0; jj < 15; ++jj) {
+            const int j = SW ? jj : 15 - jj;
+            f32x4 ahead[4];
+            if (jj < 14) row(SW ? j + 1 : j - 1, ahead);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (SW ? k > j : k < j) t[k] -= t[j] * av[k / 4][k % 4];
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) av[k4] = ahead[k4];
+            // The step's updates are independent of one another and made now:
+            // left to itself the compiler gathers each entry's into a chain
+            // at its end, with every row in registers.
+            asm volatile("" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]), "+v"(t[4]), "+v"(t[5]), "+v"(t[6]), "+v"(t[7]));
+            asm volatile("" : "+v"(t[8]), "+v"(t[9]), "+v"(t[10]), "+v"(t[11]), "+v"(t[12]), "+v"(t[13]), "+v"(t[14]), "+v"(t[15]));
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+            *reinterpret_cast<f32x4 *>(&mine[16 * ln + 4 * k4]) = f32x4{t[4 * k4], t[4 * k4 + 1], t[4 * k4 + 2], t[4 * k4 + 3]};
+        asm volatile("" ::: "memory");
+        // X = -T_L A T_R for the off-diagonal tile (lane block L, row block R),
+        // transposed and on the fp32 matrix cores: W = A^T T_L^T, X^T = -T_R^T W
+        const float *tl = OL % 2 ? s1 : s0, *tr = OL % 2 ? s0 : s1;
+        const f32x4 t0 = ld4f(&s0[16 * ln + 4 * lg]), t1 = ld4f(&s1[16 * ln + 4 * lg]);
+        const f32x4 bl = OL % 2 ? t1 : t0;
+        (void)tl;
+        f32x4 w = {0.f, 0.f, 0.f, 0.f}, x = w;
+        float ac[4], tc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ac[i] = so[16 * (4 * lg + i) + ln];
+            tc[i] = tr[16 * (4 * lg + i) + ln];
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w = __builtin_amdgcn_mfma_f32_16x16x4f32(ac[i], bl[i], w, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = __builtin_amdgcn_mfma_f32_16x16x4f32(tc[i], w[i], x, 0, 0, 0);
+        put_block(st.Tone[PR], lane, SW ? t1 : t0, eye);
+        put_side(st.Tpair[PR], lane, 0, SW ? t0 : -x, eye);
+        put_side(st.Tpair[PR], lane, 1, SW ? -x : t1, eye);
     }
 
     // builds the stage; `next` requests the chunk after it once this one's
@@ -184,13 +271,11 @@ struct Producer {
             if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
         }
         // K and Q blocks and the values to the stage
-        bf16x8 kf[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int c = 32 * s + 8 * lg;
-            kf[s] = R::bf(kw[s]);
-            *reinterpret_cast<bf16x8 *>(&st.K[Swz<DK>::at(16 * W + ln, c)]) = kf[s];
-            if constexpr (MODE != KEEP) *reinterpret_cast<bf16x8 *>(&st.Q[Swz<DK>::at(16 * X + ln, c)]) = R::bf(qx[s]);
+            const int at = Swz<DK>::at(16 * W + ln, 32 * s + 8 * lg);
+            *reinterpret_cast<bf16x8 *>(&st.K[at]) = R::bf(kw[s]);
+            if constexpr (MODE != KEEP) *reinterpret_cast<bf16x8 *>(&st.Q[at]) = R::bf(qw[s]);
         }
         {
             const int row = ptid / 4, c = (ptid % 4) * (4 * NC);
@@ -200,106 +285,92 @@ struct Producer {
         }
         __syncthreads();                 // rows of the chunk are in the stage
         next();
-        // tile products
         loosen<NC == 8>(ln, lg);
-        f32x4 kk[4] = {}, kq[4] = {};
+        const auto rows = [&](const bf16 *x, int b, int s) { return lds8(&x[Swz<DK>::at(16 * b + ln, 32 * s + 8 * lg)]); };
+        // with few registers, the reads of one step at a time
+        const auto step_end = [] {
+            if constexpr (NC == 8) __builtin_amdgcn_sched_barrier(0);
+        };
+        if constexpr (W % 2) {
+            // the three tiles of the diagonal block of 32
+            f32x4 d0 = {}, d1 = {}, off = {};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const int c = 32 * s + 8 * lg;
-            bf16x8 xf = {};
-            if constexpr (MODE == FWD) xf = lds8(&st.Q[Swz<DK>::at(16 * X + ln, c)]);
-            if constexpr (SW) xf = lds8(&st.K[Swz<DK>::at(16 * X + ln, c)]);
+            for (int s = 0; s < KS; ++s) {
+                const bf16x8 k0 = rows(st.K, 2 * PR, s), k1 = rows(st.K, 2 * PR + 1, s);
+                d0 = mma(k0, k0, d0);
+                d1 = mma(k1, k1, d1);
+                off = SW ? mma(k1, k0, off) : mma(k0, k1, off);
+                step_end();
+            }
+            loosen<NC == 8>(ln, lg);
+            const int x0 = 32 * PR + ln, y0 = 32 * PR + 4 * lg;
+            const f32x4 b0 = ld4f(&gp[2][y0]), b1 = ld4f(&gp[2][y0 + 16]);
+            d0 = decays(gp, x0, y0, b0 * d0);
+            d1 = decays(gp, x0 + 16, y0 + 16, b1 * d1);
+            off = decays(gp, 16 * OL + ln, 16 * OR + 4 * lg, (SW ? b1 : b0) * off);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!(SW ? 4 * lg + e > ln : 4 * lg + e < ln)) d0[e] = d1[e] = 0.f;
+            invert(st, d0, d1, off, eye, ln, lg);
+        } else {
+            // two tiles of the corner and five of K Q^T
+            f32x4 kk[2] = {}, q0[4] = {}, q1[4] = {};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const bf16x8 kl = rows(st.K, CL, s);
+                bf16x8 l0 = {}, l1 = {};
+                if constexpr (MODE != KEEP) {
+                    l0 = rows(SW ? st.K : st.Q, L0, s);
+                    l1 = rows(SW ? st.K : st.Q, L1, s);
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const bool corner = b == CR || b == CR + 1, any = MODE != KEEP && (reaches(L0, b) || reaches(L1, b));
+                    bf16x8 kb = {}, rb = {};
+                    if (corner || (!SW && any)) kb = rows(st.K, b, s);
+                    if (any) rb = SW ? rows(st.Q, b, s) : kb;
+                    if (corner) kk[b - CR] = mma(kb, kl, kk[b - CR]);
+                    if (MODE != KEEP && reaches(L0, b)) q0[b] = mma(rb, l0, q0[b]);
+                    if (MODE != KEEP && reaches(L1, b)) q1[b] = mma(rb, l1, q1[b]);
+                }
+                step_end();
+            }
+            loosen<NC == 8>(ln, lg);
+            lane = ln + 16 * lg;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                bf16x8 bf = {};
-                if (kk_tile(b) || (!SW && kq_tile(b))) bf = b == W ? kf[s] : lds8(&st.K[Swz<DK>::at(16 * b + ln, c)]);
-                if (kk_tile(b)) kk[b] = mma(bf, kf[s], kk[b]);
-                if (kq_tile(b)) kq[b] = mma(SW ? lds8(&st.Q[Swz<DK>::at(16 * b + ln, c)]) : bf, xf, kq[b]);
+                const int y = 16 * b + 4 * lg;
+                const f32x4 be = ld4f(&gp[2][y]), w = SW ? f32x4{scale, scale, scale, scale} : scale * be;
+                if (b == CR || b == CR + 1) kk[b - CR] = decays(gp, 16 * CL + ln, y, be * kk[b - CR]);
+                if (MODE != KEEP && reaches(L0, b)) q0[b] = decays(gp, 16 * L0 + ln, y, w * q0[b]);
+                if (MODE != KEEP && reaches(L1, b)) q1[b] = decays(gp, 16 * L1 + ln, y, w * q1[b]);
             }
-        }
-        loosen<NC == 8>(ln, lg);
-        lane = ln + 16 * lg;
-        // tiles: lane token x, row tokens y = 16 b + 4 lg + e; x is the later
-        // one in the forward, the earlier one in the sweep
-        const int xk = 16 * W + ln, xq = 16 * X + ln;
-        const float ghk = gp[0][xk], glk = gp[1][xk], ghq = gp[0][xq], glq = gp[1][xq];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (!kk_tile(b) && !kq_tile(b)) continue;
-            const int y = 16 * b + 4 * lg;
-            const f32x4 yh = ld4f(&gp[0][y]), yl = ld4f(&gp[1][y]), yb = ld4f(&gp[2][y]), sb = scale * yb;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (kk_tile(b)) {
-                    const float d = (ghk - yh[e]) + (glk - yl[e]);
-                    kk[b][e] = kda::fast_exp2(SW ? -d : d) * (yb[e] * kk[b][e]);
-                    if (b == W && !(SW ? y + e > xk : y + e < xk)) kk[b][e] = 0.f;
-                }
-                if (kq_tile(b)) {
-                    const float d = (ghq - yh[e]) + (glq - yl[e]);
-                    kq[b][e] = kda::fast_exp2(SW ? -d : d) * ((SW ? scale : sb[e]) * kq[b][e]);
-                    if (b == X && !(SW ? y + e >= xq : y + e <= xq)) kq[b][e] = 0.f;
-                }
-            }
-        }
-        float *sc = reinterpret_cast<float *>(&st.T[W]);     // the diagonal block, 20 floats a row
-        *reinterpret_cast<f32x4 *>(&sc[20 * ln + 4 * lg]) = kk[W];
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            // forward: 1 <- 0, 3 <- 2 one block, 2 and 3 <- (0, 1);
-            // sweep: 2 <- 3, 0 <- 1 one block, 1 and 0 <- (2, 3)
-            if (kk_tile(b) && b != W) {
-                if ((W ^ 1) == b) put_block(st.Aone[SW ? (W == 2 ? 0 : 1) : (W == 1 ? 0 : 1)], lane, -kk[b], eye);
-                else put_side(st.Apair[SW ? (W == 1 ? 0 : 1) : (W == 2 ? 0 : 1)], lane, b & 1, -kk[b], eye);
-            }
-            if (kq_tile(b)) {
-                constexpr int r = X;
+            for (int e = 0; e < 4; ++e)
+                if (SW ? 4 * lg + e < ln : 4 * lg + e > ln) q0[L0][e] = q1[L1][e] = 0.f;
+            // sweep: rows 1 and 0 are in this order in the pairs
+            put_side(st.Apair[SW ? 1 - PR : PR], lane, 0, -kk[0], eye);
+            put_side(st.Apair[SW ? 1 - PR : PR], lane, 1, -kk[1], eye);
+            const auto put_p = [&](int r, int b, f32x4 x) {
                 const int op = SW ? (r < 2 ? 2 * r + (b >> 1) : r + 2) : (r < 2 ? r : 2 * r - 2 + (b >> 1));
-                f32x4 x = kq[b];
 #pragma unroll
                 for (int i = 0; i < St::PP; ++i) {
                     const u32x2 h = pack4(x);
                     reinterpret_cast<u32x2 *>(&st.P[i][op][lane])[b & 1] = h;
                     if (i + 1 < St::PP) x = mma(eye.a, join(h, h), x);
                 }
+            };
+            if constexpr (MODE != KEEP) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (reaches(L0, b)) put_p(L0, b, q0[b]);
+                    if (reaches(L1, b)) put_p(L1, b, q1[b]);
+                }
             }
         }
-        // (I + A)^-1 of the diagonal block by rows: lane row i = ln solves
-        // t (I + A) = e_i, each entry when final taken out of those left
-        // (from the last to the first; sweep: A is upper triangular, from the
-        // first on)
-        float t[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) t[j] = ln == j ? 1.f : 0.f;
-        f32x4 av[4];
-#pragma unroll
-        for (int jj = 0; jj < 15; ++jj) {
-            const int j = SW ? jj : 15 - jj;
-            // row j is read a step ahead
-            const auto row = [&](int j, f32x4 *av) {
-#pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4)
-                    if (SW ? 4 * k4 + 3 > j : 4 * k4 < j) av[k4] = ld4f(&sc[20 * j + 4 * k4]);
-            };
-            if (jj == 0) row(j, av);
-            f32x4 ahead[4];
-            if (jj < 14) row(SW ? j + 1 : j - 1, ahead);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (SW ? k > j : k < j) t[k] -= t[j] * av[k / 4][k % 4];
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) av[k4] = ahead[k4];
-        }
-        f32x4 tv;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            tv[e] = lg == 0 ? t[e] : lg == 1 ? t[4 + e] : lg == 2 ? t[8 + e] : t[12 + e];
-        __builtin_amdgcn_wave_barrier();
-        put_block(st.T[W], lane, tv, eye);
     }
 
-    // every chunk of the chain: first .. in steps of `step` (chunks of them)
+    // every chunk of the chain; where(c): its first token and rows
     template <typename Tok>
     static __device__ __forceinline__ void run(const Args &a, Smem<DK, NC, MODE> &sm, int chunks, Tok where, int hk, int hv,
                                                int col, int lane, int ptid)
@@ -332,21 +403,20 @@ struct Producer {
 // eight channels of one 16-byte operand read
 __device__ __forceinline__ int channel(int t, int lg, int e) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1) + e; }
 
-// left operands in registers
-struct BlockRegs {
-    u32x2 h, m, l;
-    __device__ __forceinline__ BlockRegs(const Block &t, int lane) : h(t.p[0][lane]), m(t.p[1][lane]), l(t.p[2][lane]) {}
-};
+// a block of rows against two of columns, in registers
 struct PairRegs {
     bf16x8 h, m, l;
     __device__ __forceinline__ PairRegs(const bf16x8 (*t)[WAVE], int lane) : h(t[0][lane]), m(t[1][lane]), l(t[2][lane]) {}
+    // one block: the other's columns are zero
+    __device__ __forceinline__ PairRegs(const Block &t, int lane, bool second)
+    {
+        const u32x2 z = {0, 0};
+        const u32x2 a = t.p[0][lane], b = t.p[1][lane], c = t.p[2][lane];
+        h = second ? join(z, a) : join(a, z);
+        m = second ? join(z, b) : join(b, z);
+        l = second ? join(z, c) : join(c, z);
+    }
 };
-__device__ __forceinline__ f32x4 mul_block(const BlockRegs &t, const Half &b, f32x4 c)
-{
-    c = mma(join(t.h, t.l), b.lh, c);
-    c = mma(join(t.m, t.m), b.hm, c);
-    return mma(join(t.h, t.h), b.hm, c);
-}
 __device__ __forceinline__ f32x4 mul_pair(const PairRegs &t, const Parts<3> &b, f32x4 c)
 {
     c = mma(t.h, b.p[2], c);
@@ -430,7 +500,7 @@ struct Consumer {
             vt[t] = lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
             eg[t] = ld4f(&st.eG[16 * t + 4 * lg]);
         }
-        const BlockRegs T0(st.T[0], lane), A10(st.Aone[0], lane), T1(st.T[1], lane);
+        const PairRegs T0(st.Tone[0], lane, false), T1(st.Tpair[0], lane);
         pin();
         f32x4 X[4] = {}, O[4] = {}, R[4];
         Parts<2> p[KS];
@@ -466,31 +536,29 @@ struct Consumer {
                 for (int t = 0; t < 4; ++t)
                     O[t] = mma_by_parts(p[s], lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
         };
-        u32x2 h, m, l;
-        Half x = split_half(R[0], eye, h, m, l);
+        const Parts<3> y01 = split_pair<3>(R[0], R[1], eye);
         qs(0);
-        R[0] = mul_block(T0, x, zero);
+        R[0] = mul_pair(T0, y01, zero);
+        R[1] = mul_pair(T1, y01, zero);
         qs(1);
-        x = split_half(R[0], eye, h, m, l);
-        R[1] = mul_block(A10, x, R[1]);
-        qs(2);
-        x = split_half(R[1], eye, h, m, l);
-        qs(3);
-        R[1] = mul_block(T1, x, zero);
-        const BlockRegs T2(st.T[2], lane), A32(st.Aone[1], lane), T3(st.T[3], lane);
+        const PairRegs T2(st.Tone[1], lane, false), T3(st.Tpair[1], lane);
         const f32x4 er2 = ld4f(&st.eR[32 + 4 * lg]), er3 = ld4f(&st.eR[48 + 4 * lg]);
         pin();
-#pragma unroll
-        for (int t = 0; t < RT; ++t) S[t] *= gam;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) O[t] *= st.eGs[16 * t + ln];
         const Parts<3> r01 = split_pair<3>(R[0], R[1], eye);
+        qs(2);
         R[2] = mul_pair(A2, r01, R[2]);
         R[3] = mul_pair(A3, r01, R[3]);
+        qs(3);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) S[t] *= gam;
+        const Parts<3> y23 = split_pair<3>(R[2], R[3], eye);
         const Parts<3> u0 = split_pair<3>(er0 * R[0], er1 * R[1], eye);
-        x = split_half(R[2], eye, h, m, l);
         update(st.K, u0, 0, 0, RT / 2, ln, lg);
-        R[2] = mul_block(T2, x, zero);
+        R[2] = mul_pair(T2, y23, zero);
+        R[3] = mul_pair(T3, y23, zero);
+        update(st.K, u0, 0, RT / 2, RT, ln, lg);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) O[t] *= st.eGs[16 * t + ln];
         // operands 0, 1, 2a, 2b, 3a, 3b: rows 0, 1, 2, 2, 3, 3 against tokens
         // 0-31 (2b, 3b: 32-63)
         const auto pr = [&](int i, int t, bf16x8 rh, bf16x8 rm) {
@@ -501,15 +569,11 @@ struct Consumer {
                 O[t] = mma(rh, ph, O[t]);
             }
         };
-        pr(0, 0, r01.p[0], r01.p[1]);
-        pr(1, 1, r01.p[0], r01.p[1]);
-        x = split_half(R[2], eye, h, m, l);
-        pr(2, 2, r01.p[0], r01.p[1]);
-        R[3] = mul_block(A32, x, R[3]);
-        pr(4, 3, r01.p[0], r01.p[1]);
-        x = split_half(R[3], eye, h, m, l);
-        update(st.K, u0, 0, RT / 2, RT, ln, lg);
-        R[3] = mul_block(T3, x, zero);
+        const Parts<2> r01h = {{r01.p[0], r01.p[1]}};
+        pr(0, 0, r01h.p[0], r01h.p[1]);
+        pr(1, 1, r01h.p[0], r01h.p[1]);
+        pr(2, 2, r01h.p[0], r01h.p[1]);
+        pr(4, 3, r01h.p[0], r01h.p[1]);
         const Parts<3> u1 = split_pair<3>(er2 * R[2], er3 * R[3], eye);
         const Parts<2> r23 = MODE == FWD ? split_pair<2>(R[2], R[3], eye) : Parts<2>{};
         pr(3, 2, r23.p[0], r23.p[1]);
@@ -540,7 +604,7 @@ struct Consumer {
             d[t] = lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
             er[t] = ld4f(&st.eR[16 * t + 4 * lg]);
         }
-        const BlockRegs T3(st.T[3], lane), A23(st.Aone[0], lane), T2(st.T[2], lane);
+        const PairRegs T3(st.Tone[1], lane, true), T2(st.Tpair[1], lane);
         __builtin_amdgcn_sched_barrier(0);
         f32x4 F[4] = {};
 #pragma unroll
@@ -569,41 +633,32 @@ struct Consumer {
         };
         pd(5, 3, d23);
         pd(4, 2, d23);
-        u32x2 h, m, l;
-        Half x = split_half(F[3], eye, h, m, l);
+        const Parts<3> f23 = split_pair<3>(F[2], F[3], eye);
         pd(3, 1, d23);
-        F[3] = mul_block(T3, x, zero);
         pd(1, 0, d23);
-        x = split_half(F[3], eye, h, m, l);
+        F[3] = mul_pair(T3, f23, zero);
+        F[2] = mul_pair(T2, f23, zero);
         pd(2, 1, d01);
-        F[2] = mul_block(A23, x, F[2]);
         pd(0, 0, d01);
-        x = split_half(F[2], eye, h, m, l);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) S[t] *= gam;
-        const Parts<3> w01 = split_pair<3>(eg[0] * widen(d[0]), eg[1] * widen(d[1]), eye);
-        const Parts<3> w23 = split_pair<3>(eg[2] * widen(d[2]), eg[3] * widen(d[3]), eye);
-        F[2] = mul_block(T2, x, zero);
-        const BlockRegs T1(st.T[1], lane), A01(st.Aone[1], lane), T0(st.T[0], lane);
+        const PairRegs T1(st.Tone[0], lane, true), T0(st.Tpair[0], lane);
         f32x4 eb[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) eb[t] = ld4f(&st.eGb[16 * t + 4 * lg]);
         __builtin_amdgcn_sched_barrier(0);
         const Parts<3> u23 = split_pair<3>(F[2], F[3], eye);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) S[t] *= gam;
+        const Parts<3> w01 = split_pair<3>(eg[0] * widen(d[0]), eg[1] * widen(d[1]), eye);
         F[1] = mul_pair(A1, u23, F[1]);
         F[0] = mul_pair(A0, u23, F[0]);
-        const Parts<3> y23 = split_pair<3>(-eb[2] * F[2], -eb[3] * F[3], eye);
-        x = split_half(F[1], eye, h, m, l);
+        const Parts<3> w23 = split_pair<3>(eg[2] * widen(d[2]), eg[3] * widen(d[3]), eye);
         update(st.Q, w01, 0, 0, RT, ln, lg);
-        F[1] = mul_block(T1, x, zero);
-        update(st.Q, w23, 1, 0, RT / 2, ln, lg);
-        x = split_half(F[1], eye, h, m, l);
-        update(st.Q, w23, 1, RT / 2, RT, ln, lg);
-        F[0] = mul_block(A01, x, F[0]);
-        update(st.K, y23, 1, 0, RT / 2, ln, lg);
-        x = split_half(F[0], eye, h, m, l);
-        update(st.K, y23, 1, RT / 2, RT, ln, lg);
-        F[0] = mul_block(T0, x, zero);
+        const Parts<3> f01 = split_pair<3>(F[0], F[1], eye);
+        const Parts<3> y23 = split_pair<3>(-eb[2] * F[2], -eb[3] * F[3], eye);
+        update(st.Q, w23, 1, 0, RT, ln, lg);
+        F[1] = mul_pair(T1, f01, zero);
+        F[0] = mul_pair(T0, f01, zero);
+        update(st.K, y23, 1, 0, RT, ln, lg);
         const Parts<3> u01 = split_pair<3>(F[0], F[1], eye);
         const Parts<3> y01 = split_pair<3>(-eb[0] * F[0], -eb[1] * F[1], eye);
         // dv = beta Ub, from the transposed rows

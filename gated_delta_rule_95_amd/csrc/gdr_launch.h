@@ -58,7 +58,7 @@ constexpr int kRecurrentChunk = 32;
 // ... and in either form
 int bwd_chunk(int dk, int dv, bool bf16);
 // chunk slots cu_seqlens[n] / C + n + c of a batch: an upper bound on every slot + 1
-inline int64_t bwd_slots(int32_t n_seqs, int64_t n_tokens, int C)
+__host__ __device__ inline int64_t bwd_slots(int32_t n_seqs, int64_t n_tokens, int C)
 {
     return n_tokens / C + n_seqs + 1;
 }
