@@ -88,6 +88,16 @@ kda_status check_seqs(int32_t n_seqs, int64_t n_tokens, const int32_t *cu)
     return KDA_OK;
 }
 
+// Launches must stay below 2^32 threads.  The widest ones: 2048 threads a
+// (sequence, value head) chain, 1024 a decoded head, 512 a 64-token chunk and
+// key head (256 a 32-token one).  Checked before anything is launched.
+kda_status check_chains(int64_t chains, const char *what)
+{
+    if (chains >= (int64_t)1 << 21)
+        return set_error(KDA_ERR_INVALID_ARG, "%s * H_v must be below 2^21", what);
+    return KDA_OK;
+}
+
 kda_status check_dtype(kda_dtype t)
 {
     if (t != KDA_F32 && t != KDA_BF16)
@@ -160,6 +170,9 @@ kda_status bwd_impl(const char *fn, const void *q, const uint8_t *qe, const void
     kda_status s;
     if ((s = check_heads(Hk, Hv, dk, dv)) != KDA_OK) return s;
     if ((s = check_seqs(n_seqs, n_tokens, cu)) != KDA_OK) return s;
+    if ((s = check_chains((int64_t)n_seqs * Hv, "n_seqs")) != KDA_OK) return s;
+    if (gdr::bwd_slots(n_seqs, n_tokens, gdr::bwd_chunk(dk, dv, in != gdr::In::F32)) * Hk >= (int64_t)1 << 23)
+        return set_error(KDA_ERR_INVALID_ARG, "too many chunks times H_k for one launch (2^23)");
     if (n_seqs == 0) return ok();
     const bool e8 = in == gdr::In::E4M3, tok = n_tokens > 0;
     const size_t ib = in == gdr::In::F32 ? 4 : 2, qb = e8 ? 1 : ib;
@@ -209,6 +222,7 @@ GDR_API kda_status gdr_fwd_chunked(const void *q, const void *k, const void *v, 
     if ((s = check_dtype(in_dtype)) != KDA_OK) return s;
     if ((s = check_heads(H_k, H_v, d_k, d_v)) != KDA_OK) return s;
     if ((s = check_seqs(n_seqs, n_tokens, cu_seqlens)) != KDA_OK) return s;
+    if ((s = check_chains((int64_t)n_seqs * H_v, "n_seqs")) != KDA_OK) return s;
     if (n_seqs == 0) return ok();
     const bool tok = n_tokens > 0;
     const size_t ib = in_dtype == KDA_BF16 ? 2 : 4;
@@ -238,6 +252,7 @@ GDR_API kda_status gdr_decode_step(const void *q, const void *k, const void *v, 
     if ((s = check_dtype(in_dtype)) != KDA_OK) return s;
     if ((s = check_heads(H_k, H_v, d_k, d_v)) != KDA_OK) return s;
     if (N < 0) return set_error(KDA_ERR_INVALID_ARG, "N must be >= 0 (got %d)", N);
+    if ((s = check_chains((int64_t)N * H_v, "N")) != KDA_OK) return s;
     if (n_slots < 0) return set_error(KDA_ERR_INVALID_ARG, "n_slots must be >= 0 (got %d)", n_slots);
     if (!slots && N > n_slots)
         return set_error(KDA_ERR_INVALID_ARG, "without slots N (%d) must be at most n_slots (%d)", N,

@@ -37,7 +37,9 @@
  * decay, however fast, overflows.
  *
  * Sizes: d_k, d_v in {16, 32, 64, 128}, independently; 1 <= H_k, H_v a
- * multiple of H_k, H_v * max(d_k, d_v) < 2^22; 0 <= n_tokens <= 2^31 - 64.
+ * multiple of H_k, H_v * max(d_k, d_v) < 2^22; 0 <= n_tokens <= 2^31 - 64;
+ * n_seqs * H_v (decode: N * H_v) < 2^21.  The backward also wants fewer than
+ * 2^23 (chunk of 64 tokens, key head) pairs (32 tokens in the fp32 form).
  * in_dtype KDA_BF16 or KDA_F32.
  *
  * Alignment (bytes): q, k, v, o, dO, dq, dk, dv: eight elements of bf16 and

@@ -48,7 +48,7 @@ def fwd(lib, **kw):
     (dict(n=3), 1, "multiple"), (dict(n=0), 1, "n_seqs == 0"), (dict(dt=7), 1, "in_dtype"),
     (dict(q=P + 8), 1, "aligned"), (dict(S0=7 * P + 4), 1, "aligned"), (dict(cu=7 * P + 2), 1, "aligned"),
     (dict(o=3 * P), 1, "overlaps"), (dict(ST=3 * P), 1, "overlaps"), (dict(ST=6 * P + 64), 1, "overlaps"),
-    (dict(N=1 << 31), 1, "2^31"), (dict(Hv=1 << 16, dk=128), 1, "2^22"),
+    (dict(N=1 << 31), 1, "2^31"), (dict(n=1 << 20, N=1 << 20), 1, "2^21"), (dict(Hv=1 << 16, dk=128), 1, "2^22"),
 ])
 def test_fwd_refusals(lib, kw, status, msg):
     assert fwd(lib, **kw) == status
@@ -74,7 +74,7 @@ def dec(lib, **kw):
     (dict(S=None), 1, "S is NULL"), (dict(N=-1), 1, "N must"), (dict(ns=-1), 1, "n_slots"),
     (dict(ns=1), 1, "without slots"), (dict(dk=8), 2, "d_k"), (dict(S=P), 1, "overlaps"),
     (dict(S=8 * P + 8), 1, "aligned"), (dict(slots=7 * P + 1), 1, "aligned"), (dict(o=P), 1, "overlaps"),
-    (dict(slots=8 * P), 1, "overlaps"),
+    (dict(slots=8 * P), 1, "overlaps"), (dict(N=1 << 20, ns=1 << 20), 1, "2^21"),
 ])
 def test_decode_refusals(lib, kw, status, msg):
     assert dec(lib, **kw) == status
@@ -97,6 +97,7 @@ def bwd(lib, **kw):
     (dict(dO=None), 1, "dO is NULL"), (dict(dq=None), 1, "dq is NULL"), (dict(dk_=7 * P), 1, "overlaps"),
     (dict(dq=P), 1, "overlaps"), (dict(ws=4 * P), 1, "overlaps"), (dict(dg=10 * P + 2), 1, "aligned"),
     (dict(dS0=12 * P + 4), 1, "aligned"), (dict(Hk=2, Hv=3), 1, "multiple"), (dict(dt=2), 1, "in_dtype"),
+    (dict(N=1 << 30, dk=64, dv=64), 1, "2^23"), (dict(n=1 << 20, N=1 << 20), 1, "2^21"),
 ])
 def test_bwd_refusals(lib, kw, status, msg):
     assert bwd(lib, **kw) == status

@@ -416,6 +416,13 @@ def test_far_offsets():
     o1, S1 = m.gdr_fwd_chunked(c(q), c(k), c(v), c(g), c(beta))
     torch.cuda.synchronize()
     assert v.numel() > 2 ** 31 and torch.equal(o[at], o1) and torch.equal(S[-1:], S1)
+    del o, S
+    dO = v.flip(0).contiguous()
+    far = m.gdr_bwd_chunked(q, k, v, g, beta, dO, cu_seqlens=cu)
+    alone = m.gdr_bwd_chunked(c(q), c(k), c(v), c(g), c(beta), c(dO))
+    torch.cuda.synchronize()
+    for name, x, y in zip(GRADS, far, alone):
+        assert torch.equal(x[-1:] if name == "dS0" else x[at], y), name
 
 
 # ------------------------------------------------------------------ refusals
