@@ -92,23 +92,14 @@ __device__ __forceinline__ f32x4 mma_by_parts(const Parts<NS> &a, bf16x8 b, f32x
     return c;
 }
 
-// Products over 16 rows with both operands in three parts: the six products
-// of at least 2^-24 fill three 32-slot products,
-//   [Ah | Al] [Bl | Bh],  [Am | Am] [Bh | Bm],  [Ah | Ah] [Bh | Bm].
-struct Half {
-    bf16x8 hm, lh;
-};
-__device__ __forceinline__ Half split_half(f32x4 x, const Eye &eye, u32x2 &h, u32x2 &m, u32x2 &l)
+// the three parts of a lane's four values of one tile
+__device__ __forceinline__ void split3(f32x4 x, const Eye &eye, u32x2 (&p)[3])
 {
-    h = pack4(x);
-    x = mma(eye.a, join(h, h), x);
-    m = pack4(x);
-    Half r;
-    r.hm = join(h, m);
-    x = mma(eye.b, r.hm, x);
-    l = pack4(x);
-    r.lh = join(l, h);
-    return r;
+    p[0] = pack4(x);
+    x = mma(eye.a, join(p[0], p[0]), x);
+    p[1] = pack4(x);
+    x = mma(eye.a, join(p[1], p[1]), x);
+    p[2] = pack4(x);
 }
 
 __device__ __forceinline__ bf16x8 lds8(const void *p) { return *static_cast<const bf16x8 *>(p); }
@@ -130,8 +121,7 @@ struct Swz {
 __device__ __forceinline__ u32x2 lds_tr(const bf16 *p)
 {
     typedef __attribute__((address_space(3))) s16x4 lds_t;
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_t *)p));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)p));
 }
 __device__ __forceinline__ f32x4 widen(u32x2 w)
 {

@@ -46,8 +46,8 @@ struct Stage {
     Block Tone[2];
     bf16x8 Tpair[2][3][WAVE];
     float eG[C], eR[C];                          // e^G; b e^{G_C - G} (sweep: e^{G_C - G})
-    float eGs[C], eGb[C];                        // scale e^G; (sweep) b e^G
-    float beta[C];
+    float eGs[C];                                // scale e^G
+    float eGb[C], beta[C];                       // b e^G and b, in the sweep
     float gamma;
 };
 
@@ -152,16 +152,15 @@ struct Producer {
     // left operands in three parts from a lane's four values of one tile
     static __device__ __forceinline__ void put_block(Block &t, int lane, f32x4 x, const Eye &eye)
     {
-        u32x2 h, m, l;
-        split_half(x, eye, h, m, l);
-        t.p[0][lane] = h;
-        t.p[1][lane] = m;
-        t.p[2][lane] = l;
+        u32x2 p[3];
+        split3(x, eye, p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) t.p[i][lane] = p[i];
     }
     static __device__ __forceinline__ void put_side(bf16x8 (*t)[WAVE], int lane, int side, f32x4 x, const Eye &eye)
     {
         u32x2 p[3];
-        split_half(x, eye, p[0], p[1], p[2]);
+        split3(x, eye, p);
 #pragma unroll
         for (int i = 0; i < 3; ++i) reinterpret_cast<u32x2 *>(&t[i][lane])[side] = p[i];
     }
@@ -226,10 +225,9 @@ struct Producer {
         asm volatile("" ::: "memory");
         // X = -T_L A T_R for the off-diagonal tile (lane block L, row block R),
         // transposed and on the fp32 matrix cores: W = A^T T_L^T, X^T = -T_R^T W
-        const float *tl = OL % 2 ? s1 : s0, *tr = OL % 2 ? s0 : s1;
+        const float *tr = OL % 2 ? s0 : s1;
         const f32x4 t0 = ld4f(&s0[16 * ln + 4 * lg]), t1 = ld4f(&s1[16 * ln + 4 * lg]);
         const f32x4 bl = OL % 2 ? t1 : t0;
-        (void)tl;
         f32x4 w = {0.f, 0.f, 0.f, 0.f}, x = w;
         float ac[4], tc[4];
 #pragma unroll
@@ -265,9 +263,11 @@ struct Producer {
             const float eg = kda::fast_exp2(gh);
             st.eG[lane] = eg;
             st.eGs[lane] = scale * eg;
-            st.eGb[lane] = beta * eg;
             st.eR[lane] = SW ? er : er * beta;
-            st.beta[lane] = beta;
+            if constexpr (SW) {
+                st.eGb[lane] = beta * eg;
+                st.beta[lane] = beta;
+            }
             if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
         }
         // K and Q blocks and the values to the stage
@@ -445,8 +445,7 @@ struct Consumer {
 
     // row tiles t0 .. t1 of S += K^T (or Q^T) u over the tokens 32 s .. of the chunk
     template <int NS>
-    __device__ __forceinline__ void update(const bf16 *M, const Parts<NS> &u, int s, int t0,
-                                           int t1, int ln, int lg)
+    __device__ __forceinline__ void update(const bf16 *M, const Parts<NS> &u, int s, int t0, int t1, int ln, int lg)
     {
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -569,11 +568,10 @@ struct Consumer {
                 O[t] = mma(rh, ph, O[t]);
             }
         };
-        const Parts<2> r01h = {{r01.p[0], r01.p[1]}};
-        pr(0, 0, r01h.p[0], r01h.p[1]);
-        pr(1, 1, r01h.p[0], r01h.p[1]);
-        pr(2, 2, r01h.p[0], r01h.p[1]);
-        pr(4, 3, r01h.p[0], r01h.p[1]);
+        pr(0, 0, r01.p[0], r01.p[1]);
+        pr(1, 1, r01.p[0], r01.p[1]);
+        pr(2, 2, r01.p[0], r01.p[1]);
+        pr(4, 3, r01.p[0], r01.p[1]);
         const Parts<3> u1 = split_pair<3>(er2 * R[2], er3 * R[3], eye);
         const Parts<2> r23 = MODE == FWD ? split_pair<2>(R[2], R[3], eye) : Parts<2>{};
         pr(3, 2, r23.p[0], r23.p[1]);

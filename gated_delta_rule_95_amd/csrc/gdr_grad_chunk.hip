@@ -4,10 +4,11 @@
 //
 // A workgroup takes a (chunk, key head) and its value heads one after
 // another, so that shared heads' gradients are summed in registers, in one
-// order; each of its d_k / 16 waves owns 16 key channels of dq and dk.  Everything is formed transposed, result rows = key channels and
-// columns = tokens: the state's operands come straight from memory in the
-// order the sweeps left them, decays and masks are per-lane scalars, and dq,
-// dk go out 8 bytes at a time.
+// order; each of its d_k / 16 waves owns 16 key channels of dq and dk.
+// Everything is formed transposed, result rows = key channels and columns =
+// tokens: the state's operands come straight from memory in the order the
+// sweeps left them, decays and masks are per-lane scalars, and dq, dk go out
+// 8 bytes at a time.
 //
 // Operands of the products that dg depends on are held in three bf16 parts
 // and multiplied without the parts' products below 2^-24 (with two parts dg
@@ -35,7 +36,7 @@ struct alignas(16) GradSmem {
         bf16 rows[7][C * SW];                    // dO; U, Yb in three parts each
         bf16 mat[4][C * C];                      // dP hi, dP lo, dN hi, dN lo   [i][j]
     };
-    float G[2][C], a[NW][C], b[NW][C], e[8][C], rev[C], ls[NW];
+    float G[2][C], a[NW][C], b[NW][C], e[NW][C], rev[C], ls[NW];
 };
 
 __device__ __forceinline__ bool find_chunk(const SeqArgs &s, int64_t slot, int &n, int &c)
@@ -152,12 +153,22 @@ void gdr_grad_chunk_kernel(Args a)
     const Seq sq = seq_of(a.seq, n);
     const int64_t tok = __builtin_amdgcn_readfirstlane(sq.bos + c * C);
     const int nt = __builtin_amdgcn_readfirstlane(sq.len - c * C < C ? sq.len - c * C : C);
-    // Rows of the two C x C matrices: kind 0 is dP (with Q K^T), 1 is dN (with
-    // K K^T); eight waves take one row block of one kind each, four waves one
-    // of both.  Block rows are formed whole: the longest sets the time.
-    constexpr int NKD = 8 / NW;
-    const auto kind_of = [&](int i) { return NKD == 2 ? i : wave >> 2; };
-    const auto block_of = [&](int i) { return kind_of(i) ? 3 - (wave & 3) : wave & 3; };
+    // The 16 x 16 tiles on and below the diagonal of the two C x C matrices,
+    // dP (with Q K^T) and dN (with K K^T), in the order (0, 0), (1, 0), (1, 1),
+    // ...  A tile of dN costs six products a step, one of dP three.  Eight
+    // waves: 0 .. 4 take a tile of both and one more of dP, 5 .. 7 two of dN
+    // (7: one); four waves: two or three tiles of both.
+    constexpr int NS = NW == 8 ? 2 : 3;
+    int row_block[NS], col_block[NS];
+    bool in_p[NS], in_n[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int t = NW == 4 ? wave + 4 * i : wave < 5 ? wave + 5 * i : 2 * wave - 5 + i;
+        row_block[i] = (t > 0) + (t > 2) + (t > 5);
+        col_block[i] = t - row_block[i] * (row_block[i] + 1) / 2;
+        in_p[i] = NW == 4 ? t < 10 : wave < 5;
+        in_n[i] = NW == 4 ? t < 10 : wave < 5 ? i == 0 : t < 10;
+    }
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     const Eye eye = make_eye(lane);
     // rows of dO, R and Ub for one stage of value columns of one head, a
@@ -206,7 +217,7 @@ void gdr_grad_chunk_kernel(Args a)
             s.G[1][lane] = (float)(G - (double)gh);
         }
         // products over the value columns
-        f32x4 mat[NKD][4] = {}, x1[4] = {}, x2[4] = {}, x3[4] = {}, ls = zero;
+        f32x4 mp[NS] = {}, mn[NS] = {}, x1[4] = {}, x2[4] = {}, x3[4] = {}, ls = zero;
         float db = 0.f;
         const int64_t st = (slot * a.Hv + hv) * (int64_t)(DK * DV / 4) + wave * VS * 2 * WAVE + lane;     // in f32x4
         const f32x4 *Sc = reinterpret_cast<const f32x4 *>(a.Sc) + st, *Lc = reinterpret_cast<const f32x4 *>(a.Lc) + st;
@@ -235,19 +246,16 @@ void gdr_grad_chunk_kernel(Args a)
                     const int at = Swz<SW>::at(row, vc);
                     return Parts<3>{{lds8(&s.rows[first][at]), lds8(&s.rows[first + 1][at]), lds8(&s.rows[first + 2][at])}};
                 };
-                const int t0=(v0/32+ks)*2*WAVE; const Parts<3> S = split8(__builtin_nontemporal_load(Sc + t0), __builtin_nontemporal_load(Sc + t0 + WAVE)), L = split8(__builtin_nontemporal_load(Lc + t0), __builtin_nontemporal_load(Lc + t0 + WAVE));
+                const int t0 = (v0 / 32 + ks) * 2 * WAVE;
+                const Parts<3> S = split8(__builtin_nontemporal_load(Sc + t0), __builtin_nontemporal_load(Sc + t0 + WAVE));
+                const Parts<3> L = split8(__builtin_nontemporal_load(Lc + t0), __builtin_nontemporal_load(Lc + t0 + WAVE));
 #pragma unroll
-                for (int i = 0; i < NKD; ++i) {
-                    const int own = 16 * block_of(i) + ln;
-                    if (kind_of(i) == 0) {
-                        const bf16x8 x = row8<SW>(s.rows[0], own, vc);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) mat[i][b] = mma_by_parts<3>(rows3(1, 16 * b + ln), x, mat[i][b]);
-                    } else {
-                        const Parts<3> x = rows3(4, own);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) mat[i][b] = mma33(rows3(1, 16 * b + ln), x, mat[i][b]);
-                    }
+                for (int i = 0; i < NS; ++i) {
+                    if (!in_p[i] && !in_n[i]) continue;
+                    const int own = 16 * row_block[i] + ln;
+                    const Parts<3> U = rows3(1, 16 * col_block[i] + ln);
+                    if (in_p[i]) mp[i] = mma_by_parts<3>(U, row8<SW>(s.rows[0], own, vc), mp[i]);
+                    if (in_n[i]) mn[i] = mma33(U, rows3(4, own), mn[i]);
                 }
                 ls = mma33(S, L, ls);            // its diagonal is wanted
                 __builtin_amdgcn_sched_barrier(0);
@@ -302,55 +310,95 @@ void gdr_grad_chunk_kernel(Args a)
         }
         __syncthreads();                         // the staged rows are read
         // the chunk's own pairs: lane row i of the row block, rows j of the tile
+        fresh();
+        if (tid < 256) {                         // tiles above the diagonal that are read below: zeros
+            const int y = tid / 2 % 32, x = y + (y & 16);
+            *reinterpret_cast<bf16x8 *>(&s.mat[tid / 64][Swz<C>::at(x, (x & 32) + 16 + 8 * (tid % 2))]) = bf16x8{};
+        }
+        float es[4] = {};
+        bf16x8 ones, tri;                        // [1 | 1], [j < t | j < t]
 #pragma unroll
-        for (int kd = 0; kd < NKD; ++kd) {
-            fresh();
-            const int kind = kind_of(kd), rb = block_of(kd), i = 16 * rb + ln;
+        for (int x = 0; x < 8; ++x) {
+            ones[x] = (bf16)1.f;
+            tri[x] = 4 * lg + (x & 3) < ln ? (bf16)1.f : (bf16)0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < NS; ++x) {
+            if (!in_p[x] && !in_n[x]) continue;
+            const int rb = row_block[x], cb = col_block[x], i = 16 * rb + ln, j = 16 * cb + 4 * lg;
+            const f32x4 gjh = *reinterpret_cast<const f32x4 *>(&s.G[0][j]), gjl = *reinterpret_cast<const f32x4 *>(&s.G[1][j]);
             const float gih = s.G[0][i], gil = s.G[1][i];
-            f32x4 (&E)[4] = mat[kd];
+            f32x4 pq = zero, pk = zero, E = zero, d;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                f32x4 pair = zero;
-                const bf16 *x = kind == 0 ? s.q : s.k;
+            for (int ks = 0; ks < KS; ++ks) {
+                const bf16x8 kj = row8<DK>(s.k, 16 * cb + ln, 32 * ks + 8 * lg);
+                if (in_p[x]) pq = mma(kj, row8<DK>(s.q, i, 32 * ks + 8 * lg), pq);
+                if (in_n[x]) pk = mma(kj, row8<DK>(s.k, i, 32 * ks + 8 * lg), pk);
+            }
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    pair = mma(row8<DK>(s.k, 16 * b + ln, 32 * ks + 8 * lg), row8<DK>(x, i, 32 * ks + 8 * lg), pair);
-                const int j = 16 * b + 4 * lg;
-                f32x4 v;
+            for (int e = 0; e < 4; ++e) d[e] = j + e <= i ? kda::fast_exp2((gih - gjh[e]) + (gil - gjl[e])) : 0.f;
+            const auto put = [&](int m, f32x4 v) {
+                const u32x2 vh = pack4(v);
+                const int at = Swz<C>::at(i, j);
+                *reinterpret_cast<u32x2 *>(&s.mat[m][at]) = vh;
+                *reinterpret_cast<u32x2 *>(&s.mat[m + 1][at]) = pack4(v - widen(vh));
+            };
+            if (in_p[x]) {
+                f32x4 v = (a.scale * d) * mp[x];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float d = kda::fast_exp2((gih - s.G[0][j + e]) + (gil - s.G[1][j + e]));
-                    v[e] = (kind == 0 ? a.scale : -1.f) * d * mat[kd][b][e];
-                    if (kind == 0 ? j + e > i : j + e >= i) v[e] = 0.f;
-                    E[b][e] = j + e < i ? v[e] * pair[e] : 0.f;
+                    v[e] = j + e <= i ? v[e] : 0.f;
+                    E[e] = j + e < i ? v[e] * pq[e] : 0.f;
                 }
-                const u32x2 vh = pack4(v), vl = pack4(v - widen(vh));
-                const int at = Swz<C>::at(i, j);
-                *reinterpret_cast<u32x2 *>(&s.mat[2 * kind][at]) = vh;
-                *reinterpret_cast<u32x2 *>(&s.mat[2 * kind + 1][at]) = vl;
+                put(0, v);
             }
-            // sum over j < t <= i of E_ij: [j < t] E by products with zeros
-            // and ones, then the rows i >= t
-            const Parts<3> e01 = split_pair<3>(E[0], E[1], eye), e23 = split_pair<3>(E[2], E[3], eye);
-            bf16x8 ones, tri0, tri1;             // all; [j < t | 0]; [1 | j < t]
+            if (in_n[x]) {
+                f32x4 v = -d * mn[x];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const bf16 lt = 4 * lg + (x & 3) < ln ? (bf16)1.f : (bf16)0.f;
-                ones[x] = (bf16)1.f;
-                tri0[x] = x < 4 ? lt : (bf16)0.f;
-                tri1[x] = x < 4 ? (bf16)1.f : lt;
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = j + e < i ? v[e] : 0.f;
+                    E[e] += j + e < i ? v[e] * pk[e] : 0.f;
+                }
+                put(2, v);
             }
+            // sum over j < t <= i of E_ij: E [j < t] by products with zeros
+            // and ones (rows i of the tile, a lane's column t), then the rows
+            // i >= t
+            u32x2 ep[3];
+            split3(E, eye, ep);
+            const bf16x8 hm = join(ep[0], ep[1]), lo = join(ep[2], u32x2{0, 0});
+            const f32x4 wt = mma(hm, tri, mma(lo, tri, zero)), wo = mma(hm, ones, mma(lo, ones, zero));
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
-                f32x4 w = mma_parts<3>(tb == 0 ? tri0 : tb == 1 ? tri1 : ones, e01, zero);
-                if (tb >= 2) w = mma_parts<3>(tb == 2 ? tri0 : tri1, e23, w);
+                if (tb < cb || tb > rb) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * tb + 4 * lg + e;
-                    const float x = sum16(i >= t ? w[e] : 0.f);
-                    if (ln == 0) s.e[4 * kind + rb][t] = x;
+                    const float w = tb == cb ? wt[e] : wo[e];
+                    es[tb] += tb < rb || 4 * lg + e >= ln ? w : 0.f;
                 }
             }
+        }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            const float x = sum_groups(es[tb]);
+            if (lg == 0) s.e[wave][16 * tb + ln] = x;
+        }
+        // the last wave has the least to do here: the sums over the chunk that
+        // do not need the pairs
+        float dg = 0.f;
+        if (wave == NW - 1) {
+            const auto at = [&](const float (*x)[C], int r) {
+                float y = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) y += x[w][r];
+                return y;
+            };
+            s.rev[lane] = scan64<float>(at(s.a, C - 1 - lane));
+            const float before = scan64<float>(lane ? at(s.b, lane - 1) : 0.f);
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) l += s.ls[w];
+            dg = s.rev[C - 1 - lane] + before + kda::fast_exp2(s.G[0][C - 1]) * l;
         }
         __syncthreads();
         // products with the chunk's own rows
@@ -374,24 +422,11 @@ void gdr_grad_chunk_kernel(Args a)
                 }
             }
         }
-        if (wave == 0) {
-            const auto at = [&](const float (*x)[C], int r) {
-                float y = 0.f;
+        if (wave == NW - 1) {
 #pragma unroll
-                for (int w = 0; w < NW; ++w) y += x[w][r];
-                return y;
-            };
-            s.rev[lane] = scan64<float>(at(s.a, C - 1 - lane));
-            const float before = scan64<float>(lane ? at(s.b, lane - 1) : 0.f);
-            float e = 0.f, l = 0.f;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) e += s.e[r][lane];
-#pragma unroll
-            for (int w = 0; w < NW; ++w) l += s.ls[w];
-            if (lane < nt)
-                a.dg[(tok + lane) * a.Hv + hv] = s.rev[C - 1 - lane] + before + e + kda::fast_exp2(s.G[0][C - 1]) * l;
+            for (int w = 0; w < NW; ++w) dg += s.e[w][lane];
+            if (lane < nt) a.dg[(tok + lane) * a.Hv + hv] = dg;
         }
-        if (h + 1 < grp) __syncthreads();        // the sums are read
     }
     const int rb = a.Hk * DK * 2;
     const rsrc_t oq = make_rsrc(static_cast<char *>(a.dq) + tok * rb, nt * rb), ok = make_rsrc(static_cast<char *>(a.dkey) + tok * rb, nt * rb);
