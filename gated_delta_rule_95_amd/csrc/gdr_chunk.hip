@@ -36,9 +36,8 @@ struct Block {
 
 template <int DK, int NC, int MODE>
 struct Stage {
-    static constexpr int LV = 16 * NC + 8;
     static constexpr int PP = MODE == SWEEP ? 3 : 2;
-    bf16 K[C * DK], Q[C * DK], V[C][LV];         // K, Q by Swz; V: v, or dO in the sweep
+    bf16 K[C * DK], Q[C * DK];                   // by Swz
     // operands of 1 KiB in lane order
     bf16x8 P[PP][MODE == KEEP ? 1 : 6][WAVE];   // [part][0, 1, 2a, 2b, 3a, 3b]
     bf16x8 Apair[2][3][WAVE];                    // a block of rows against two of columns
@@ -51,9 +50,17 @@ struct Stage {
     float gamma;
 };
 
+template <int NC>
+struct Values {
+    bf16 x[C][16 * NC + 8];
+};
+
 template <int DK, int NC, int MODE>
 struct alignas(16) Smem {
     Stage<DK, NC, MODE> st[2];
+    // v, or dO in the sweep: read before a chunk's first barrier, written
+    // behind it, so one is enough
+    Values<NC> V;
     float G[4][3][C];                            // per producer: G hi, G lo, beta
 };
 
@@ -248,7 +255,7 @@ struct Producer {
     // builds the stage; `next` requests the chunk after it once this one's
     // rows are in the stage
     template <typename F>
-    __device__ __forceinline__ void build(St &st, float (*gp)[C], const Eye &eye, float scale,
+    __device__ __forceinline__ void build(St &st, Values<NC> &values, float (*gp)[C], const Eye &eye, float scale,
                                           int ln, int lg, int ptid, F next)
     {
         int lane = ln + 16 * lg;
@@ -270,20 +277,20 @@ struct Producer {
             }
             if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
         }
-        // K and Q blocks and the values to the stage
+        // K and Q blocks to the stage
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int at = Swz<DK>::at(16 * W + ln, 32 * s + 8 * lg);
             *reinterpret_cast<bf16x8 *>(&st.K[at]) = R::bf(kw[s]);
             if constexpr (MODE != KEEP) *reinterpret_cast<bf16x8 *>(&st.Q[at]) = R::bf(qw[s]);
         }
+        __syncthreads();                 // rows of the chunk are in the stage, and the values of the one before read
         {
             const int row = ptid / 4, c = (ptid % 4) * (4 * NC);
 #pragma unroll
             for (int i = 0; i < VL; ++i)
-                *reinterpret_cast<bf16x8 *>(&st.V[row][c + 8 * i]) = SW ? Rows<bf16>::bf(v[i]) : R::bf(v8[i]);
+                *reinterpret_cast<bf16x8 *>(&values.x[row][c + 8 * i]) = SW ? Rows<bf16>::bf(v[i]) : R::bf(v8[i]);
         }
-        __syncthreads();                 // rows of the chunk are in the stage
         next();
         loosen<NC == 8>(ln, lg);
         const auto rows = [&](const bf16 *x, int b, int s) { return lds8(&x[Swz<DK>::at(16 * b + ln, 32 * s + 8 * lg)]); };
@@ -389,7 +396,7 @@ struct Producer {
         request(0);
         for (int c = 0; c < chunks; ++c) {
             loosen<NC == 8>(ln, lg);
-            p.build(sm.st[c & 1], sm.G[W], eye, a.scale, ln, lg, ptid, [&] { request(c + 1); });
+            p.build(sm.st[c & 1], sm.V, sm.G[W], eye, a.scale, ln, lg, ptid, [&] { request(c + 1); });
             __syncthreads();
         }
     }
@@ -480,7 +487,7 @@ struct Consumer {
 
     // out: buffer of the chunk's rows of o (R); off: this lane's byte in block
     // 0; keep: where the entry state goes (KEEP)
-    __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Eye &eye, int w, int ln, int lg,
+    __device__ __forceinline__ void forward(const Stage<DK, NC, MODE> &st, const Values<NC> &values, const Eye &eye, int w, int ln, int lg,
                                             rsrc_t out, int row_bytes, int off, float *keep, int dv, int cw,
                                             bool more)
     {
@@ -496,7 +503,7 @@ struct Consumer {
         f32x4 eg[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            vt[t] = lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
+            vt[t] = lds_tr(&values.x[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
             eg[t] = ld4f(&st.eG[16 * t + 4 * lg]);
         }
         const PairRegs T0(st.Tone[0], lane, false), T1(st.Tpair[0], lane);
@@ -589,7 +596,7 @@ struct Consumer {
 
     // out: buffer of the chunk's rows of Ub; offs: this lane's byte in block
     // 0 of it and of dv; keep: where the exit cotangent goes
-    __device__ __forceinline__ void sweep(const Stage<DK, NC, MODE> &st, const Eye &eye, int w, int ln, int lg, rsrc_t out,
+    __device__ __forceinline__ void sweep(const Stage<DK, NC, MODE> &st, const Values<NC> &values, const Eye &eye, int w, int ln, int lg, rsrc_t out,
                                           int row_bytes, int off, rsrc_t dval, int vrow_bytes, int voff, float *keep, int dv,
                                           int cw, bool more)
     {
@@ -599,7 +606,7 @@ struct Consumer {
         f32x4 er[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            d[t] = lds_tr(&st.V[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
+            d[t] = lds_tr(&values.x[16 * t + 4 * lg + (ln >> 2)][16 * w + 4 * (ln & 3)]);
             er[t] = ld4f(&st.eR[16 * t + 4 * lg]);
         }
         const PairRegs T3(st.Tone[1], lane, true), T2(st.Tpair[1], lane);
@@ -779,9 +786,9 @@ __device__ __forceinline__ void chain_pass(const Args &a, Smem<DK, NC, MODE> &sm
         float *keep = border + (slot * a.Hv + hv) * DK * a.dv;
         if constexpr (MODE == SWEEP) {
             const rsrc_t dval = make_rsrc(static_cast<char *>(a.dval) + tok * (rb / 2), nrow * (rb / 2));
-            q.sweep(sm.st[c & 1], eye, wave, ln, lg, out, rb, e0 * 4, dval, rb / 2, e0 * 2, keep, a.dv, cw, c + 1 < chunks);
+            q.sweep(sm.st[c & 1], sm.V, eye, wave, ln, lg, out, rb, e0 * 4, dval, rb / 2, e0 * 2, keep, a.dv, cw, c + 1 < chunks);
         } else
-            q.forward(sm.st[c & 1], eye, wave, ln, lg, out, rb, e0 * es, keep, a.dv, cw, c + 1 < chunks);
+            q.forward(sm.st[c & 1], sm.V, eye, wave, ln, lg, out, rb, e0 * es, keep, a.dv, cw, c + 1 < chunks);
     }
     float *fin = MODE == FWD ? a.S_T : MODE == SWEEP ? a.dS0 : nullptr;
     if (fin) store_state<DK / 16>(q.S, fin + st, a.dv, lg);
