@@ -74,6 +74,22 @@ __device__ __forceinline__ Seq seq_of(const SeqArgs &s, int n)
 // 64 such values keep far more than single precision in their differences
 __device__ __forceinline__ float floor_g(float g) { return g < -1e4f ? -1e4f : g; }
 
+// the upper 32 lanes of a change places with the lower 32 of b
+__device__ __forceinline__ void swap32(float &a, float &b)
+{
+    uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\ts_nop 1" : "+v"(x), "+v"(y));
+    a = __uint_as_float(x);
+    b = __uint_as_float(y);
+}
+// the same with odd rows of 16 lanes of a and even ones of b
+__device__ __forceinline__ void swap16(float &a, float &b)
+{
+    uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\ts_nop 1" : "+v"(x), "+v"(y));
+    a = __uint_as_float(x);
+    b = __uint_as_float(y);
+}
 // sum over the lanes of equal lane % 16
 __device__ __forceinline__ float sum_groups(float x)
 {
