@@ -154,6 +154,20 @@ def test_gates_and_shared_heads(gates, Hk, Hv, dtype):
         close(x, y, name)
 
 
+# 80 and 320 chains: other tilings of the state than those for few chains
+@pytest.mark.parametrize("dtype,dk,dv,Hv", [(F32, 128, 128, 4), (F32, 128, 128, 16), (F32, 64, 128, 16),
+                                            (F32, 32, 128, 16), (F32, 64, 16, 16), (BF, 128, 128, 16),
+                                            (BF, 64, 128, 16), (BF, 128, 64, 16)])
+def test_many_chains(dtype, dk, dv, Hv):
+    b = make(907 + dk + dv, [33, 1, 70, 0, 16] * 4, 2, Hv, dk, dv, dtype)
+    o, S = fwd(b)
+    ro, rS = oracle_fwd(b)
+    close(o, ro, "o")
+    close(S, rS, "S_T")
+    for name, x, y in zip(GRADS, bwd(b), oracle_bwd(b)):
+        close(x, y, name)
+
+
 @pytest.mark.parametrize("dk,dv", [(128, 128), (32, 16)])
 def test_longer_sequences_and_small_cotangents(dk, dv):
     """Many chunks, and the 1e-6 cotangents that a mean over tokens gives."""
@@ -349,6 +363,55 @@ def test_decode(dk, dv, dtype, N, Hk, Hv):
     close(S, ref_S, "S", 1e-6)
     left = [i for i in range(N + 3) if i not in slots.tolist()]
     assert torch.equal(S[left], pool[left])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_captured_decode_replays(dtype):
+    """A captured step, replayed on new tokens and other slots, with eager
+    steps on another pool between the replays."""
+    m = lib()
+    b = make(43, [1] * 5, 2, 4, 128, 64, dtype)
+    slots = torch.tensor([4, 0, 6, 1, 3], dtype=torch.int32, device="cuda")
+    pool = torch.randn(7, 4, 128, 64, device="cuda")
+    eager, o = pool.clone(), torch.empty_like(b["v"])
+    run = lambda S, **kw: m.gdr_decode_step(b["q"], b["k"], b["v"], b["g"], b["beta"], S, slots=slots, **kw)  # noqa: E731
+    run(pool.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(pool, o=o)
+    for seed in (44, 45, 46):
+        new = make(seed, [1] * 5, 2, 4, 128, 64, dtype)
+        for x in ("q", "k", "v", "g", "beta"):
+            b[x].copy_(new[x])
+        slots.copy_((slots + 2) % 8)                      # some replays pad a row
+        want = run(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(pool, eager)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_two_streams_at_once(dtype):
+    """Calls on two streams, each with its own workspace, change nothing in
+    each other's results."""
+    sets = [make(61 + i, [70, 65, 3], 2, 4, 64, 128, dtype) for i in range(2)]
+    want = [fwd(b) + bwd(b) for b in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for b, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                args = [b[x] for x in ("q", "k", "v", "g", "beta")]
+                kw = dict(S0=b["S0"], cu_seqlens=b["cu"], scale=b["scale"])
+                got.append(lib().gdr_fwd_chunked(*args, **kw)
+                           + lib().gdr_bwd_chunked(*args, b["dO"], dS_T=b["dS_T"], **kw))
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        for y, z in zip(x, want[i % 2]):
+            assert torch.equal(y, z)
 
 
 def test_decode_without_slots_continues_a_prefill():
