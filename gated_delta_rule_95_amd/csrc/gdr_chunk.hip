@@ -20,6 +20,17 @@
 // build the next chunk's left operands in the other half of the LDS meanwhile,
 // two barriers a chunk: two of them form and invert a diagonal block of 32
 // each, two the rest of K K^T and K Q^T, without a word among them.
+//
+// Bound by the chain of chunks: a chunk's products wait for one another, most
+// of all in the substitution, and the matrix cores are busy for 45% of the
+// forward's time (37% of the backward's two passes).  Forward, 4 sequences of
+// 4096 tokens, 32 heads of 128 x 128: 255-275 us (1.6 TB/s of inputs, outputs
+// and states; the consumers by themselves 216 us, the producers 178); 13 ragged
+// sequences, 20011 tokens: 280 us.  Keeping forward and sweep of the former:
+// 0.70 ms for 2.3 GB moved.  The substitution over blocks of 16 tokens took 290
+// and 302 us; operands straight from global memory in place of the LDS twice
+// the time (a load of 64 scattered pieces takes 900 cycles and more to issue);
+// one bf16 part of S and R in o saved 5% and missed repeated keys by 4e-3.
 #include "gdr_chunk.h"
 
 namespace gdr {
@@ -58,8 +69,9 @@ struct Values {
 template <int DK, int NC, int MODE>
 struct alignas(16) Smem {
     Stage<DK, NC, MODE> st[2];
-    // v, or dO in the sweep: read before a chunk's first barrier, written
-    // behind it, so one is enough
+    // v, or dO in the sweep: read before a chunk's first barrier and the next
+    // written behind it, so one is enough (two measured 2% slower in a ragged
+    // batch)
     Values<NC> V;
     float G[4][3][C];                            // per producer: G hi, G lo, beta
 };
@@ -93,17 +105,6 @@ __device__ __forceinline__ double last_lane(double x)
     const uint64_t b = __builtin_bit_cast(uint64_t, x);
     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, 63), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), 63);
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-
-// Cuts what follows loose from the lane indices before it: addresses and masks
-// made of them are then formed where they are used, and not kept in registers
-// across the chunks.  With twelve waves (168 registers each) 2 registers are
-// spilled in place of 213; with eight there is room, and forming them again
-// would cost 9%.
-template <bool ON>
-__device__ __forceinline__ void loosen(int &ln, int &lg)
-{
-    if constexpr (ON) asm volatile("" : "+v"(ln), "+v"(lg));
 }
 
 // Producer W of four.  A tile pairs the lane tokens of one block of 16 with the
@@ -258,7 +259,7 @@ struct Producer {
     __device__ __forceinline__ void build(St &st, Values<NC> &values, float (*gp)[C], const Eye &eye, float scale,
                                           int ln, int lg, int ptid, F next)
     {
-        int lane = ln + 16 * lg;
+        const int lane = ln + 16 * lg;
         // cumulative log2-decay in double, held as two floats
         const double G = scan64((double)floor_g(g) * (double)LOG2E), Gend = last_lane(G);
         const float gh = (float)G;
@@ -292,12 +293,7 @@ struct Producer {
                 *reinterpret_cast<bf16x8 *>(&values.x[row][c + 8 * i]) = SW ? Rows<bf16>::bf(v[i]) : R::bf(v8[i]);
         }
         next();
-        loosen<NC == 8>(ln, lg);
         const auto rows = [&](const bf16 *x, int b, int s) { return lds8(&x[Swz<DK>::at(16 * b + ln, 32 * s + 8 * lg)]); };
-        // with few registers, the reads of one step at a time
-        const auto step_end = [] {
-            if constexpr (NC == 8) __builtin_amdgcn_sched_barrier(0);
-        };
         if constexpr (W % 2) {
             // the three tiles of the diagonal block of 32
             f32x4 d0 = {}, d1 = {}, off = {};
@@ -307,9 +303,7 @@ struct Producer {
                 d0 = mma(k0, k0, d0);
                 d1 = mma(k1, k1, d1);
                 off = SW ? mma(k1, k0, off) : mma(k0, k1, off);
-                step_end();
             }
-            loosen<NC == 8>(ln, lg);
             const int x0 = 32 * PR + ln, y0 = 32 * PR + 4 * lg;
             const f32x4 b0 = ld4f(&gp[2][y0]), b1 = ld4f(&gp[2][y0 + 16]);
             d0 = decays(gp, x0, y0, b0 * d0);
@@ -340,10 +334,7 @@ struct Producer {
                     if (MODE != KEEP && reaches(L0, b)) q0[b] = mma(rb, l0, q0[b]);
                     if (MODE != KEEP && reaches(L1, b)) q1[b] = mma(rb, l1, q1[b]);
                 }
-                step_end();
             }
-            loosen<NC == 8>(ln, lg);
-            lane = ln + 16 * lg;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int y = 16 * b + 4 * lg;
@@ -382,7 +373,7 @@ struct Producer {
     static __device__ __forceinline__ void run(const Args &a, Smem<DK, NC, MODE> &sm, int chunks, Tok where, int hk, int hv,
                                                int col, int lane, int ptid)
     {
-        int ln = lane % 16, lg = lane / 16;
+        const int ln = lane % 16, lg = lane / 16;
         const Eye eye = make_eye(lane);
         Producer p;
         const auto request = [&](int c) {
@@ -395,7 +386,6 @@ struct Producer {
         };
         request(0);
         for (int c = 0; c < chunks; ++c) {
-            loosen<NC == 8>(ln, lg);
             p.build(sm.st[c & 1], sm.V, sm.G[W], eye, a.scale, ln, lg, ptid, [&] { request(c + 1); });
             __syncthreads();
         }

@@ -12,6 +12,10 @@
 //
 // Every term of dg carries the decays it passes through, so none cancels
 // against another however fast the decay is.
+//
+// Bound by latency: a workgroup passes through the phases above once for each
+// value head, with some tens of products a wave in each.  fp32, 600 tokens, 4
+// value heads of 32 x 64: 23.5 us for 40 workgroups.
 #include "gdr_device.h"
 
 namespace gdr {

@@ -9,7 +9,8 @@
 // backward reads is exact in its matrix operands.
 // A copy in its cost: 2 + 1 + 1/32 bytes an element each way.  One thread
 // takes eight elements (16 bytes of bf16); a block is four neighbouring
-// lanes (two at d = 16).
+// lanes (two at d = 16).  16384 tokens of 16 + 16 + 32 heads of 128: 407 MB each
+// way, both ways in 139 us, 5.8 TB/s.
 #include "gdr_device.h"
 
 namespace gdr {

@@ -26,9 +26,12 @@ Modules
               normalisation ahead of the recurrence
   backward    reverse-mode gradients of the recurrence (dq, dk, dv, dg,
               dbeta, dS0)
+  gdr         the gated delta rule (one decay per head and token), its
+              gradients, and q, k, v in 8 bits
 
 Every function is pinned (``tests/test_oracle_pins.py``, ``tests/test_oracle_spec.py``,
-``tests/test_oracle_prologue.py``, ``tests/test_oracle_backward.py``) against facts that
+``tests/test_oracle_prologue.py``, ``tests/test_oracle_backward.py``,
+``tests/test_oracle_gdr.py``) against facts that
 do not come from the oracle itself (closed forms, a hand-derived example,
 retrieval identities, brute force, invariants); none is "parity unpinned".
 """
