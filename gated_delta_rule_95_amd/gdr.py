@@ -142,7 +142,7 @@ def gdr_fwd_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     if S0 is not None:
         _need(S0, "S0", torch.float32, d.state, d.dev)
     if o is None:
-        o = torch.empty(v.shape, dtype=q.dtype, device=d.dev)
+        o = torch.empty_like(v)                         # in q's dtype, which v has
     else:
         _need(o, "o", q.dtype, v.shape, d.dev)
     if S_T is not None:
@@ -173,7 +173,7 @@ def gdr_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     if slots is not None:
         _need(slots, "slots", torch.int32, q.shape[:1], d.dev)
     if o is None:
-        o = torch.empty(v.shape, dtype=q.dtype, device=d.dev)
+        o = torch.empty_like(v)                         # in q's dtype, which v has
     else:
         _need(o, "o", q.dtype, v.shape, d.dev)
     d.run(_lib.load().gdr_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
@@ -202,8 +202,8 @@ def _bwd(d, dt, fn, args, g, beta, dO, S0, dS_T, cu_seqlens, scale, workspace):
         _need(workspace, "workspace", torch.uint8, workspace.shape, d.dev)
     new = lambda shape, t: torch.empty(shape, dtype=t, device=d.dev)   # noqa: E731
     dq, dk = new(d.lead + (d.Hk, d.dk), dt), new(d.lead + (d.Hk, d.dk), dt)
-    dv, dS0 = new(dO.shape, dt), new(d.state, torch.float32)
-    dg, db = new(g.shape, torch.float32), new(g.shape, torch.float32)
+    dv, dS0 = torch.empty_like(dO), new(d.state, torch.float32)
+    dg, db = torch.empty_like(g), torch.empty_like(g)
     d.run(fn, *args[0], _ptr(g), _ptr(beta), _ptr(S0), _ptr(cu_seqlens), d.n_seqs, d.N, d.Hk, d.Hv,
           d.dk, d.dv, d.scale(scale), *args[1], _ptr(dO), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv),
           _ptr(dg), _ptr(db), _ptr(dS0), _ptr(workspace), workspace.numel())
