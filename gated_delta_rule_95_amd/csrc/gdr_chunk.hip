@@ -499,17 +499,19 @@ struct Consumer {
         const PairRegs T0(st.Tone[0], lane, false), T1(st.Tpair[0], lane);
         pin();
         f32x4 X[4] = {}, O[4] = {}, R[4];
-        Parts<2> p[KS];
+        // two parts of S in the forward (S_T is off by 6e-7 at most), three where
+        // the backward's gradients depend on R
+        constexpr int NX = MODE == KEEP ? 3 : 2;
+        Parts<NX> p[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             if constexpr (MODE == KEEP) {
-                const Parts<3> x = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
-                p[s] = Parts<2>{{x.p[0], x.p[1]}};
-                put_state(x, s, eye, keep, dv, cw, ln, lg);
+                p[s] = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
+                put_state(p[s], s, eye, keep, dv, cw, ln, lg);
             } else
                 p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = mma_parts<2>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p[s], X[t]);
+            for (int t = 0; t < 4; ++t) X[t] = mma_parts<NX>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p[s], X[t]);
             if constexpr (MODE == FWD && LEAN) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) O[t] = mma_by_parts(p[s], lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
