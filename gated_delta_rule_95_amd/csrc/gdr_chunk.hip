@@ -499,22 +499,18 @@ struct Consumer {
         const PairRegs T0(st.Tone[0], lane, false), T1(st.Tpair[0], lane);
         pin();
         f32x4 X[4] = {}, O[4] = {}, R[4];
-        // two parts of S in the forward (S_T is off by 6e-7 at most), three where
-        // the backward's gradients depend on R
-        constexpr int NX = MODE == KEEP ? 3 : 2;
-        Parts<NX> p[KS];
+        // three parts of S where R depends on it (with two the forward was 2%
+        // faster and S_T off by up to 1e-6, dg by 1.9e-6), two where only o does
+        Parts<3> p[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            if constexpr (MODE == KEEP) {
-                p[s] = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
-                put_state(p[s], s, eye, keep, dv, cw, ln, lg);
-            } else
-                p[s] = split_pair<2>(S[2 * s], S[2 * s + 1], eye);
+            p[s] = split_pair<3>(S[2 * s], S[2 * s + 1], eye);
+            if constexpr (MODE == KEEP) put_state(p[s], s, eye, keep, dv, cw, ln, lg);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = mma_parts<NX>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p[s], X[t]);
+            for (int t = 0; t < 4; ++t) X[t] = mma_parts<3>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p[s], X[t]);
             if constexpr (MODE == FWD && LEAN) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) O[t] = mma_by_parts(p[s], lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
+                for (int t = 0; t < 4; ++t) O[t] = mma_by_parts(Parts<2>{{p[s].p[0], p[s].p[1]}}, lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
             }
             if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }
@@ -532,7 +528,7 @@ struct Consumer {
             if (MODE == FWD && s < KS && !LEAN)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    O[t] = mma_by_parts(p[s], lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
+                    O[t] = mma_by_parts(Parts<2>{{p[s].p[0], p[s].p[1]}}, lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
         };
         const Parts<3> y01 = split_pair<3>(R[0], R[1], eye);
         qs(0);
