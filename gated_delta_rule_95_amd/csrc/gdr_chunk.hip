@@ -24,9 +24,9 @@
 // Bound by the chain of chunks: a chunk's products wait for one another, most
 // of all in the substitution, and the matrix cores are busy for 45% of the
 // forward's time (37% of the backward's two passes).  Forward, 4 sequences of
-// 4096 tokens, 32 heads of 128 x 128: 255-275 us (1.6 TB/s of inputs, outputs
+// 4096 tokens, 32 heads of 128 x 128: 260-285 us (1.5 TB/s of inputs, outputs
 // and states; the consumers by themselves 216 us, the producers 178); 13 ragged
-// sequences, 20011 tokens: 280 us.  Keeping forward and sweep of the former:
+// sequences, 20011 tokens: 290 us.  Keeping forward and sweep of the former:
 // 0.70 ms for 2.3 GB moved.  The substitution over blocks of 16 tokens took 290
 // and 302 us; operands straight from global memory in place of the LDS twice
 // the time (a load of 64 scattered pieces takes 900 cycles and more to issue);
@@ -510,7 +510,8 @@ struct Consumer {
             for (int t = 0; t < 4; ++t) X[t] = mma_parts<3>(lds8(&st.K[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), p[s], X[t]);
             if constexpr (MODE == FWD && LEAN) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) O[t] = mma_by_parts(Parts<2>{{p[s].p[0], p[s].p[1]}}, lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
+                for (int t = 0; t < 4; ++t)
+                    O[t] = mma_by_parts(Parts<2>{{p[s].p[0], p[s].p[1]}}, lds8(&st.Q[Swz<DK>::at(16 * t + ln, 32 * s + 8 * lg)]), O[t]);
             }
             if (s == 0 && more) __syncthreads();         // the producers' rows of the next chunk
         }

@@ -12,7 +12,7 @@
 //
 // Operands of the products that dg depends on are held in three bf16 parts
 // and multiplied without the parts' products below 2^-24 (with two parts dg
-// was off by 4e-6 of its norm, with three by 6e-7: sums in fp32 are little
+// was off by 4e-6 of its norm, with three by 2e-7 to 6e-7: sums in fp32 are no
 // better); dP and dN, which only dq and dk see, in two.
 //
 // Bound by the latencies between its phases: a workgroup has a compute unit's
