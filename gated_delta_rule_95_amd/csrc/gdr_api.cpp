@@ -171,6 +171,12 @@ kda_status bwd_impl(const char *fn, const void *q, const uint8_t *qe, const void
     if ((s = check_heads(Hk, Hv, dk, dv)) != KDA_OK) return s;
     if ((s = check_seqs(n_seqs, n_tokens, cu)) != KDA_OK) return s;
     if ((s = check_chains((int64_t)n_seqs * Hv, "n_seqs")) != KDA_OK) return s;
+    // the chunk form deals a key head's workgroups out in rounds of eight (2048
+    // threads a chain at d_v = 128, half of that at 64)
+    if (gdr::chunked(dk, dv, in != gdr::In::F32) && dv == 128 &&
+        ((int64_t)n_seqs * Hk + 7) / 8 * 8 * (Hv / Hk) >= (int64_t)1 << 21)
+        return set_error(KDA_ERR_INVALID_ARG,
+                         "n_seqs * H_k rounded up to a multiple of 8, times H_v / H_k, must be below 2^21");
     if (gdr::bwd_slots(n_seqs, n_tokens, gdr::bwd_chunk(dk, dv, in != gdr::In::F32)) * Hk >= (int64_t)1 << 23)
         return set_error(KDA_ERR_INVALID_ARG, "too many chunks times H_k for one launch (2^23)");
     if (n_seqs == 0) return ok();

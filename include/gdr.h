@@ -39,7 +39,9 @@
  * Sizes: d_k, d_v in {16, 32, 64, 128}, independently; 1 <= H_k, H_v a
  * multiple of H_k, H_v * max(d_k, d_v) < 2^22; 0 <= n_tokens <= 2^31 - 64;
  * n_seqs * H_v (decode: N * H_v) < 2^21.  The backward also wants fewer than
- * 2^23 (chunk of 64 tokens, key head) pairs (32 tokens in the fp32 form).
+ * 2^23 (chunk of 64 tokens, key head) pairs (32 tokens in the fp32 form), and
+ * from bf16 or 8-bit inputs with d_k >= 64, d_v = 128 counts n_seqs * H_k
+ * rounded up to a multiple of 8 against the 2^21.
  * in_dtype KDA_BF16 or KDA_F32.
  *
  * Alignment (bytes): q, k, v, o, dO, dq, dk, dv: eight elements of bf16 and
