@@ -28,10 +28,12 @@ Modules
               dbeta, dS0)
   gdr         the gated delta rule (one decay per head and token), its
               gradients, and q, k, v in 8 bits
+  gdr_chunked the same in chunks, with operands held in few parts or terms
+              left out on request: what the GPU tests' tolerances must reject
 
 Every function is pinned (``tests/test_oracle_pins.py``, ``tests/test_oracle_spec.py``,
 ``tests/test_oracle_prologue.py``, ``tests/test_oracle_backward.py``,
-``tests/test_oracle_gdr.py``) against facts that
+``tests/test_oracle_gdr.py``, ``tests/test_oracle_gdr_chunked.py``) against facts that
 do not come from the oracle itself (closed forms, a hand-derived example,
 retrieval identities, brute force, invariants); none is "parity unpinned".
 """
