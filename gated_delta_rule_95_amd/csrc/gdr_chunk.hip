@@ -172,7 +172,9 @@ struct Producer {
 #pragma unroll
         for (int i = 0; i < 3; ++i) reinterpret_cast<u32x2 *>(&t[i][lane])[side] = p[i];
     }
-    // decays between lane token x and the row tokens y .. y + 3, times w
+    // decays between lane token x and the row tokens y .. y + 3, times w.  The
+    // exponent's sum rounds (|d| 2^-25 of the factor 2^d): such a factor stands
+    // in a row beside the token's own, which has no decay.
     static __device__ __forceinline__ f32x4 decays(const float (*gp)[C], int x, int y, f32x4 w)
     {
         const float gh = gp[0][x], gl = gp[1][x];
@@ -261,14 +263,14 @@ struct Producer {
     {
         const int lane = ln + 16 * lg;
         // cumulative log2-decay in double, held as two floats
-        const double G = scan64((double)floor_g(g) * (double)LOG2E), Gend = last_lane(G);
-        const float gh = (float)G;
+        const double G = scan64((double)floor_g(g) * LOG2E64), Gend = last_lane(G);
+        const float gh = (float)G, gl = (float)(G - (double)gh);
         gp[0][lane] = gh;
-        gp[1][lane] = (float)(G - (double)gh);
+        gp[1][lane] = gl;
         gp[2][lane] = beta;
         if constexpr (W == 0) {
-            const float er = kda::fast_exp2((float)(Gend - G));
-            const float eg = kda::fast_exp2(gh);
+            const float er = exp2_64(Gend - G);
+            const float eg = exp2_two(gh, gl);
             st.eG[lane] = eg;
             st.eGs[lane] = scale * eg;
             st.eR[lane] = SW ? er : er * beta;
@@ -276,7 +278,7 @@ struct Producer {
                 st.eGb[lane] = beta * eg;
                 st.beta[lane] = beta;
             }
-            if (lane == 0) st.gamma = kda::fast_exp2((float)Gend);
+            if (lane == 0) st.gamma = exp2_64(Gend);
         }
         // K and Q blocks to the stage
 #pragma unroll

@@ -50,7 +50,7 @@ void gdr_decode_kernel(DecodeArgs a)
         s_q[i] = kda::Elem<T>::ld(qp + i);
     }
     const f32x4 vv = kda::Elem<T>::ld4(static_cast<const T *>(a.v) + nh * DV + 4 * cb);
-    const float b = a.beta[nh], al = kda::fast_exp2(floor_g(a.g[nh]) * LOG2E);
+    const float b = a.beta[nh], al = decay(floor_g(a.g[nh]));
     __syncthreads();
 
     f32x4 pk = {0.f, 0.f, 0.f, 0.f}, pq = pk;

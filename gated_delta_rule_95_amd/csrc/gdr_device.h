@@ -74,6 +74,43 @@ __device__ __forceinline__ Seq seq_of(const SeqArgs &s, int n)
 // 64 such values keep far more than single precision in their differences
 __device__ __forceinline__ float floor_g(float g) { return g < -1e4f ? -1e4f : g; }
 
+// e^g for the decay of one token.  With k the nearest whole number to
+// g log2 e, r = g - k ln 2 (ln 2 in two floats; |r| <= 0.35) and e^r to the
+// seventh power of r (the eighth is below 6e-9): the last sum rounds once, so
+// the factor is off by little more than half a step, to either side as often.
+// The hardware's 2^x of a product g log2 e is off by |g| 2^-24 at fast decays
+// (3e-6 at g = -80) and by -7e-9 in the mean at slow ones, which a state
+// multiplied by one such factor a token adds up (fp32, g > -1e-4, 700 tokens:
+// o off by 1.65e-6).
+__device__ __forceinline__ float decay(float g)
+{
+    const float k = __builtin_rintf(g * LOG2E);
+    float r = __builtin_fmaf(-k, 0.693147182464599609375f, g);
+    r = __builtin_fmaf(-k, -1.904654299957767878541e-9f, r);
+    float p = 1.f / 5040;
+    p = __builtin_fmaf(p, r, 1.f / 720);
+    p = __builtin_fmaf(p, r, 1.f / 120);
+    p = __builtin_fmaf(p, r, 1.f / 24);
+    p = __builtin_fmaf(p, r, 1.f / 6);
+    p = __builtin_fmaf(p, r, 0.5f);
+    p = __builtin_fmaf(p, r, 1.f);
+    return __builtin_ldexpf(__builtin_fmaf(p, r, 1.f), (int)k);
+}
+
+// 2^(h + l), l what is left of the exponent behind the float h: alone, h would
+// leave the factor off by |h| 2^-25
+constexpr double LOG2E64 = 1.4426950408889634;
+__device__ __forceinline__ float exp2_two(float h, float l)
+{
+    const float e = kda::fast_exp2(h);
+    return __builtin_fmaf(e, 0.6931472f * l, e);
+}
+__device__ __forceinline__ float exp2_64(double x)
+{
+    const float h = (float)x;
+    return exp2_two(h, (float)(x - (double)h));
+}
+
 // the upper 32 lanes of a change places with the lower 32 of b
 __device__ __forceinline__ void swap32(float &a, float &b)
 {

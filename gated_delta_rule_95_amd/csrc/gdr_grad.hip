@@ -116,8 +116,8 @@ void gdr_grad_kernel(Args a)
         }
         __syncthreads();
         if (tid < C) {
-            s.eG[tid] = kda::fast_exp2((float)(s.G[tid] * LOG2E));
-            s.eR[tid] = kda::fast_exp2((float)((s.G[C - 1] - s.G[tid]) * LOG2E));
+            s.eG[tid] = exp2_64(s.G[tid] * LOG2E64);
+            s.eR[tid] = exp2_64((s.G[C - 1] - s.G[tid]) * LOG2E64);
         }
         // dbeta: eight threads a token
         {
@@ -154,7 +154,7 @@ void gdr_grad_kernel(Args a)
             const int i = x / C, j = x % C;
             float p = 0.f, nn = 0.f, e = 0.f;
             if (i >= j) {
-                const float d = kda::fast_exp2((float)((s.G[i] - s.G[j]) * LOG2E));
+                const float d = exp2_64((s.G[i] - s.G[j]) * LOG2E64);
                 p = a.scale * d * s.dP[i][j];
                 if (i > j) {
                     nn = -d * s.dN[i][j];
@@ -261,7 +261,7 @@ void gdr_grad_kernel(Args a)
             for (int m = 1; m < 8; m *= 2) x += __shfl_xor(x, m);
             if (tid % 8 == 0 && t < nt)
                 a.dg[(int64_t)(tok + t) * a.Hv + hv] =
-                    x + kda::fast_exp2((float)(s.G[C - 1] * LOG2E)) * (s.ls[0] + s.ls[1] + s.ls[2] + s.ls[3]);
+                    x + exp2_64(s.G[C - 1] * LOG2E64) * (s.ls[0] + s.ls[1] + s.ls[2] + s.ls[3]);
         }
     }
 #pragma unroll

@@ -222,7 +222,7 @@ void gdr_grad_chunk_kernel(Args a)
         const int hv = hk * grp + h;
         fresh();
         if (wave == 0) {
-            const double G = scan64<double>((double)floor_g(rgate) * (double)LOG2E);
+            const double G = scan64<double>((double)floor_g(rgate) * LOG2E64);
             const float gh = (float)G;
             s.G[0][lane] = gh;
             s.G[1][lane] = (float)(G - (double)gh);
@@ -291,7 +291,7 @@ void gdr_grad_chunk_kernel(Args a)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int i = 16 * t + ln;
-            const float eg = kda::fast_exp2(s.G[0][i]);
+            const float eg = exp2_two(s.G[0][i], s.G[1][i]);
             const float er = kda::fast_exp2((s.G[0][C - 1] - s.G[0][i]) + (s.G[1][C - 1] - s.G[1][i]));
             const f32x4 qv = widen(*reinterpret_cast<const u32x2 *>(&s.q[Swz<DK>::at(i, ch0)]));
             const f32x4 kv = widen(*reinterpret_cast<const u32x2 *>(&s.k[Swz<DK>::at(i, ch0)]));
@@ -409,7 +409,7 @@ void gdr_grad_chunk_kernel(Args a)
             float l = 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) l += s.ls[w];
-            dg = s.rev[C - 1 - lane] + before + kda::fast_exp2(s.G[0][C - 1]) * l;
+            dg = s.rev[C - 1 - lane] + before + exp2_two(s.G[0][C - 1], s.G[1][C - 1]) * l;
         }
         __syncthreads();
         // products with the chunk's own rows

@@ -221,7 +221,7 @@ __device__ __forceinline__ void token_pass(const Args &a, Tile<DK, DV, GC> *s_t,
             if (t < TT) *reinterpret_cast<f32x4 *>(&s.v[t][y]) = rv[x];
         }
         if (tid < TT) {
-            s.gate[tid / 2][2 * (tid & 1)] = kda::fast_exp2(floor_g(ra) * LOG2E);
+            s.gate[tid / 2][2 * (tid & 1)] = decay(floor_g(ra));
             s.gate[tid / 2][2 * (tid & 1) + 1] = rb;
         }
     };
