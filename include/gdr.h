@@ -30,10 +30,14 @@
  *                 sequences of n_tokens / n_seqs tokens each
  * g = -inf is allowed and forgets the state (every g below -1e4 counts as
  * -1e4, whose exponential is 0).  g > 0 is computed as given where nothing
- * overflows.  NaN in g, beta, q, k or v of a token may reach any output of
- * its own sequence and heads (tokens before it in its chunk among them), and
- * none of another's.  Inside a chunk of 64 tokens the factors exp(G_i - G_j) of the
- * log-decay's cumulative sums are formed from their differences, so no
+ * overflows.  NaN or an infinity in g (but -inf), beta, q, k, v or dO of a
+ * token, or in a state or its cotangent, may reach any output of its own
+ * sequence and value head (from q and k: of the value heads of their key
+ * head), and dq and dk of that key head, and none of another's.  Tokens before
+ * it in its chunk of 64 are among them: the chunk's products multiply what the
+ * mask leaves out by zero, and zero times such a value is NaN.  Inside a chunk
+ * the factors exp(G_i - G_j) of the log-decay's cumulative sums are formed
+ * from their differences, so no
  * decay, however fast, overflows.
  *
  * Sizes: d_k, d_v in {16, 32, 64, 128}, independently; 1 <= H_k, H_v a
