@@ -129,14 +129,6 @@ __device__ __forceinline__ f32x4 widen(u32x2 w)
                  __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xffff0000u)};
 }
 
-// Raw buffer resources: reads at or past `bytes` give 0, stores there are dropped.
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ __forceinline__ rsrc_t make_rsrc(const void *base, int bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0,
-                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-}
-
 // Rows of q, k or v: n rows from token tok on (n <= 0: none), zeros behind
 // them.  at() is a lane's place (row, channel of head h), raw() requests the
 // eight channels c (a constant) behind it, bf() gives them in bf16.

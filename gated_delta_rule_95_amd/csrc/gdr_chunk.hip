@@ -82,24 +82,6 @@ __device__ __forceinline__ f32x4 ld4f(const float *p) { return *reinterpret_cast
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
-// inclusive sum over the 64 lanes in double, on register moves between lanes
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double scan_step(double x)
-{
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
-    return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-__device__ __forceinline__ double scan64(double x)
-{
-    x = scan_step<0x111, 0xf>(x);       // row_shr 1, 2, 4, 8
-    x = scan_step<0x112, 0xf>(x);
-    x = scan_step<0x114, 0xf>(x);
-    x = scan_step<0x118, 0xf>(x);
-    x = scan_step<0x142, 0xa>(x);       // lane 15 of each even row to the row behind it
-    return scan_step<0x143, 0xc>(x);    // lane 31 to the upper half
-}
 __device__ __forceinline__ double last_lane(double x)
 {
     const uint64_t b = __builtin_bit_cast(uint64_t, x);

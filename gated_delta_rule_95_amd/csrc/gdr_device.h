@@ -70,6 +70,29 @@ __device__ __forceinline__ Seq seq_of(const SeqArgs &s, int n)
     return Seq{b, e > b ? e - b : 0};
 }
 
+// the sequence and chunk of a slot: slots of sequence n start at
+// edge(n) / C + n, which grows with n
+__device__ __forceinline__ bool find_chunk(const SeqArgs &s, int64_t slot, int C, int &n, int &c)
+{
+    int lo = 0, hi = s.n_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((int64_t)(seq_edge(s, mid) / C) + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    n = lo;
+    c = (int)(slot - (seq_edge(s, lo) / C + lo));
+    return c >= 0 && (int64_t)c * C < seq_of(s, lo).len;
+}
+
+// Raw buffer resources: reads at or past `bytes` give 0, stores there are dropped.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void *base, int bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
 // log-decay with its floor (a NaN stays): exp of the floor is 0, and sums of
 // 64 such values keep far more than single precision in their differences
 __device__ __forceinline__ float floor_g(float g) { return g < -1e4f ? -1e4f : g; }
@@ -127,6 +150,29 @@ __device__ __forceinline__ void swap16(float &a, float &b)
     a = __uint_as_float(x);
     b = __uint_as_float(y);
 }
+// inclusive sum over the 64 lanes, on register moves between lanes
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T scan_step(T x)
+{
+    if constexpr (sizeof(T) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+        return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+    } else
+        return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, ROWS, 0xf, false));
+}
+template <typename T>
+__device__ __forceinline__ T scan64(T x)
+{
+    x = scan_step<0x111, 0xf>(x);       // row_shr 1, 2, 4, 8
+    x = scan_step<0x112, 0xf>(x);
+    x = scan_step<0x114, 0xf>(x);
+    x = scan_step<0x118, 0xf>(x);
+    x = scan_step<0x142, 0xa>(x);       // lane 15 of each even row to the row behind it
+    return scan_step<0x143, 0xc>(x);    // lane 31 to the upper half
+}
+
 // sum over the lanes of equal lane % 16
 __device__ __forceinline__ float sum_groups(float x)
 {

@@ -26,21 +26,6 @@ __device__ __forceinline__ f32x4 mma4(float a, float b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// the sequence and chunk of a slot: slots of sequence n start at
-// edge(n) / C + n, which grows with n
-__device__ __forceinline__ bool find_chunk(const SeqArgs &s, int64_t slot, int C, int &n, int &c)
-{
-    int lo = 0, hi = s.n_seqs - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if ((int64_t)(seq_edge(s, mid) / C) + mid <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    n = lo;
-    c = (int)(slot - (seq_edge(s, lo) / C + lo));
-    return c >= 0 && (int64_t)c * C < seq_of(s, lo).len;
-}
-
 // fp32 on the fp32 matrix cores (16x16x4): lane (n, g) = (lane % 16, lane / 16)
 // takes contraction index 4 g + i at step i, so both operands of a product
 // of row-major tiles are 16-byte reads of a row.
@@ -53,8 +38,7 @@ struct alignas(16) GradSmem {
     float dO[C32][DV + 4], U[C32][DV + 4], Yb[C32][DV + 4];
     float dP[C32][C32 + 4], dN[C32][C32 + 4], qk[C32][C32 + 4], kk[C32][C32 + 4];
     double G[C32];
-    float eG[C32], eR[C32], beta[C32], a[4][C32], b[4][C32], ls[4];
-    float gam;
+    float eG[C32], eR[C32], a[4][C32], b[4][C32], ls[4];
 };
 
 template <typename TI, int DK, int DV>

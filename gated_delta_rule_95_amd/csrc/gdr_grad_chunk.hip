@@ -50,20 +50,6 @@ struct alignas(16) GradSmem {
     float G[2][C], a[NW][C], b[NW][C], e[NW][C], rev[C], ls[NW];
 };
 
-__device__ __forceinline__ bool find_chunk(const SeqArgs &s, int64_t slot, int &n, int &c)
-{
-    // slots of sequence n start at edge(n) / C + n, which grows with n
-    int lo = 0, hi = s.n_seqs - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if ((int64_t)(seq_edge(s, mid) / C) + mid <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    n = lo;
-    c = (int)(slot - (seq_edge(s, lo) / C + lo));
-    return c >= 0 && (int64_t)c * C < seq_of(s, lo).len;
-}
-
 // four rows (consecutive, from row on) of one column a lane; see lds_tr
 template <int D>
 __device__ __forceinline__ u32x2 tr4(const bf16 *m, int row, int c, int ln)
@@ -91,30 +77,6 @@ __device__ __forceinline__ float sum16(float x)
     x = dpp_add<0x4e>(x);        // quad_perm 2 3 0 1
     x = dpp_add<0x141>(x);       // row_half_mirror
     return dpp_add<0x140>(x);    // row_mirror
-}
-
-template <typename T, int CTRL, int ROWS>
-__device__ __forceinline__ T scan_step(T x);
-template <typename T>
-__device__ __forceinline__ T scan64(T x)
-{
-    x = scan_step<T, 0x111, 0xf>(x);
-    x = scan_step<T, 0x112, 0xf>(x);
-    x = scan_step<T, 0x114, 0xf>(x);
-    x = scan_step<T, 0x118, 0xf>(x);
-    x = scan_step<T, 0x142, 0xa>(x);
-    return scan_step<T, 0x143, 0xc>(x);
-}
-template <typename T, int CTRL, int ROWS>
-__device__ __forceinline__ T scan_step(T x)
-{
-    if constexpr (sizeof(T) == 8) {
-        const uint64_t b = __builtin_bit_cast(uint64_t, x);
-        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
-        const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
-        return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-    } else
-        return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, ROWS, 0xf, false));
 }
 
 // the three parts of eight values
@@ -160,7 +122,7 @@ void gdr_grad_chunk_kernel(Args a)
     const int64_t slot = blockIdx.x / a.Hk;
     const int hk = blockIdx.x % a.Hk, grp = a.Hv / a.Hk;
     int n, c;
-    if (!find_chunk(a.seq, slot, n, c)) return;
+    if (!find_chunk(a.seq, slot, C, n, c)) return;
     const Seq sq = seq_of(a.seq, n);
     const int64_t tok = __builtin_amdgcn_readfirstlane(sq.bos + c * C);
     const int nt = __builtin_amdgcn_readfirstlane(sq.len - c * C < C ? sq.len - c * C : C);

@@ -36,13 +36,6 @@ namespace {
 
 constexpr int TT = 16;               // tokens staged at a time
 
-// raw buffer resource: stores at or past `bytes` are dropped
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ __forceinline__ rsrc_t make_rsrc(const void *base, int bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-}
-
 enum { FWD = 0, KEEP = 1, SWEEP = 2 };
 
 constexpr int64_t kFew = 8192, kSome = 32768;
