@@ -134,7 +134,8 @@ def gdr_fwd_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     v    : [..., H_v, d_v], H_v a multiple of H_k (value head h reads key head h // (H_v // H_k))
     g    : [..., H_v] fp32 log-decay <= 0 (-inf allowed);  beta : [..., H_v] fp32
     S0   : [n_seqs, H_v, d_k, d_v] fp32 or None
-    cu_seqlens : int32 [n_seqs + 1] on the device (packed input only)
+    cu_seqlens : int32 [n_seqs + 1] on the device (packed input only); rows of tokens behind
+        its last entry are left as they are in a given o, unset in one allocated here
     scale : multiplies o; d_k ** -0.5 by default
     Returns (o in q's dtype, S_T fp32 or None).
     """
@@ -217,8 +218,9 @@ def gdr_bwd_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
                     workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, ...]:
     """Gradients of gdr_fwd_chunked: dq, dk (summed over the value heads of a
     key head) and dv in q's dtype, dg, dbeta, dS0 in fp32.  dO has o's shape
-    and q's dtype, dS_T is the final states' cotangent or None.  The workspace
-    (uint8) is allocated through torch unless given."""
+    and q's dtype, dS_T is the final states' cotangent or None.  Rows of tokens
+    behind cu_seqlens' last entry are unset.  The workspace (uint8) is
+    allocated through torch unless given."""
     d = _Dims(q, k, v, g, beta, cu_seqlens)
     return _bwd(d, q.dtype, _lib.load().gdr_bwd_chunked, ((_ptr(q), _ptr(k), _ptr(v)), (_dt(q.dtype),)),
                 g, beta, dO, S0, dS_T, cu_seqlens, scale, workspace)

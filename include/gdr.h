@@ -57,7 +57,10 @@
  * every buffer, nothing is allocated or synchronised, argument problems are
  * reported as a kda_status (kda_last_error has the message) before anything
  * is launched, and cu_seqlens and slots that break their contract change
- * results, never the addresses touched.
+ * results, never the addresses touched: entries of cu_seqlens count as the
+ * nearest of 0 .. n_tokens, and a sequence that ends before it starts as
+ * empty.  Rows of tokens that no sequence has (behind a last entry below
+ * n_tokens) are not read, and in the outputs not written.
  */
 #ifndef GDR_H
 #define GDR_H
@@ -89,8 +92,9 @@ kda_status gdr_fwd_chunked(const void *q, const void *k, const void *v, const fl
  * and writes the state slots[n] (slots NULL: state n, N <= n_slots).  A slot
  * outside [0, n_slots) marks a padded row of the batch: its o row is written
  * with zeros and no state is touched.  The slots of a call must differ from
- * one another; two requests of one slot race and leave either's state (no
- * other memory is touched).
+ * one another: two requests of one slot race, which leaves that state and both
+ * o rows undefined (the state may hold elements of either, or of one computed
+ * from the other's) and touches no other memory.
  */
 kda_status gdr_decode_step(const void *q, const void *k, const void *v, const float *g,
                            const float *beta, float *S, const int32_t *slots, int32_t n_slots,
