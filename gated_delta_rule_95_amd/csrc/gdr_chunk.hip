@@ -22,15 +22,21 @@
 // each, two the rest of K K^T and K Q^T, without a word among them.
 //
 // Bound by the chain of chunks: a chunk's products wait for one another, most
-// of all in the substitution, and the matrix cores are busy for 45% of the
+// of all in the substitution, and the matrix cores are busy for 48% of the
 // forward's time (37% of the backward's two passes).  Forward, 4 sequences of
-// 4096 tokens, 32 heads of 128 x 128: 260-285 us (1.5 TB/s of inputs, outputs
-// and states; the consumers by themselves 216 us, the producers 178); 13 ragged
-// sequences, 20011 tokens: 290 us.  Keeping forward and sweep of the former:
-// 0.70 ms for 2.3 GB moved.  The substitution over blocks of 16 tokens took 290
-// and 302 us; operands straight from global memory in place of the LDS twice
-// the time (a load of 64 scattered pieces takes 900 cycles and more to issue);
-// one bf16 part of S and R in o saved 5% and missed repeated keys by 4e-3.
+// 4096 tokens, 32 heads of 128 x 128: 262 us (1.6 TB/s of inputs, outputs and
+// states; the consumers by themselves 183 us, the producers 178); 13 ragged
+// sequences, 20011 tokens: 281 us (201 and 170).  Keeping forward and sweep of
+// the former: 0.71 ms for 2.3 GB moved.  Operands straight from global memory
+// in place of the LDS take twice the time (a load of 64 scattered pieces takes
+// 900 cycles and more to issue).
+//
+// What only o sees, S, R and P in its products, is held in two bf16 parts, the
+// products below 2^-16 left out: o is rounded to bf16 (2^-8) behind it, and its
+// error stays that of the rounding (1.66e-3 of its norm, as in 32 bits
+// throughout); 0.3% of its elements round to the other neighbour.  Three parts
+// bring that to 0.02% and cost 8 to 10% (262 -> 288 and 284 -> 311 us); one part
+// of S and R saves 5% and misses repeated keys by 4e-3.
 #include "gdr_chunk.h"
 
 namespace gdr {
@@ -670,9 +676,12 @@ __device__ __forceinline__ void store_state(const f32x4 *S, float *p, int dv, in
 
 // Workgroups of one key head (its value heads' column blocks) share q and k:
 // unit u of them runs on XCD u % 8 (workgroups go round the XCDs in order), so
-// that the second and later reads hit that XCD's L2.  Units are dealt out with
-// the longest sequences first (up to 128 of them): a long chain that starts
-// last would run alone at the end.
+// that the second and later reads hit that XCD's L2.  Fewer than eight units
+// leave XCDs without work, which costs where a unit has more workgroups than
+// an XCD has compute units (32): 16384 tokens, 32 value heads of 128 x 128 on
+// one key head take 1784 us, on two 877.  Units are dealt out with the longest
+// sequences first (up to 128 of them): a long chain that starts last would run
+// alone at the end.
 constexpr int kSorted = 128;
 __device__ __forceinline__ bool my_chain(const Args &a, int64_t b, int per_unit, int *lens, int tid, int nthreads, int &n, int &hk,
                                          int &j)
@@ -823,10 +832,13 @@ hipError_t launch_bwd_t(const Args &a)
 }  // namespace
 
 // Eight consumers (one workgroup a chain of 128 columns) or four (two): with
-// both halves of every chain running at once, four are faster (281 against
-// 367 us, 128 chains of 64 chunks on 256 compute units); with more chains than
+// both halves of every chain running at once, four are faster (273 against
+// 335 us, 128 chains of 64 chunks on 256 compute units); with more chains than
 // half the compute units the halves would queue, and eight do the work of two
-// workgroups in 1.3 times the time of one.
+// workgroups in 1.2 times the time of one (129 chains: 448 against 329 us; 256:
+// 534 against 429).  The count says nothing of the chains' lengths: one
+// sequence of 16384 tokens beside eight of 100, 16 heads, takes 1248 us with
+// eight and would take 918 with four.
 constexpr int64_t kWide = 129;
 
 hipError_t launch_chunk_fwd(const Args &a)

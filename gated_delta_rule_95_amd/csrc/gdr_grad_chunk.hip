@@ -13,12 +13,12 @@
 // Operands of the products that dg depends on are held in three bf16 parts
 // and multiplied without the parts' products below 2^-24 (with two parts dg
 // was off by 4e-6 of its norm, with three by 2e-7 to 6e-7: sums in fp32 are no
-// better); dP and dN, which only dq and dk see, in two.
+// better); dP and dN, which only dq and dk see (rounded to bf16), in two.
 //
 // Bound by the latencies between its phases: a workgroup has a compute unit's
-// LDS to itself, the matrix cores are busy for 28% of the time and the vector
-// ALU for 41%, and 2.0 GB of states, cotangents and rows go at 3.1 TB/s.  4
-// sequences of 4096 tokens, 32 value heads of 128 x 128 on 16 key heads: 0.64
+// LDS to itself, the matrix cores are busy for 29% of the time and the vector
+// ALU for 41%, and 2.0 GB of states, cotangents and rows go at 3.2 TB/s.  4
+// sequences of 4096 tokens, 32 value heads of 128 x 128 on 16 key heads: 0.63
 // ms, of which per workgroup and value head the products over the value
 // columns take 40%, the pairs 12%, the products with the chunk's rows 9%,
 // staging 6%, the state's part 5%, and the workgroup's start 10%.  Two waves
