@@ -107,7 +107,8 @@ __device__ __forceinline__ float floor_g(float g) { return g < -1e4f ? -1e4f : g
 // o off by 1.65e-6).
 __device__ __forceinline__ float decay(float g)
 {
-    const float k = __builtin_rintf(g * LOG2E);
+    // the bounds only keep NaN and overflow out of the conversion below
+    const float k = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(g * LOG2E), -2e4f), 2e4f);
     float r = __builtin_fmaf(-k, 0.693147182464599609375f, g);
     r = __builtin_fmaf(-k, -1.904654299957767878541e-9f, r);
     float p = 1.f / 5040;
