@@ -2,9 +2,9 @@
 // Declarations and the contract of every entry point are in include/gdr.h.
 #include <hip/hip_runtime.h>
 
+#include "api_checks.h"
 #include "gdr.h"
 #include "gdr_launch.h"
-#include "kda_launch.h"
 
 #define GDR_API extern "C" __attribute__((visibility("default")))
 
@@ -37,15 +37,13 @@ static hipError_t launch_bwd(const Args &a)
 
 namespace {
 
-using kda::set_error;
-
-kda_status ok() { return set_error(KDA_OK, "%s", ""); }
-
-kda_status hip_status(hipError_t e, const char *what)
-{
-    if (e == hipSuccess) return ok();
-    return set_error(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
+using api::Buf;
+using api::check_bufs;
+using api::check_dtype;
+using api::hip_status;
+using api::ok;
+using api::round256;
+using api::set_error;
 
 bool head_dim_ok(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
@@ -98,39 +96,6 @@ kda_status check_chains(int64_t chains, const char *what)
     return KDA_OK;
 }
 
-kda_status check_dtype(kda_dtype t)
-{
-    if (t != KDA_F32 && t != KDA_BF16)
-        return set_error(KDA_ERR_INVALID_ARG, "in_dtype %d is not a kda_dtype", (int)t);
-    return KDA_OK;
-}
-
-struct Buf {
-    const void *p;
-    const char *name;
-    bool required;
-    size_t align, bytes;
-    bool written;
-};
-
-kda_status check_bufs(const Buf *b, int n)
-{
-    for (int i = 0; i < n; ++i) {
-        if (!b[i].p) {
-            if (b[i].required) return set_error(KDA_ERR_INVALID_ARG, "%s is NULL", b[i].name);
-        } else if (reinterpret_cast<uintptr_t>(b[i].p) % b[i].align)
-            return set_error(KDA_ERR_INVALID_ARG, "%s is not %zu-byte aligned", b[i].name, b[i].align);
-    }
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; b[i].written && j < n; ++j) {
-            if (j == i || !b[i].p || !b[j].p || !b[i].bytes || !b[j].bytes) continue;
-            const char *x = static_cast<const char *>(b[i].p), *y = static_cast<const char *>(b[j].p);
-            if (x < y + b[j].bytes && y < x + b[i].bytes)
-                return set_error(KDA_ERR_INVALID_ARG, "%s overlaps %s", b[i].name, b[j].name);
-        }
-    return KDA_OK;
-}
-
 gdr::Args base_args(const float *g, const float *beta, const float *S0, const int32_t *cu,
                     int32_t n_seqs, int64_t n_tokens, int32_t Hk, int32_t Hv, int32_t dk,
                     int32_t dv, float scale, void *stream)
@@ -143,8 +108,6 @@ gdr::Args base_args(const float *g, const float *beta, const float *S0, const in
     a.stream = static_cast<hipStream_t>(stream);
     return a;
 }
-
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Parts {
     size_t state, rows;                  // bytes of each of the two state and two row arrays
