@@ -20,6 +20,23 @@ and of the gated delta rule with one decay per head (C ABI: include/gdr.h):
     gdr_bwd_chunked(q, k, v, g, beta, dO, ...) -> (dq, dk, dv, dg, dbeta, dS0)
     gdr_save8(q, k, v) -> Saved8;  gdr_load8(saved) -> (q, k, v)    (inputs kept in 8 bits)
     gdr_bwd_chunked_saved8(saved, g, beta, dO, ...) -> (dq, dk, dv, dg, dbeta, dS0)
+
+of the gated linear recurrence, one number a channel (C ABI: include/glr.h):
+
+    glr_fwd_scan(x, g, h0=None, cu_seqlens=None, ...) -> (h, h_T) or (h, h_T, kept)
+    glr_fwd_scan_gated(x, r, i, rate, ...) -> the same              (gates fused)
+    glr_bwd_scan(x, g, dh, ...) -> (dx, dg, dh0)
+    glr_bwd_scan_gated(x, r, i, rate, dh, ...) -> (dx, dr, di, drate, dh0)
+    glr_decode_step(x, g, S, slots=None, ...) -> h                  (pool S updated in place)
+    glr_decode_step_gated(x, r, i, rate, S, slots=None, ...) -> h
+
+and of the pools of states that the decode steps update (C ABI: include/pool.h):
+
+    pool_alloc(pools, used, n) -> slots                             (free slots taken, zeroed)
+    pool_fork(pools, used, src) -> dst                              (free slots taken for copies)
+    pool_free(used, slots)
+    pool_compact(pools, used, table=None) -> remap
+    pool_copy(from_pools, src, to_pools, dst)
 """
 from __future__ import annotations
 
@@ -31,6 +48,10 @@ from . import _lib
 from ._lib import KDAError, KDA_BF16, KDA_F32, KDA_OK  # noqa: F401
 from .gdr import (Saved8, gdr_bwd_chunked, gdr_bwd_chunked_saved8, gdr_bwd_workspace_bytes,
                   gdr_decode_step, gdr_fwd_chunked, gdr_load8, gdr_save8)
+from .glr import (glr_bwd_scan, glr_bwd_scan_gated, glr_bwd_workspace_bytes, glr_decode_step,
+                  glr_decode_step_gated, glr_fwd_scan, glr_fwd_scan_gated, glr_fwd_workspace_bytes)
+from .pool import (pool_alloc, pool_compact, pool_compact_workspace_bytes, pool_copy, pool_fork,
+                   pool_free)
 
 __all__ = ["kda_fwd_chunked", "kda_fwd_chunked_gated", "kda_fwd_workspace_bytes",
            "kda_bwd_chunked", "kda_bwd_workspace_bytes",
@@ -38,6 +59,11 @@ __all__ = ["kda_fwd_chunked", "kda_fwd_chunked_gated", "kda_fwd_workspace_bytes"
            "kda_decode_verify", "kda_decode_commit", "kda_decode_spec", "KDAError",
            "gdr_fwd_chunked", "gdr_decode_step", "gdr_bwd_chunked", "gdr_bwd_workspace_bytes",
            "gdr_save8", "gdr_load8", "gdr_bwd_chunked_saved8", "Saved8",
+           "glr_fwd_scan", "glr_fwd_scan_gated", "glr_bwd_scan", "glr_bwd_scan_gated",
+           "glr_decode_step", "glr_decode_step_gated", "glr_fwd_workspace_bytes",
+           "glr_bwd_workspace_bytes",
+           "pool_alloc", "pool_fork", "pool_free", "pool_compact", "pool_copy",
+           "pool_compact_workspace_bytes",
            "version", "library_path"]
 
 

@@ -1,4 +1,4 @@
-"""ctypes binding of libkda.so (the C ABI in include/kda.h and include/gdr.h).
+"""ctypes binding of libkda.so (the C ABI in include/kda.h, gdr.h, glr.h and pool.h).
 
 Argument marshalling only: every step of KDA runs in the library's HIP
 kernels.  There is no fallback: if libkda.so is missing or cannot be loaded
@@ -87,6 +87,24 @@ def load() -> ctypes.CDLL:
         lib.gdr_save8.argtypes = [P] * 3 + [I64, I32, I32, I32, I32] + [P] * 7
         lib.gdr_load8.restype = ctypes.c_int
         lib.gdr_load8.argtypes = [P] * 6 + [I64, I32, I32, I32, I32] + [P] * 4
+        seqs = [P, P, I32, I64, I32, U]                 # h0, cu_seqlens, sizes, dtype
+        for name, res, args in (
+                ("glr_kept_bytes", SZ, [I64, I32]), ("glr_fwd_workspace_bytes", SZ, [I64, I32]),
+                ("glr_bwd_workspace_bytes", SZ, [I64, I32]),
+                ("glr_fwd_scan", U, [P] * 2 + seqs + [P] * 4 + [SZ, P]),
+                ("glr_fwd_scan_gated", U, [P] * 4 + seqs + [P] * 4 + [SZ, P]),
+                ("glr_bwd_scan", U, [P] * 2 + seqs + [P] * 7 + [SZ, P]),
+                ("glr_bwd_scan_gated", U, [P] * 4 + seqs + [P] * 9 + [SZ, P]),
+                ("glr_decode_step", U, [P] * 4 + [I32] * 3 + [U, P, P]),
+                ("glr_decode_step_gated", U, [P] * 6 + [I32] * 3 + [U, P, P]),
+                ("pool_copy", U, [P, P, I32, I32, I32, P, P, I32, P]),
+                ("pool_alloc", U, [P, I32, P, I32, I32, P, P]),
+                ("pool_fork", U, [P, I32, P, I32, P, I32, P, P]),
+                ("pool_free", U, [P, I32, P, I32, P]),
+                ("pool_compact_workspace_bytes", SZ, [I32]),
+                ("pool_compact", U, [P, I32, P, I32, P, I64, P, P, SZ, P])):
+            f = getattr(lib, name)
+            f.restype, f.argtypes = res, args
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_last_error.restype = ctypes.c_char_p

@@ -4,7 +4,8 @@
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 instruction
 selection disabled (-packed-fp32-ops), and linked into one shared library
-next to this file.  The C-ABI declarations are in include/kda.h and include/gdr.h.
+next to this file.  The C-ABI declarations are in include/ (kda.h, gdr.h,
+glr.h, pool.h).
 """
 from __future__ import annotations
 
@@ -23,7 +24,9 @@ ARCH = "gfx950"
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill.hip", "kda_noalloc.hip",
            "kda_spec.hip", "kda_backward.hip",
            "gdr_api.cpp", "gdr_decode.hip", "gdr_recurrent.hip", "gdr_grad.hip",
-           "gdr_chunk.hip", "gdr_grad_chunk.hip", "gdr_save8.hip"]
+           "gdr_chunk.hip", "gdr_grad_chunk.hip", "gdr_save8.hip",
+           "glr_api.cpp", "glr_scan.hip", "glr_grad.hip", "glr_decode.hip",
+           "pool_api.cpp", "pool.hip"]
 
 
 def hipcc() -> str:

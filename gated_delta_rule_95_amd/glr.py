@@ -1,0 +1,222 @@
+"""Torch front of the gated linear recurrence entry points (C ABI: include/glr.h).
+
+    glr_fwd_scan(x, g, h0=None, cu_seqlens=None, ...) -> (h, h_T) or (h, h_T, kept)
+    glr_fwd_scan_gated(x, r, i, rate, ...) -> the same             (gates fused)
+    glr_bwd_scan(x, g, dh, ...) -> (dx, dg, dh0)
+    glr_bwd_scan_gated(x, r, i, rate, dh, ...) -> (dx, dr, di, drate, dh0)
+    glr_decode_step(x, g, S, slots=None, ...) -> h                 (pool S updated in place)
+    glr_decode_step_gated(x, r, i, rate, S, slots=None, ...) -> h
+
+Marshalling only: outputs and workspaces are allocated through torch, the
+work runs in the library's kernels on the inputs' device and its current
+stream.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from .gdr import _need, _ptr, _stream
+
+__all__ = ["glr_fwd_scan", "glr_fwd_scan_gated", "glr_bwd_scan", "glr_bwd_scan_gated",
+           "glr_decode_step", "glr_decode_step_gated", "glr_fwd_workspace_bytes",
+           "glr_bwd_workspace_bytes"]
+
+KEPT = 64          # tokens between two kept states
+
+_DT = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
+
+
+def _run(dev: torch.device, fn, *args) -> None:
+    """Calls the library with `dev` current, on its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    if st:
+        _lib.check(st)
+
+
+class _Batch:
+    """Sizes of a batch of x [B, T, D] or packed [N, D]; checks everything
+    whose shape follows from them."""
+
+    def __init__(self, x, gates, cu_seqlens):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("x must be a torch.Tensor")
+        self.dev = dev = x.device
+        if dev.type != "cuda":
+            raise ValueError(f"x is on {dev}: the kernels run on a GPU, there is no CPU fallback")
+        if x.dim() not in (2, 3):
+            raise ValueError("x must be [B, T, D] or [N, D]")
+        if x.dtype not in _DT:
+            raise TypeError(f"unsupported dtype {x.dtype}; the gated linear recurrence takes bfloat16 or float32")
+        self.dt, self.shape = _DT[x.dtype], x.shape
+        self.D = x.shape[-1]
+        if self.D < 1:
+            raise ValueError("x must have a channel")
+        self.N = x.shape[0] if x.dim() == 2 else x.shape[0] * x.shape[1]
+        if cu_seqlens is not None:
+            if x.dim() == 3 and x.shape[0] != 1:
+                raise ValueError("cu_seqlens needs packed input ([N, D] or [1, N, D])")
+            if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+                raise ValueError("cu_seqlens must be a 1-D tensor of n_seqs + 1 entries")
+            _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+            self.n_seqs = cu_seqlens.numel() - 1
+        else:
+            self.n_seqs = x.shape[0] if x.dim() == 3 else 1
+        _need(x, "x", x.dtype, x.shape, dev)
+        if len(gates) == 1:
+            _need(gates[0], "g", torch.float32, x.shape, dev)
+        else:
+            _need(gates[0], "r", x.dtype, x.shape, dev)
+            _need(gates[1], "i", x.dtype, x.shape, dev)
+            _need(gates[2], "rate", torch.float32, (self.D,), dev)
+        self.state = torch.Size((self.n_seqs, self.D))
+        self.kept = torch.Size((-(-self.N // KEPT), self.D))
+
+    def workspace(self, need, given):
+        if given is not None:
+            _need(given, "workspace", torch.uint8, given.shape, self.dev)
+            return given
+        return torch.empty(need, dtype=torch.uint8, device=self.dev) if need else None
+
+
+def glr_fwd_workspace_bytes(n_tokens: int, D: int) -> int:
+    """Bytes of workspace glr_fwd_scan and glr_fwd_scan_gated need for these sizes (0: none)."""
+    return int(_lib.load().glr_fwd_workspace_bytes(n_tokens, D))
+
+
+def glr_bwd_workspace_bytes(n_tokens: int, D: int) -> int:
+    """Bytes of workspace glr_bwd_scan and glr_bwd_scan_gated need for these sizes (0: none)."""
+    return int(_lib.load().glr_bwd_workspace_bytes(n_tokens, D))
+
+
+def _fwd(fn, x, gates, h0, cu_seqlens, output_final_state, keep, h, h_T, workspace):
+    b = _Batch(x, gates, cu_seqlens)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, b.state, b.dev)
+    if h is None:
+        h = torch.empty_like(x)
+    else:
+        _need(h, "h", x.dtype, x.shape, b.dev)
+    if h_T is not None:
+        _need(h_T, "h_T", torch.float32, b.state, b.dev)
+    elif output_final_state:
+        h_T = torch.empty(b.state, dtype=torch.float32, device=b.dev)
+    kept = torch.empty(b.kept, dtype=torch.float32, device=b.dev) if keep else None
+    ws = b.workspace(_lib.load().glr_fwd_workspace_bytes(b.N, b.D), workspace)
+    _run(b.dev, fn, _ptr(x), *(_ptr(t) for t in gates), _ptr(h0), _ptr(cu_seqlens), b.n_seqs, b.N, b.D, b.dt,
+         _ptr(h), _ptr(h_T), _ptr(kept), _ptr(ws), 0 if ws is None else ws.numel())
+    return (h, h_T, kept) if keep else (h, h_T)
+
+
+def glr_fwd_scan(x: torch.Tensor, g: torch.Tensor, h0: Optional[torch.Tensor] = None,
+                 cu_seqlens: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                 keep: bool = False, h: Optional[torch.Tensor] = None,
+                 h_T: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                 ) -> Tuple[Optional[torch.Tensor], ...]:
+    """h_t = exp(g_t) h_{t-1} + x_t for each channel, over a batch of sequences.
+
+    x  : [B, T, D] or packed [N, D] (bf16 or fp32)
+    g  : like x, fp32 log-decay <= 0 (-inf allowed)
+    h0 : [n_seqs, D] fp32 or None
+    cu_seqlens : int32 [n_seqs + 1] on the device (packed input only); rows of tokens behind
+        its last entry are left as they are in a given h, unset in one allocated here
+    keep : also return what the backward wants, the state before every 64th token of the batch
+    Returns (h in x's dtype, h_T fp32 or None), with keep (h, h_T, kept).
+    """
+    return _fwd(_lib.load().glr_fwd_scan, x, (g,), h0, cu_seqlens, output_final_state, keep, h, h_T, workspace)
+
+
+def glr_fwd_scan_gated(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, rate: torch.Tensor,
+                       h0: Optional[torch.Tensor] = None,
+                       cu_seqlens: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                       keep: bool = False, h: Optional[torch.Tensor] = None,
+                       h_T: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None
+                       ) -> Tuple[Optional[torch.Tensor], ...]:
+    """h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t with a_t = exp(-rate
+    sigmoid(r_t)), the gates formed inside.  r, i : like x; rate : [D] fp32 >= 0;
+    the rest as in glr_fwd_scan."""
+    return _fwd(_lib.load().glr_fwd_scan_gated, x, (r, i, rate), h0, cu_seqlens, output_final_state, keep, h, h_T,
+                workspace)
+
+
+def _bwd(fn, x, gates, dh, h0, dh_T, cu_seqlens, kept, workspace):
+    b = _Batch(x, gates, cu_seqlens)
+    _need(dh, "dh", x.dtype, x.shape, b.dev)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, b.state, b.dev)
+    if dh_T is not None:
+        _need(dh_T, "dh_T", torch.float32, b.state, b.dev)
+    if kept is not None:
+        _need(kept, "kept", torch.float32, b.kept, b.dev)
+    ws = b.workspace(_lib.load().glr_bwd_workspace_bytes(b.N, b.D), workspace)
+    # the gradients of x and of the gates are shaped like them
+    out = [torch.empty_like(x)] + [torch.empty_like(t) for t in gates]
+    out.append(torch.empty(b.state, dtype=torch.float32, device=b.dev))
+    _run(b.dev, fn, _ptr(x), *(_ptr(t) for t in gates), _ptr(h0), _ptr(cu_seqlens), b.n_seqs, b.N, b.D, b.dt,
+         _ptr(kept), _ptr(dh), _ptr(dh_T), *(_ptr(t) for t in out), _ptr(ws), 0 if ws is None else ws.numel())
+    return tuple(out)
+
+
+def glr_bwd_scan(x: torch.Tensor, g: torch.Tensor, dh: torch.Tensor,
+                 h0: Optional[torch.Tensor] = None, dh_T: Optional[torch.Tensor] = None,
+                 cu_seqlens: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, ...]:
+    """Gradients of glr_fwd_scan: dx in x's dtype, dg and dh0 in fp32.  dh has
+    h's shape and dtype, dh_T is the final states' cotangent or None, kept is
+    what the forward of these inputs returned (formed again where None).  Rows
+    of tokens behind cu_seqlens' last entry are unset.  The workspace (uint8)
+    is allocated through torch unless given."""
+    return _bwd(_lib.load().glr_bwd_scan, x, (g,), dh, h0, dh_T, cu_seqlens, kept, workspace)
+
+
+def glr_bwd_scan_gated(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, rate: torch.Tensor,
+                       dh: torch.Tensor, h0: Optional[torch.Tensor] = None,
+                       dh_T: Optional[torch.Tensor] = None,
+                       cu_seqlens: Optional[torch.Tensor] = None,
+                       kept: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, ...]:
+    """Gradients of glr_fwd_scan_gated: dx, dr, di in x's dtype, drate [D]
+    (summed over the tokens) and dh0 in fp32; the rest as in glr_bwd_scan."""
+    return _bwd(_lib.load().glr_bwd_scan_gated, x, (r, i, rate), dh, h0, dh_T, cu_seqlens, kept, workspace)
+
+
+def _decode(fn, x, gates, S, slots, h):
+    if isinstance(x, torch.Tensor) and x.dim() != 2:
+        raise ValueError("x must be [N, D]")
+    b = _Batch(x, gates, None)
+    if not isinstance(S, torch.Tensor) or S.dim() != 2:
+        raise ValueError("S must be [n_slots, D]")
+    _need(S, "S", torch.float32, S.shape[:1] + b.shape[1:], b.dev)
+    if slots is not None:
+        _need(slots, "slots", torch.int32, x.shape[:1], b.dev)
+    if h is None:
+        h = torch.empty_like(x)
+    else:
+        _need(h, "h", x.dtype, x.shape, b.dev)
+    _run(b.dev, fn, _ptr(x), *(_ptr(t) for t in gates), _ptr(S), _ptr(slots), S.shape[0], b.N, b.D, b.dt, _ptr(h))
+    return h
+
+
+def glr_decode_step(x: torch.Tensor, g: torch.Tensor, S: torch.Tensor,
+                    slots: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None
+                    ) -> torch.Tensor:
+    """One token for each request.  x [N, D]; g [N, D] fp32; S : a pool
+    [n_slots, D] fp32, updated in place; slots : int32 [N] on the device, each
+    request's state (all different; one outside the pool marks a padded row,
+    whose h is zeros), or None for states 0 .. N - 1.  Returns h in x's dtype."""
+    return _decode(_lib.load().glr_decode_step, x, (g,), S, slots, h)
+
+
+def glr_decode_step_gated(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, rate: torch.Tensor,
+                          S: torch.Tensor, slots: Optional[torch.Tensor] = None,
+                          h: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """glr_decode_step with the gates of glr_fwd_scan_gated formed inside: r, i
+    like x, rate [D] fp32."""
+    return _decode(_lib.load().glr_decode_step_gated, x, (r, i, rate), S, slots, h)

@@ -30,10 +30,13 @@ Modules
               gradients, and q, k, v in 8 bits
   gdr_chunked the same in chunks, with operands held in few parts or terms
               left out on request: what the GPU tests' tolerances must reject
+  glr         the gated linear recurrence (one number a channel), plain and
+              gated, and its gradients
 
 Every function is pinned (``tests/test_oracle_pins.py``, ``tests/test_oracle_spec.py``,
 ``tests/test_oracle_prologue.py``, ``tests/test_oracle_backward.py``,
-``tests/test_oracle_gdr.py``, ``tests/test_oracle_gdr_chunked.py``) against facts that
+``tests/test_oracle_gdr.py``, ``tests/test_oracle_gdr_chunked.py``,
+``tests/test_oracle_glr.py``) against facts that
 do not come from the oracle itself (closed forms, a hand-derived example,
 retrieval identities, brute force, invariants); none is "parity unpinned".
 """

@@ -1,0 +1,139 @@
+"""CPU tests of the gated linear recurrence's C ABI: exports, and the refusal
+of bad arguments before anything reaches the GPU (no compute call is made
+here)."""
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+from gated_delta_rule_95_amd import _lib
+
+P = 0x1000000      # a fake, aligned address: every call below fails before any launch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+@pytest.mark.parametrize("header,prefix", [("glr.h", "glr_"), ("pool.h", "pool_")])
+def test_exports_match_header(lib, header, prefix):
+    with open(os.path.join(os.path.dirname(_lib.HEADER), header)) as f:
+        src = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    declared = sorted(set(re.findall(r"\b(" + prefix + r"[a-z0-9_]+)\s*\(", src)))
+    out = subprocess.run(["nm", "-D", "--defined-only", _lib.LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    exported = sorted({ln.split()[-1] for ln in out.splitlines()
+                       if " T " in ln and ln.split()[-1].startswith(prefix)})
+    assert exported == declared
+    for name in declared:
+        assert getattr(lib, name).argtypes
+
+
+def fwd(lib, gated, **kw):
+    a = dict(x=P, r=2 * P, i=3 * P, rate=4 * P, g=5 * P, h0=None, cu=None, n=1, N=300, D=16, dt=1, h=6 * P, hT=None,
+             kept=None, ws=64 * P, wsb=1 << 30)
+    a.update(kw)
+    gates = (a["r"], a["i"], a["rate"]) if gated else (a["g"],)
+    f = lib.glr_fwd_scan_gated if gated else lib.glr_fwd_scan
+    return f(a["x"], *gates, a["h0"], a["cu"], a["n"], a["N"], a["D"], a["dt"], a["h"], a["hT"], a["kept"], a["ws"],
+             a["wsb"], None)
+
+
+def bwd(lib, gated, **kw):
+    a = dict(x=P, r=2 * P, i=3 * P, rate=4 * P, g=5 * P, h0=None, cu=None, n=1, N=300, D=16, dt=1, kept=None, dh=6 * P,
+             dhT=None, dx=7 * P, dr=8 * P, di=9 * P, drate=10 * P, dg=11 * P, dh0=12 * P, ws=64 * P, wsb=1 << 30)
+    a.update(kw)
+    gates = (a["r"], a["i"], a["rate"]) if gated else (a["g"],)
+    outs = (a["dx"], a["dr"], a["di"], a["drate"]) if gated else (a["dx"], a["dg"])
+    f = lib.glr_bwd_scan_gated if gated else lib.glr_bwd_scan
+    return f(a["x"], *gates, a["h0"], a["cu"], a["n"], a["N"], a["D"], a["dt"], a["kept"], a["dh"], a["dhT"], *outs,
+             a["dh0"], a["ws"], a["wsb"], None)
+
+
+SIZES = [(dict(D=0), "D must"), (dict(n=-1), "n_seqs"), (dict(N=-1), "n_tokens"), (dict(N=(1 << 31) - 255), "2^31"),
+         (dict(n=7), "multiple"), (dict(n=0), "n_seqs == 0"), (dict(dt=7), "in_dtype"),
+         (dict(N=1 << 30, D=1 << 10), "2^40"), (dict(n=1 << 30, D=1 << 10, N=0), "2^40"),
+         (dict(N=1 << 28, D=64), "2^22"), (dict(N=1 << 17, D=1 << 17), "2^22"),
+         (dict(x=None), "x is NULL"), (dict(x=P + 1), "aligned"), (dict(h0=20 * P + 2), "aligned"),
+         (dict(cu=20 * P + 2), "aligned"), (dict(kept=20 * P + 2), "aligned")]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kw,msg", SIZES + [
+    (dict(h=P), "overlaps"), (dict(hT=6 * P), "overlaps"), (dict(kept=6 * P + 64), "overlaps"), (dict(h=6 * P + 1), "aligned"),
+    (dict(h0=20 * P, hT=20 * P), "overlaps"), (dict(hT=20 * P + 2), "aligned")])
+def test_fwd_refusals(lib, gated, kw, msg):
+    assert fwd(lib, gated, **kw) == 1
+    assert msg in _lib.last_error()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kw,msg", SIZES + [
+    (dict(dh=None), "dh is NULL"), (dict(dx=None), "dx is NULL"), (dict(dx=P), "overlaps"), (dict(dx=6 * P), "overlaps"),
+    (dict(kept=20 * P, dh0=20 * P), "overlaps"), (dict(dhT=12 * P), "overlaps"), (dict(dx=7 * P + 1), "aligned"),
+    (dict(ws=64 * P + 16), "aligned"), (dict(ws=7 * P), "overlaps"), (dict(ws=None), "workspace is NULL"),
+    (dict(wsb=64), "below")])
+def test_bwd_refusals(lib, gated, kw, msg):
+    assert bwd(lib, gated, **kw) == 1
+    assert msg in _lib.last_error()
+
+
+def test_refusals_of_the_gates(lib):
+    for kw, msg in ((dict(r=None), "r is NULL"), (dict(i=None), "i is NULL"), (dict(rate=None), "rate is NULL"),
+                    (dict(r=2 * P + 1), "aligned"), (dict(rate=4 * P + 2), "aligned")):
+        assert fwd(lib, True, **kw) == 1 and msg in _lib.last_error()
+        assert bwd(lib, True, **kw) == 1 and msg in _lib.last_error()
+    for kw, msg in ((dict(dr=None), "dr is NULL"), (dict(di=7 * P), "overlaps"), (dict(drate=None), "drate is NULL")):
+        assert bwd(lib, True, **kw) == 1 and msg in _lib.last_error()
+    for kw, msg in ((dict(g=None), "g is NULL"), (dict(dg=None), "dg is NULL"), (dict(g=5 * P + 2), "aligned")):
+        assert bwd(lib, False, **kw) == 1 and msg in _lib.last_error()
+
+
+def test_nothing_to_do_is_ok(lib):
+    for gated in (False, True):
+        assert fwd(lib, gated, n=0, N=0) == 0 and _lib.last_error() == ""
+        assert dec(lib, gated, N=0) == 0
+
+
+def dec(lib, gated, **kw):
+    a = dict(x=P, r=2 * P, i=3 * P, rate=4 * P, g=5 * P, S=8 * P, slots=None, ns=2, N=2, D=16, dt=1, h=6 * P)
+    a.update(kw)
+    gates = (a["r"], a["i"], a["rate"]) if gated else (a["g"],)
+    f = lib.glr_decode_step_gated if gated else lib.glr_decode_step
+    return f(a["x"], *gates, a["S"], a["slots"], a["ns"], a["N"], a["D"], a["dt"], a["h"], None)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kw,msg", [
+    (dict(S=None), "S is NULL"), (dict(N=-1), "N must"), (dict(ns=-1), "n_slots"), (dict(ns=1), "without slots"),
+    (dict(D=0), "D must"), (dict(S=P), "overlaps"), (dict(S=8 * P + 2), "aligned"), (dict(slots=7 * P + 1), "aligned"),
+    (dict(h=P), "overlaps"), (dict(slots=8 * P), "overlaps"), (dict(h=None), "h is NULL"), (dict(dt=2), "in_dtype"),
+    (dict(ns=1 << 30, D=1 << 10), "2^40"), (dict(x=None), "x is NULL")])
+def test_decode_refusals(lib, gated, kw, msg):
+    assert dec(lib, gated, **kw) == 1
+    assert msg in _lib.last_error()
+
+
+def test_sizes_of_workspaces_and_kept_states(lib):
+    import gated_delta_rule_95_amd as m
+    assert lib.glr_kept_bytes(0, 5) == 0 and lib.glr_kept_bytes(1, 5) == 20 and lib.glr_kept_bytes(129, 5) == 60
+    for f in (m.glr_fwd_workspace_bytes, m.glr_bwd_workspace_bytes):
+        assert f(0, 16) == 0 and f(1 << 20, 16) <= f(1 << 21, 16)
+        for bad in ((-1, 16), (16, 0), (1 << 31, 1)):
+            assert f(*bad) == 0
+
+
+def test_python_refuses_cpu_tensors_and_types():
+    import gated_delta_rule_95_amd as m
+    x, g = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, 16)
+    for call in (lambda: m.glr_fwd_scan(x, g), lambda: m.glr_bwd_scan(x, g, x), lambda: m.glr_decode_step(x, g, g),
+                 lambda: m.glr_fwd_scan_gated(x, x, x, g[0]), lambda: m.pool_alloc([g], torch.zeros(4, dtype=torch.bool), 1),
+                 lambda: m.pool_copy([g], torch.zeros(1, dtype=torch.int32), [g], torch.zeros(1, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="no CPU fallback"):
+            call()
+    for call in (lambda: m.glr_fwd_scan([1.0], g), lambda: m.pool_free([True], x), lambda: m.pool_copy(g, [0], g, [0])):
+        with pytest.raises(TypeError):
+            call()
