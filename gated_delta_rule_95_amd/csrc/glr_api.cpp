@@ -18,7 +18,7 @@ using api::ok;
 using api::set_error;
 
 // The products keep every byte count below 2^63 and launches below 2^32
-// threads (512 a tile of 64 tokens and 64 channels).
+// threads (512 a tile of 64 tokens and 64 channels, 512 for 64 sequences).
 kda_status check_sizes(int64_t n_tokens, int32_t D)
 {
     if (D < 1) return set_error(KDA_ERR_INVALID_ARG, "D must be >= 1 (got %d)", D);
@@ -36,6 +36,7 @@ kda_status check_sizes(int64_t n_tokens, int32_t D)
 kda_status check_seqs(int32_t n_seqs, int64_t n_tokens, int32_t D, const int32_t *cu)
 {
     if (n_seqs < 0) return set_error(KDA_ERR_INVALID_ARG, "n_seqs must be >= 0 (got %d)", n_seqs);
+    if (n_seqs >= 1 << 27) return set_error(KDA_ERR_INVALID_ARG, "n_seqs must be below 2^27 (got %d)", n_seqs);
     if ((int64_t)n_seqs * D >= (int64_t)1 << 40)
         return set_error(KDA_ERR_INVALID_ARG, "n_seqs * D must be below 2^40");
     if (n_seqs == 0 && n_tokens != 0)

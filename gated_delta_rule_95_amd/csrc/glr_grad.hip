@@ -73,9 +73,14 @@ void launch_t(const Args &a)
 
 }  // namespace
 
-size_t bwd_workspace(int64_t n_tokens, int32_t D)
+static size_t kept_part(int64_t n_tokens, int32_t D)
 {
     return ((size_t)((n_tokens + kKept - 1) / kKept) * D * 4 + 255) & ~(size_t)255;
+}
+
+size_t bwd_workspace(int64_t n_tokens, int32_t D)
+{
+    return kept_part(n_tokens, D) + fwd_workspace(n_tokens, D);
 }
 
 hipError_t launch_bwd(const Args &arg)
@@ -86,6 +91,7 @@ hipError_t launch_bwd(const Args &arg)
         Args f = a;
         f.h = nullptr;
         f.h_T = nullptr;
+        f.ws = static_cast<char *>(a.ws) + kept_part(a.n_tokens, a.D);
         const hipError_t e = launch_fwd(f);
         if (e != hipSuccess) return e;
     }

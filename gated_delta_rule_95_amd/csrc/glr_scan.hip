@@ -1,55 +1,217 @@
-// Gated linear recurrence, forward: one thread per (sequence, channel), token
-// after token.
-#include "glr_device.h"
+// Gated linear recurrence, forward.
+//
+// A tile is 128 tokens by 64 V channels, one workgroup: each of eight waves
+// takes 16 tokens in registers (each lane V channels), forms their factors
+// and inputs, and folds them into one map h -> A h + B.  The waves' maps meet
+// in the LDS, the tile's goes to the tiles behind it (glr_tiles.h), the state
+// that comes in is looked up from the tiles before it, and every wave runs
+// its 16 tokens once more from the state that reaches it and stores them.
+// Everything is read and written once, by one launch, however the batch is
+// cut into sequences: a sequence's first token forgets what came before it,
+// so borders cost nothing elsewhere.
+#include "glr_tiles.h"
 
 namespace glr {
 namespace {
 
-constexpr int NT = 64;
+constexpr int NW = 8, K = 16, C = NW * K, NT = NW * WAVE;
 
-template <typename T, bool GATED>
-__global__ __launch_bounds__(NT) void glr_scan_kernel(Args a)
+template <typename T, bool GATED, int V>
+__global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
 {
-    const int c = blockIdx.x * NT + threadIdx.x, D = a.D;
-    if (c >= D) return;
+    typedef Row<T, V> R;
+    typedef Row<float, V> RF;
+    __shared__ int s_idx, s_first[C], s_last[C];
+    __shared__ Map s_map[NW][WAVE * V];
+    __shared__ float s_in[WAVE * V];
+    const int tid = threadIdx.x, lane = tid % WAVE, w = __builtin_amdgcn_readfirstlane(tid / WAVE), D = a.D;
     const gdr::SeqArgs sa = seq_args(a);
-    const T *x = static_cast<const T *>(a.x), *rp = static_cast<const T *>(a.r), *ip = static_cast<const T *>(a.i);
-    T *out = static_cast<T *>(a.h);
-    for (int n = blockIdx.y; n < a.n_seqs; n += gridDim.y) {
-        const gdr::Seq s = gdr::seq_of(sa, n);
-        float h = a.h0 ? a.h0[(int64_t)n * D + c] : 0.f;
-        const float nr = GATED && s.len ? -a.rate[c] : 0.f;
-        for (int t = s.bos; t < s.bos + s.len; ++t) {
-            const int64_t at = (int64_t)t * D + c;
-            if (a.kept && t % kKept == 0) a.kept[(int64_t)(t / kKept) * D + c] = h;
-            const float xv = kda::Elem<T>::ld(x + at);
-            if (GATED) {
-                const Gates gt = gates(kda::Elem<T>::ld(rp + at), kda::Elem<T>::ld(ip + at), nr);
-                h = __builtin_fmaf(gt.a, h, gt.b * xv);
-            } else
-                h = __builtin_fmaf(decay(a.g[at]), h, xv);
-            if (out) kda::Elem<T>::st(out + at, h);
+    if (tid == 0) s_idx = chain.ticket ? (int)atomicAdd(chain.ticket, 1u) : (int)blockIdx.x;
+    if (tid < C) s_first[tid] = s_last[tid] = -1;
+    const int total = total_tokens(sa);
+    __syncthreads();
+    const int idx = __builtin_amdgcn_readfirstlane(s_idx);
+    if (idx >= chain.tiles * chain.blocks) {
+        empty_states(sa, idx - chain.tiles * chain.blocks, D, a.h0, a.h_T, NT);
+        return;
+    }
+    const int tile = idx / chain.blocks, t0 = tile * C;
+    if (t0 >= total) return;
+    const int count = total - t0 < C ? total - t0 : C;
+    const int c = (idx - tile * chain.blocks) * WAVE * V + lane * V;
+    const bool active = c < D;
+    const int cc = active ? c : 0;
+    const int tw = t0 + w * K, mine = count - w * K < 0 ? 0 : count - w * K < K ? count - w * K : K;
+
+    typename R::raw rx[K], rr[K], ri[K];
+    typename RF::raw rg[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t row = (int64_t)(k < mine ? tw + k : t0) * D;
+        rx[k] = R::ld(static_cast<const T *>(a.x) + row + cc);
+        if constexpr (GATED) {
+            rr[k] = R::ld(static_cast<const T *>(a.r) + row + cc);
+            ri[k] = R::ld(static_cast<const T *>(a.i) + row + cc);
+        } else
+            rg[k] = RF::ld(a.g + row + cc);
+    }
+    float nr[V];
+    if constexpr (GATED) {
+        const typename RF::raw rate = RF::ld(a.rate + cc);
+#pragma unroll
+        for (int j = 0; j < V; ++j) nr[j] = -RF::get(rate, j);
+    }
+    if (w == 0) mark_borders(sa, t0, C, lane, s_first, s_last);
+    __syncthreads();
+    const uint64_t starts = __ballot(lane < K && s_first[w * K + lane % K] >= 0);
+    const uint64_t ends = __ballot(lane < K && s_last[w * K + lane % K] >= 0);
+
+    float al[K][V], u[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if constexpr (GATED) {
+                const Gates g = gates(R::get(rr[k], j), R::get(ri[k], j), nr[j]);
+                al[k][j] = g.a;
+                u[k][j] = g.b * R::get(rx[k], j);
+            } else {
+                al[k][j] = decay(RF::get(rg[k], j));
+                u[k][j] = R::get(rx[k], j);
+            }
         }
-        if (a.h_T) a.h_T[(int64_t)n * D + c] = h;
+    Map m[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) m[j] = Map{1.f, 0.f};
+    const bool plain = starts == 0 && mine == K;
+    if (plain) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) m[j] = Map{m[j].A * al[k][j], __builtin_fmaf(al[k][j], m[j].B, u[k][j])};
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool start = starts >> k & 1;
+            if (start && a.h0) {
+                const int n = __builtin_amdgcn_readfirstlane(s_first[w * K + k]);
+                const typename RF::raw h0 = RF::ld(a.h0 + (int64_t)n * D + cc);
+#pragma unroll
+                for (int j = 0; j < V; ++j) u[k][j] = __builtin_fmaf(al[k][j], RF::get(h0, j), u[k][j]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (k >= mine) {
+                    al[k][j] = 1.f;
+                    u[k][j] = 0.f;
+                }
+                m[j] = start ? Map{kForget, u[k][j]} : Map{m[j].A * al[k][j], __builtin_fmaf(al[k][j], m[j].B, u[k][j])};
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_map[w][lane * V + j] = m[j];
+    __syncthreads();
+
+    if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < NW; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) m[j] = after(s_map[i][lane * V + j], m[j]);
+        const bool more = chain.ticket && t0 + C < total;       // a tile behind this one
+        const bool alone = tile == 0 || s_first[0] >= 0;        // nothing comes in
+        uint64_t *p = chain.words + (int64_t)tile * D + cc;
+        float in[V];
+        if (alone) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                in[j] = 0.f;
+                if (more && active) put(p + j, Map{kForget, m[j].B});
+            }
+        } else {
+            if (more && active)
+#pragma unroll
+                for (int j = 0; j < V; ++j) put(p + j, m[j]);
+            look_back<V>(p - D, -(int64_t)D, tile, active, in);
+            if (more && active)
+#pragma unroll
+                for (int j = 0; j < V; ++j) put(p + j, Map{kForget, m[j](in[j])});
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) s_in[lane * V + j] = in[j];
+    }
+    __syncthreads();
+
+    float h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        h[j] = s_in[lane * V + j];
+        for (int i = 0; i < w; ++i) h[j] = s_map[i][lane * V + j](h[j]);
+    }
+    if (!active || mine == 0) return;
+    if (a.kept && w * K % kKept == 0) RF::st(a.kept + (int64_t)(tw / kKept) * D + c, h);
+    T *out = static_cast<T *>(a.h);
+    if (plain && !ends) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = __builtin_fmaf(al[k][j], h[j], u[k][j]);
+            if (out) R::st(out + (int64_t)(tw + k) * D + c, h);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (k >= mine) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = starts >> k & 1 ? u[k][j] : __builtin_fmaf(al[k][j], h[j], u[k][j]);
+            if (out) R::st(out + (int64_t)(tw + k) * D + c, h);
+            if (a.h_T && (ends >> k & 1)) {
+                const int n = __builtin_amdgcn_readfirstlane(s_last[w * K + k]);
+                RF::st(a.h_T + (int64_t)n * D + c, h);
+            }
+        }
     }
 }
 
-template <typename T>
-void launch_t(const Args &a)
+__global__ __launch_bounds__(256) void glr_clear_kernel(Chain c, int64_t words)
 {
-    const dim3 grid((a.D + NT - 1) / NT, a.n_seqs < 65535 ? a.n_seqs : 65535);
-    if (a.gated) hipLaunchKernelGGL((glr_scan_kernel<T, true>), grid, dim3(NT), 0, a.stream, a);
-    else hipLaunchKernelGGL((glr_scan_kernel<T, false>), grid, dim3(NT), 0, a.stream, a);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *c.ticket = 0;
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256)
+        c.words[i] = kEmpty;
+}
+
+int64_t tiles_of(int64_t n_tokens) { return (n_tokens + C - 1) / C; }
+
+template <typename T, bool GATED>
+void launch_v(const Args &a, const Chain &ch, int64_t groups, int V, hipStream_t s)
+{
+    const dim3 grid((unsigned)((int64_t)ch.tiles * ch.blocks + groups));
+    if (V == 2) hipLaunchKernelGGL((glr_scan_kernel<T, GATED, 2>), grid, dim3(NT), 0, s, a, ch);
+    else hipLaunchKernelGGL((glr_scan_kernel<T, GATED, 1>), grid, dim3(NT), 0, s, a, ch);
 }
 
 }  // namespace
 
-size_t fwd_workspace(int64_t, int32_t) { return 0; }
+hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s)
+{
+    if (!c.ticket) return hipSuccess;
+    const int64_t words = (int64_t)c.tiles * D, blocks = (words + 1023) / 1024;
+    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, c, words);
+    return hipGetLastError();
+}
+
+size_t fwd_workspace(int64_t n_tokens, int32_t D) { return chain_bytes(tiles_of(n_tokens), D); }
 
 hipError_t launch_fwd(const Args &a)
 {
-    if (a.bf16) launch_t<bf16>(a);
-    else launch_t<float>(a);
+    const int V = pairs(a) ? 2 : 1;
+    const Chain ch = make_chain(a.ws, (int)tiles_of(a.n_tokens), (a.D + WAVE * V - 1) / (WAVE * V));
+    const int64_t groups = empty_groups(a, a.h_T);
+    if ((int64_t)ch.tiles * ch.blocks + groups == 0) return hipSuccess;
+    const hipError_t e = clear_chain(ch, a.D, a.stream);
+    if (e != hipSuccess) return e;
+    if (a.bf16) a.gated ? launch_v<bf16, true>(a, ch, groups, V, a.stream) : launch_v<bf16, false>(a, ch, groups, V, a.stream);
+    else a.gated ? launch_v<float, true>(a, ch, groups, V, a.stream) : launch_v<float, false>(a, ch, groups, V, a.stream);
     return hipGetLastError();
 }
 

@@ -1,0 +1,206 @@
+// What the scan and its gradients share: tiles of tokens and channels handed
+// out in order, sequence borders inside a tile, and the chain of states from
+// tile to tile (gfx950 only).
+#pragma once
+
+#include "glr_device.h"
+
+namespace glr {
+
+// V neighbouring channels of a row, as stored and in fp32
+template <typename T, int V> struct Row {
+    typedef T raw __attribute__((ext_vector_type(V)));
+    static __device__ __forceinline__ raw ld(const T *p) { return *reinterpret_cast<const raw *>(p); }
+    static __device__ __forceinline__ float get(raw x, int j) { return (float)x[j]; }
+    static __device__ __forceinline__ void st(T *p, const float *x)
+    {
+        raw v;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = (T)x[j];
+        *reinterpret_cast<raw *>(p) = v;
+    }
+};
+template <typename T> struct Row<T, 1> {
+    typedef T raw;
+    static __device__ __forceinline__ raw ld(const T *p) { return *p; }
+    static __device__ __forceinline__ float get(raw x, int) { return (float)x; }
+    static __device__ __forceinline__ void st(T *p, const float *x) { *p = (T)x[0]; }
+};
+
+// An affine map h -> A h + B of a channel's state.  A = -0 forgets: whatever
+// comes in, infinities and NaN of another sequence included, goes nowhere.  (A
+// product of factors that is too small for fp32 is +0 and forgets no NaN.)
+constexpr float kForget = -0.f;
+struct Map {
+    float A, B;
+    __device__ __forceinline__ bool forgets() const { return __float_as_uint(A) == 0x80000000u; }
+    __device__ __forceinline__ float operator()(float h) const
+    {
+        return forgets() ? B : __builtin_fmaf(A, h, B);
+    }
+};
+// `late` after `early`
+__device__ __forceinline__ Map after(const Map &late, const Map &early)
+{
+    return Map{late.forgets() || early.forgets() ? kForget : late.A * early.A, late(early.B)};
+}
+
+// Maps travel between workgroups as one 64-bit word that is stored and loaded
+// whole, so a word is either empty or a map, and no order between words is
+// asked for.  kEmpty is a NaN that no A is stored as.
+constexpr uint64_t kEmpty = ~(uint64_t)0;
+__device__ __forceinline__ void put(uint64_t *p, const Map &m)
+{
+    const uint32_t a = m.A != m.A ? 0x7fc00000u : __float_as_uint(m.A);
+    __hip_atomic_store(p, (uint64_t)a << 32 | __float_as_uint(m.B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t *p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ Map map_of(uint64_t w)
+{
+    return Map{__uint_as_float((uint32_t)(w >> 32)), __uint_as_float((uint32_t)w)};
+}
+
+// Workspace of a chain: a ticket, then one word for each tile and channel.
+struct Chain {
+    uint32_t *ticket;                    // nullptr: one tile, which needs no chain
+    uint64_t *words;
+    int tiles, blocks;                   // of tokens, of channels
+};
+constexpr size_t kChainHead = 256;
+inline size_t chain_bytes(int64_t tiles, int32_t D)
+{
+    return tiles > 1 ? kChainHead + (((size_t)tiles * D * 8 + 255) & ~(size_t)255) : 0;
+}
+inline Chain make_chain(void *ws, int tiles, int blocks)
+{
+    if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks};
+    return Chain{static_cast<uint32_t *>(ws),
+                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + kChainHead), tiles, blocks};
+}
+hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s);
+
+// The state (or cotangent) that comes into a tile: the maps of the tiles
+// before it, nearest first, until one forgets or there is none left.  Words
+// of `n` tiles lie `step` apart, from `p` on.  Waits for words that are
+// empty: every tile before this one was handed out earlier, to a workgroup
+// that runs and stores its map before it waits itself, so each wait ends.
+template <int V>
+__device__ __forceinline__ void look_back(const uint64_t *p, int64_t step, int n, bool active, float *in)
+{
+    constexpr int W = 8;
+    Map m[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) m[j] = Map{active ? 1.f : kForget, 0.f};
+    int at = 0;
+    while (at < n) {
+        uint64_t w[W][V];
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[i][j] = peek(p + step * (at + i < n ? at + i : n - 1) + j);
+        bool go = true, forgets = true;
+        int seen = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            bool there = true;
+#pragma unroll
+            for (int j = 0; j < V; ++j) there = there && w[i][j] != kEmpty;
+            go = go && at + i < n && __all(there || !active);
+            if (!go) continue;
+            ++seen;
+#pragma unroll
+            for (int j = 0; j < V; ++j) m[j] = after(m[j], map_of(w[i][j]));
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) forgets = forgets && m[j].forgets();
+        if (__all(forgets)) break;
+        at += seen;
+        if (!seen) __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) in[j] = m[j].B;
+}
+
+// Borders of sequences inside tokens [t0, t0 + C): first[k] = the sequence
+// whose first token is t0 + k, last[k] = the one whose last it is (entries
+// that are neither keep the -1 that the caller put there).  One wave; a table
+// that breaks its contract gives any sequences, but only such as there are.
+__device__ __forceinline__ void mark_borders(const gdr::SeqArgs &s, int t0, int C, int lane, int *first, int *last)
+{
+    if (!s.cu_seqlens) {
+        for (int k = lane; k < C; k += WAVE) {
+            const unsigned t = (unsigned)(t0 + k), n = t / (unsigned)s.seqlen, at = t - n * (unsigned)s.seqlen;
+            if (t >= (unsigned)s.n_tokens) break;
+            if (at == 0) first[k] = (int)n;
+            if (at + 1 == (unsigned)s.seqlen) last[k] = (int)n;
+        }
+        return;
+    }
+    // the count of sequences that end at or before t0, 64 at a time
+    int lo = 0, hi = s.n_seqs;
+    while (lo < hi) {
+        const int step = (hi - lo + WAVE - 1) / WAVE;
+        const int64_t n = lo + (int64_t)lane * step;
+        const int ended = __popcll(__ballot(n < hi && gdr::seq_edge(s, (int)(n < hi ? n : lo) + 1) <= t0));
+        const int64_t next = lo + (int64_t)ended * step;
+        if (ended) lo += (ended - 1) * step + 1;
+        hi = next < hi ? (int)next : hi;
+    }
+    for (int64_t base = lo; base < s.n_seqs; base += WAVE) {
+        const int64_t n = base + lane;
+        int b = t0 + C;
+        if (n < s.n_seqs) {
+            b = gdr::seq_edge(s, (int)n);
+            const int e = gdr::seq_edge(s, (int)n + 1);
+            if (e > b) {
+                if (b >= t0 && b - t0 < C) first[b - t0] = (int)n;
+                if (e - 1 >= t0 && e - 1 - t0 < C) last[e - 1 - t0] = (int)n;
+            }
+        }
+        if (__any(b - t0 >= C)) break;
+    }
+}
+
+// States of empty sequences: to[n] = from[n] (zeros where from is nullptr) for
+// those of 64 sequences that have no token.
+__device__ __forceinline__ void empty_states(const gdr::SeqArgs &s, int64_t group, int D, const float *from, float *to,
+                                             int threads)
+{
+    const int64_t n = group * WAVE + threadIdx.x % WAVE;
+    const bool empty = n < s.n_seqs && gdr::seq_edge(s, (int)n + 1) <= gdr::seq_edge(s, (int)n);
+    for (uint64_t left = __ballot(empty); left; left &= left - 1) {
+        const int64_t row = (group * WAVE + __builtin_ctzll(left)) * D;
+        for (int c = threadIdx.x; c < D; c += threads) to[row + c] = from ? from[row + c] : 0.f;
+    }
+}
+
+// tokens that sequences have: [0, total)
+__device__ __forceinline__ int total_tokens(const gdr::SeqArgs &s)
+{
+    return s.cu_seqlens ? gdr::seq_edge(s, s.n_seqs) : s.n_tokens;
+}
+
+// workgroups that look for empty sequences
+inline int64_t empty_groups(const Args &a, bool wanted)
+{
+    return wanted && (a.cu_seqlens || !a.n_tokens) ? ((int64_t)a.n_seqs + WAVE - 1) / WAVE : 0;
+}
+
+// Pairs of channels at once where every row of every tensor starts on a pair
+// (D even, addresses to two elements); single channels else.
+inline bool pairs(const Args &a)
+{
+    const size_t es = a.bf16 ? 2 : 4;
+    uintptr_t in = 0, st = 0;
+    for (const void *p : {a.x, a.r, a.i, (const void *)a.h, a.dh, (const void *)a.dx, (const void *)a.dr, (const void *)a.di})
+        in |= reinterpret_cast<uintptr_t>(p);
+    for (const float *p : {a.g, a.rate, a.h0, (const float *)a.h_T, (const float *)a.kept, a.dh_T, (const float *)a.dg,
+                           (const float *)a.drate, (const float *)a.dh0})
+        st |= reinterpret_cast<uintptr_t>(p);
+    return a.D % 2 == 0 && in % (2 * es) == 0 && st % 8 == 0;
+}
+
+}  // namespace glr

@@ -41,7 +41,7 @@
  * the gradients that passes through sqrt(1 - a^2), whose slope is infinite
  * there, is taken as 0.
  *
- * Sizes: D >= 1; 0 <= n_seqs; 0 <= n_tokens <= 2^31 - 256; n_tokens, n_seqs
+ * Sizes: D >= 1; 0 <= n_seqs < 2^27; 0 <= n_tokens <= 2^31 - 256; n_tokens, n_seqs
  * and (decode) N times D below 2^40, and the number of (64 tokens, 64
  * channels) tiles below 2^22.  in_dtype KDA_BF16 or KDA_F32.
  *

@@ -55,7 +55,7 @@ def bwd(lib, gated, **kw):
 
 SIZES = [(dict(D=0), "D must"), (dict(n=-1), "n_seqs"), (dict(N=-1), "n_tokens"), (dict(N=(1 << 31) - 255), "2^31"),
          (dict(n=7), "multiple"), (dict(n=0), "n_seqs == 0"), (dict(dt=7), "in_dtype"),
-         (dict(N=1 << 30, D=1 << 10), "2^40"), (dict(n=1 << 30, D=1 << 10, N=0), "2^40"),
+         (dict(N=1 << 30, D=1 << 10), "2^40"), (dict(n=1 << 26, D=1 << 15, N=0), "2^40"), (dict(n=1 << 27, N=0), "2^27"),
          (dict(N=1 << 28, D=64), "2^22"), (dict(N=1 << 17, D=1 << 17), "2^22"),
          (dict(x=None), "x is NULL"), (dict(x=P + 1), "aligned"), (dict(h0=20 * P + 2), "aligned"),
          (dict(cu=20 * P + 2), "aligned"), (dict(kept=20 * P + 2), "aligned")]
