@@ -22,6 +22,7 @@ using api::set_error;
 kda_status check_sizes(int64_t n_tokens, int32_t D)
 {
     if (D < 1) return set_error(KDA_ERR_INVALID_ARG, "D must be >= 1 (got %d)", D);
+    if (D >= 1 << 24) return set_error(KDA_ERR_INVALID_ARG, "D must be below 2^24 (got %d)", D);
     if (n_tokens < 0) return set_error(KDA_ERR_INVALID_ARG, "n_tokens must be >= 0");
     if (n_tokens > ((int64_t)1 << 31) - 256)
         return set_error(KDA_ERR_INVALID_ARG, "n_tokens must be at most 2^31 - 256");

@@ -20,7 +20,7 @@ __global__ __launch_bounds__(NT) void glr_decode_kernel(DecodeArgs a)
             float *S = a.S + (int64_t)slot * D + c;
             const float xv = kda::Elem<T>::ld(static_cast<const T *>(a.x) + at);
             if (GATED) {
-                const Gates g = gates(kda::Elem<T>::ld(static_cast<const T *>(a.r) + at),
+                const Gates g = gates<false>(kda::Elem<T>::ld(static_cast<const T *>(a.r) + at),
                                       kda::Elem<T>::ld(static_cast<const T *>(a.i) + at), -a.rate[c]);
                 h = __builtin_fmaf(g.a, *S, g.b * xv);
             } else

@@ -14,22 +14,27 @@
 namespace glr {
 namespace {
 
-constexpr int NW = 8, K = 8, C = NW * K, NT = NW * WAVE;
-static_assert(C == kKept, "a tile starts from a kept state");
+constexpr int K = 8;
+// Eight waves a tile, but four where each lane forms the gates of two channels
+// and a workgroup of eight would leave room for no second one beside it.
+constexpr int waves(bool gated, int V) { return gated && V == 2 ? 4 : 8; }
+constexpr int tokens(bool gated, int V) { return waves(gated, V) * K; }
+static_assert(tokens(true, 2) % kKept == 0 && tokens(true, 1) % kKept == 0, "a tile starts from a kept state");
 
 template <typename T, bool GATED, int V>
-__global__ __launch_bounds__(NT) void glr_grad_kernel(Args a, Chain chain, float *part)
+__global__ __launch_bounds__(waves(GATED, V) * WAVE) void glr_grad_kernel(Args a, Chain chain, float *part)
 {
+    constexpr int NW = waves(GATED, V), C = tokens(GATED, V), NT = NW * WAVE;
     typedef Row<T, V> R;
     typedef Row<float, V> RF;
     __shared__ int s_idx, s_first[C], s_last[C];
-    __shared__ Map s_up[NW][WAVE * V], s_down[NW][WAVE * V];
-    __shared__ float s_in[WAVE * V];
+    __shared__ Map s_up[NW - 1][WAVE * V], s_down[NW][WAVE * V];
+    __shared__ float s_in[WAVE * V], s_late[GATED ? K : 1][2][V][NT];
     const int tid = threadIdx.x, lane = tid % WAVE, w = __builtin_amdgcn_readfirstlane(tid / WAVE), D = a.D;
     const gdr::SeqArgs sa = seq_args(a);
-    if (tid == 0) s_idx = chain.ticket ? (int)atomicAdd(chain.ticket, 1u) : (int)blockIdx.x;
-    if (tid < C) s_first[tid] = s_last[tid] = -1;
     const int total = total_tokens(sa);
+    if (tid == 0) s_idx = take(chain);
+    if (tid < C) s_first[tid] = s_last[tid] = -1;
     __syncthreads();
     const int idx = __builtin_amdgcn_readfirstlane(s_idx);
     if (idx >= chain.tiles * chain.blocks) {
@@ -44,26 +49,30 @@ __global__ __launch_bounds__(NT) void glr_grad_kernel(Args a, Chain chain, float
     const int cc = active ? c : 0;
     const int tw = t0 + w * K, mine = count - w * K < 0 ? 0 : count - w * K < K ? count - w * K : K;
 
+    const unsigned ct = active ? c * (unsigned)sizeof(T) : kNowhere, cf = active ? c * 4u : kNowhere;
+    const Rows<T, V> bx(a.x, tw, mine, D), br(a.r, tw, GATED ? mine : 0, D), bi(a.i, tw, GATED ? mine : 0, D),
+        bdh(a.dh, tw, mine, D);
+    const Rows<float, V> bg(a.g, tw, GATED ? 0 : mine, D);
+
     typename R::raw rx[K], rr[K], ri[K], rd[K];
     typename RF::raw rg[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int64_t row = (int64_t)(k < mine ? tw + k : t0) * D;
-        rx[k] = R::ld(static_cast<const T *>(a.x) + row + cc);
+        rx[k] = bx.ld(k, ct);
         if constexpr (GATED) {
-            rr[k] = R::ld(static_cast<const T *>(a.r) + row + cc);
-            ri[k] = R::ld(static_cast<const T *>(a.i) + row + cc);
+            rr[k] = br.ld(k, ct);
+            ri[k] = bi.ld(k, ct);
         } else
-            rg[k] = RF::ld(a.g + row + cc);
-        rd[k] = R::ld(static_cast<const T *>(a.dh) + row + cc);
+            rg[k] = bg.ld(k, cf);
+        rd[k] = bdh.ld(k, ct);
     }
     float nr[V], h[V];
     if constexpr (GATED) {
-        const typename RF::raw rate = RF::ld(a.rate + cc);
+        const typename RF::raw rate = ld<V>(a.rate + cc);
 #pragma unroll
         for (int j = 0; j < V; ++j) nr[j] = -RF::get(rate, j);
     }
-    const typename RF::raw left = RF::ld(a.kept + (int64_t)tile * D + cc);
+    const typename RF::raw left = ld<V>(a.kept + (int64_t)(t0 / kKept) * D + cc);
     if (w == 0) mark_borders(sa, t0, C, lane, s_first, s_last);
     __syncthreads();
     const uint64_t starts = __ballot(lane < K && s_first[w * K + lane % K] >= 0);
@@ -72,64 +81,80 @@ __global__ __launch_bounds__(NT) void glr_grad_kernel(Args a, Chain chain, float
 
     // u: the token's input; gated, of h's derivatives: b by x, e by i over L,
     // and with w = a h_{t-1}: (w - cx) q by r, (w - cx) s by -rate
-    float al[K][V], u[K][V], d[K][V], b[K][V], e[K][V], cx[K][V], q[K][V], s[K][V];
+    float al[K][V], u[K][V], b[K][V], cx[K][V], s[K][V];
+    const auto form = [&](auto near) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float x = R::get(rx[k], j);
-            d[k][j] = R::get(rd[k], j);
-            if constexpr (GATED) {
-                const GateGrads g = gate_grads(R::get(rr[k], j), R::get(ri[k], j), nr[j]);
-                al[k][j] = g.a;
-                b[k][j] = g.b;
-                u[k][j] = g.b * x;
-                e[k][j] = u[k][j] * g.rest_i;
-                cx[k][j] = g.c * x;
-                q[k][j] = g.q;
-                s[k][j] = g.s_r;
-            } else {
-                al[k][j] = decay(RF::get(rg[k], j));
-                u[k][j] = x;
+            for (int j = 0; j < V; ++j) {
+                const float x = R::get(rx[k], j);
+                if constexpr (GATED) {
+                    const GateGrads g = gate_grads<decltype(near)::value>(R::get(rr[k], j), R::get(ri[k], j), nr[j]);
+                    al[k][j] = g.a;
+                    b[k][j] = g.b;
+                    u[k][j] = g.b * x;
+                    s_late[k][0][j][tid] = u[k][j] * g.rest_i;
+                    cx[k][j] = g.c * x;
+                    s_late[k][1][j][tid] = g.q;
+                    s[k][j] = g.s_r;
+                } else {
+                    al[k][j] = decay(RF::get(rg[k], j));
+                    u[k][j] = x;
+                }
             }
-        }
+    };
+    if (GATED && all_near<V>(nr)) form(std::true_type{});
+    else form(std::false_type{});
     Map up[V], down[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) up[j] = down[j] = Map{1.f, 0.f};
-    // a start's input holds what comes of the state before the sequence, a
-    // last token's cotangent what comes of the state behind it
+    // what comes into a sequence's last token from behind is dh_T (0 without
+    // one), what leaves its first token goes to dh0 and no further
+    const auto behind = [&](int k, float *M) {
+        typename RF::raw t{};
+        if (a.dh_T) {
+            const int n = __builtin_amdgcn_readfirstlane(s_last[w * K + k]);
+            t = ld<V>(a.dh_T + (int64_t)n * D + cc);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) M[j] = RF::get(t, j);
+    };
+    const auto before = [&](int k, float *H) {
+        typename RF::raw t{};
+        if (a.h0) {
+            const int n = __builtin_amdgcn_readfirstlane(s_first[w * K + k]);
+            t = ld<V>(a.h0 + (int64_t)n * D + cc);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) H[j] = RF::get(t, j);
+    };
     if (!plain) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (k < mine) {
-                if (a.dh_T && (ends >> k & 1)) {
-                    const int n = __builtin_amdgcn_readfirstlane(s_last[w * K + k]);
-                    const typename RF::raw t = RF::ld(a.dh_T + (int64_t)n * D + cc);
+            if (k >= mine) continue;
+            if (starts >> k & 1) {
+                float H[V];
+                before(k, H);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) d[k][j] += RF::get(t, j);
-                }
-                const bool start = starts >> k & 1;
-                float h0[V] = {};
-                if (start && a.h0) {
-                    const int n = __builtin_amdgcn_readfirstlane(s_first[w * K + k]);
-                    const typename RF::raw t = RF::ld(a.h0 + (int64_t)n * D + cc);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) h0[j] = RF::get(t, j);
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    up[j] = start ? Map{kForget, __builtin_fmaf(al[k][j], h0[j], u[k][j])}
-                                  : Map{up[j].A * al[k][j], __builtin_fmaf(al[k][j], up[j].B, u[k][j])};
+                for (int j = 0; j < V; ++j) up[j] = Map{kForget, H[j]};
             }
+#pragma unroll
+            for (int j = 0; j < V; ++j) up[j] = Map{up[j].A * al[k][j], __builtin_fmaf(al[k][j], up[j].B, u[k][j])};
         }
 #pragma unroll
-        for (int k = K - 1; k >= 0; --k)
-            if (k < mine) {
+        for (int k = K - 1; k >= 0; --k) {
+            if (k >= mine) continue;
+            if (ends >> k & 1) {
+                float M[V];
+                behind(k, M);
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    down[j] = starts >> k & 1 ? Map{kForget, 0.f}
-                                              : Map{down[j].A * al[k][j], al[k][j] * (d[k][j] + down[j].B)};
+                for (int j = 0; j < V; ++j) down[j] = Map{kForget, M[j]};
             }
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                down[j] = starts >> k & 1 ? Map{kForget, 0.f}
+                                          : Map{down[j].A * al[k][j], al[k][j] * (R::get(rd[k], j) + down[j].B)};
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -138,130 +163,133 @@ __global__ __launch_bounds__(NT) void glr_grad_kernel(Args a, Chain chain, float
 #pragma unroll
         for (int k = K - 1; k >= 0; --k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) down[j].B = al[k][j] * (d[k][j] + down[j].B);
+            for (int j = 0; j < V; ++j) down[j].B = al[k][j] * (R::get(rd[k], j) + down[j].B);
 #pragma unroll
         for (int j = 0; j < V; ++j) down[j].A = up[j].A;
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        s_up[w][lane * V + j] = up[j];
+        if (w < NW - 1) s_up[w][lane * V + j] = up[j];
         s_down[w][lane * V + j] = down[j];
     }
     __syncthreads();
 
+    // the tile's map of the cotangent: wave 0 stores it for the tiles before
+    // this one as soon as it is there
+    const bool more = chain.ticket && tile > 0;
+    const bool alone = t0 + C >= total || s_last[C - 1] >= 0;
+    uint64_t *const p = chain.words + (int64_t)tile * D + cc;
+    Map t[V];
     if (w == 0) {
-        Map m[V];
-        float in[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) m[j] = s_down[NW - 1][lane * V + j];
+        for (int j = 0; j < V; ++j) t[j] = s_down[NW - 1][lane * V + j];
 #pragma unroll
         for (int i = NW - 2; i >= 0; --i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) m[j] = after(s_down[i][lane * V + j], m[j]);
-        const bool more = chain.ticket && tile > 0;
-        const bool alone = t0 + C >= total || s_last[C - 1] >= 0;
-        uint64_t *p = chain.words + (int64_t)tile * D + cc;
-        if (alone) {
+            for (int j = 0; j < V; ++j) t[j] = after(s_down[i][lane * V + j], t[j]);
+        if (more && active)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                in[j] = 0.f;
-                if (more && active) put(p + j, Map{kForget, m[j].B});
-            }
-        } else {
-            if (more && active)
-#pragma unroll
-                for (int j = 0; j < V; ++j) put(p + j, m[j]);
-            look_back<V>(p + D, D, (total - 1) / C - tile, active, in);
-            if (more && active)
-#pragma unroll
-                for (int j = 0; j < V; ++j) put(p + j, Map{kForget, m[j](in[j])});
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) s_in[lane * V + j] = in[j];
+            for (int j = 0; j < V; ++j) put(p + j, alone ? Map{kForget, t[j].B} : t[j]);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         h[j] = RF::get(left, j);
         for (int i = 0; i < w; ++i) h[j] = s_up[i][lane * V + j](h[j]);
     }
-    // cx becomes w - cx (plain: w)
+    // cx becomes w - cx (plain: w).  (Here and below the waves without a border
+    // have code of their own: a load in a branch would make every token wait
+    // for the stores before it.)
+    const auto ascend = [&](auto borders) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        if (starts >> k & 1) {
-            typename RF::raw t{};
-            if (a.h0) {
-                const int n = __builtin_amdgcn_readfirstlane(s_first[w * K + k]);
-                t = RF::ld(a.h0 + (int64_t)n * D + cc);
+        for (int k = 0; k < K; ++k) {
+            if (decltype(borders)::value && (starts >> k & 1)) before(k, h);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float ah = al[k][j] * h[j];
+                h[j] = ah + u[k][j];
+                cx[k][j] = GATED ? ah - cx[k][j] : ah;
             }
+        }
+    };
+    if (plain) ascend(std::false_type{});
+    else ascend(std::true_type{});
+    if (w == 0) {
+        float in[V] = {};
+        if (!alone) {
+            look_back<8 / V, V>(p + D, D, (total - 1) / C - tile, active, in);
+            if (more && active)
 #pragma unroll
-            for (int j = 0; j < V; ++j) h[j] = RF::get(t, j);
+                for (int j = 0; j < V; ++j) put(p + j, Map{kForget, t[j](in[j])});
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float ah = al[k][j] * h[j];
-            h[j] = ah + u[k][j];
-            cx[k][j] = GATED ? ah - cx[k][j] : ah;
-        }
+        for (int j = 0; j < V; ++j) s_in[lane * V + j] = in[j];
     }
     __syncthreads();
 
+    const Rows<T, V> bdx(a.dx, tw, mine, D), bdr(a.dr, tw, GATED ? mine : 0, D), bdi(a.di, tw, GATED ? mine : 0, D);
+    const Rows<float, V> bdg(a.dg, tw, GATED ? 0 : mine, D);
     float M[V], rate[V] = {};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         M[j] = s_in[lane * V + j];
         for (int i = NW - 1; i > w; --i) M[j] = s_down[i][lane * V + j](M[j]);
     }
+    const auto descend = [&](auto borders) {
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-        if (k >= mine) continue;
-        const int64_t at = (int64_t)(tw + k) * D + c;
-        float L[V], dr[V], di[V];
+        for (int k = K - 1; k >= 0; --k) {
+            if (decltype(borders)::value && k >= mine) continue;
+            if (decltype(borders)::value && (ends >> k & 1)) behind(k, M);
+            float L[V], dr[V], di[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            L[j] = d[k][j] + M[j];
-            M[j] = al[k][j] * L[j];
-            if constexpr (GATED) {
-                const float dg = L[j] * cx[k][j];
-                dr[j] = dg * q[k][j];
-                rate[j] = __builtin_fmaf(-dg, s[k][j], rate[j]);
-                di[j] = L[j] * e[k][j];
-                L[j] *= b[k][j];
-            } else
-                dr[j] = L[j] * cx[k][j];
-        }
-        if (active) {
-            R::st(static_cast<T *>(a.dx) + at, L);
-            if constexpr (GATED) {
-                R::st(static_cast<T *>(a.dr) + at, dr);
-                R::st(static_cast<T *>(a.di) + at, di);
-            } else
-                RF::st(a.dg + at, dr);
-        }
-        if (starts >> k & 1) {
-            if (a.dh0 && active) {
-                const int n = __builtin_amdgcn_readfirstlane(s_first[w * K + k]);
-                RF::st(a.dh0 + (int64_t)n * D + c, M);
+            for (int j = 0; j < V; ++j) {
+                L[j] = R::get(rd[k], j) + M[j];
+                M[j] = al[k][j] * L[j];
+                if constexpr (GATED) {
+                    const float dg = L[j] * cx[k][j];
+                    dr[j] = dg * s_late[k][1][j][tid];
+                    rate[j] = __builtin_fmaf(-dg, s[k][j], rate[j]);
+                    di[j] = L[j] * s_late[k][0][j][tid];
+                    L[j] *= b[k][j];
+                } else
+                    dr[j] = L[j] * cx[k][j];
             }
+            bdx.st(k, ct, L);
+            if constexpr (GATED) {
+                bdr.st(k, ct, dr);
+                bdi.st(k, ct, di);
+            } else
+                bdg.st(k, cf, dr);
+            if (decltype(borders)::value && (starts >> k & 1)) {
+                if (a.dh0 && active) {
+                    const int n = __builtin_amdgcn_readfirstlane(s_first[w * K + k]);
+                    st<V>(a.dh0 + (int64_t)n * D + c, M);
+                }
 #pragma unroll
-            for (int j = 0; j < V; ++j) M[j] = 0.f;
+                for (int j = 0; j < V; ++j) M[j] = 0.f;
+            }
         }
-    }
+    };
+    if (plain) descend(std::false_type{});
+    else descend(std::true_type{});
     if constexpr (GATED) {
+        // a wave is done with what it laid aside, and all are with the maps of the state
+        float (*s_rate)[WAVE * V] = reinterpret_cast<float (*)[WAVE * V]>(&s_up[0][0]);
+        static_assert(sizeof(s_up) >= NW * WAVE * V * sizeof(float), "room for the rates");
 #pragma unroll
-        for (int j = 0; j < V; ++j) s_up[w][lane * V + j].B = rate[j];
+        for (int j = 0; j < V; ++j) s_rate[w][lane * V + j] = rate[j];
         __syncthreads();
         if (w == 0 && active) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                for (int i = 1; i < NW; ++i) rate[j] += s_up[i][lane * V + j].B;
-            RF::st(part + (int64_t)tile * D + c, rate);
+                for (int i = 1; i < NW; ++i) rate[j] += s_rate[i][lane * V + j];
+            st<V>(part + (int64_t)tile * D + c, rate);
         }
     }
 }
 
 // drate: the tiles' rows, each wave every 16th of them, in 64 bits
 constexpr int RW = 16;
-__global__ __launch_bounds__(RW * WAVE) void glr_rate_kernel(Args a, const float *part)
+__global__ __launch_bounds__(RW * WAVE) void glr_rate_kernel(Args a, const float *part, int C)
 {
     __shared__ double s_sum[RW][WAVE];
     const int lane = threadIdx.x % WAVE, w = threadIdx.x / WAVE, c = blockIdx.x * WAVE + lane;
@@ -277,18 +305,26 @@ __global__ __launch_bounds__(RW * WAVE) void glr_rate_kernel(Args a, const float
     }
 }
 
-int64_t tiles_of(int64_t n_tokens) { return (n_tokens + C - 1) / C; }
-size_t rows_bytes(int64_t n_tokens, int32_t D)          // one fp32 row a tile
+int64_t tiles_of(int64_t n_tokens, bool gated, int V)
 {
-    return ((size_t)tiles_of(n_tokens) * D * 4 + 255) & ~(size_t)255;
+    return (n_tokens + tokens(gated, V) - 1) / tokens(gated, V);
+}
+// one fp32 row for each kept state, and no fewer than tiles
+size_t rows_bytes(int64_t n_tokens, int32_t D)
+{
+    return ((size_t)((n_tokens + kKept - 1) / kKept) * D * 4 + 255) & ~(size_t)255;
 }
 
 template <typename T, bool GATED>
-void launch_v(const Args &a, const Chain &ch, float *part, int64_t groups, int V, hipStream_t s)
+void launch_v(const Args &a, const Chain &ch, float *part, int V, hipStream_t s)
 {
-    const dim3 grid((unsigned)((int64_t)ch.tiles * ch.blocks + groups));
-    if (V == 2) hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 2>), grid, dim3(NT), 0, s, a, ch, part);
-    else hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 1>), grid, dim3(NT), 0, s, a, ch, part);
+    const dim3 grid((unsigned)ch.items);
+    if constexpr (kPairs<T, GATED>)
+        if (V == 2) {
+            hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 2>), grid, dim3(waves(GATED, 2) * WAVE), 0, s, a, ch, part);
+            return;
+        }
+    hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 1>), grid, dim3(waves(GATED, 1) * WAVE), 0, s, a, ch, part);
 }
 
 }  // namespace
@@ -297,7 +333,7 @@ void launch_v(const Args &a, const Chain &ch, float *part, int64_t groups, int V
 // chain (the forward's first, which is never longer)
 size_t bwd_workspace(int64_t n_tokens, int32_t D)
 {
-    return 2 * rows_bytes(n_tokens, D) + chain_bytes(tiles_of(n_tokens), D);
+    return 2 * rows_bytes(n_tokens, D) + chain_bytes(tiles_of(n_tokens, true, 2), D);
 }
 
 hipError_t launch_bwd(const Args &arg)
@@ -315,17 +351,18 @@ hipError_t launch_bwd(const Args &arg)
         f.ws = chain;
         if ((e = launch_fwd(f)) != hipSuccess) return e;
     }
-    const int V = pairs(a) ? 2 : 1;
-    const Chain ch = make_chain(chain, (int)tiles_of(a.n_tokens), (a.D + WAVE * V - 1) / (WAVE * V));
-    const int64_t groups = empty_groups(a, a.dh0);
-    if ((int64_t)ch.tiles * ch.blocks + groups) {
+    const int V = channels(a);
+    const Chain ch = make_chain(chain, (int)tiles_of(a.n_tokens, a.gated, V), (a.D + WAVE * V - 1) / (WAVE * V),
+                                empty_groups(a, a.dh0));
+    if (ch.items) {
         if ((e = clear_chain(ch, a.D, a.stream)) != hipSuccess) return e;
-        if (a.bf16) a.gated ? launch_v<bf16, true>(a, ch, part, groups, V, a.stream) : launch_v<bf16, false>(a, ch, part, groups, V, a.stream);
-        else a.gated ? launch_v<float, true>(a, ch, part, groups, V, a.stream) : launch_v<float, false>(a, ch, part, groups, V, a.stream);
+        if (a.bf16) a.gated ? launch_v<bf16, true>(a, ch, part, V, a.stream) : launch_v<bf16, false>(a, ch, part, V, a.stream);
+        else a.gated ? launch_v<float, true>(a, ch, part, V, a.stream) : launch_v<float, false>(a, ch, part, V, a.stream);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.gated) {
-        hipLaunchKernelGGL(glr_rate_kernel, dim3((unsigned)((a.D + WAVE - 1) / WAVE)), dim3(RW * WAVE), 0, a.stream, a, part);
+        hipLaunchKernelGGL(glr_rate_kernel, dim3((unsigned)((a.D + WAVE - 1) / WAVE)), dim3(RW * WAVE), 0, a.stream, a, part,
+                           tokens(true, V));
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -11,7 +11,7 @@
 namespace glr {
 
 // tokens between two kept states
-constexpr int kKept = 64;
+constexpr int kKept = 32;
 
 struct Args {
     const void *x, *r, *i;               // r, i: gated

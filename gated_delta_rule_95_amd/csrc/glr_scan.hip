@@ -17,7 +17,7 @@ namespace {
 constexpr int NW = 8, K = 16, C = NW * K, NT = NW * WAVE;
 
 template <typename T, bool GATED, int V>
-__global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
+__global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
 {
     typedef Row<T, V> R;
     typedef Row<float, V> RF;
@@ -26,9 +26,9 @@ __global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
     __shared__ float s_in[WAVE * V];
     const int tid = threadIdx.x, lane = tid % WAVE, w = __builtin_amdgcn_readfirstlane(tid / WAVE), D = a.D;
     const gdr::SeqArgs sa = seq_args(a);
-    if (tid == 0) s_idx = chain.ticket ? (int)atomicAdd(chain.ticket, 1u) : (int)blockIdx.x;
-    if (tid < C) s_first[tid] = s_last[tid] = -1;
     const int total = total_tokens(sa);
+    if (tid == 0) s_idx = take(chain);
+    if (tid < C) s_first[tid] = s_last[tid] = -1;
     __syncthreads();
     const int idx = __builtin_amdgcn_readfirstlane(s_idx);
     if (idx >= chain.tiles * chain.blocks) {
@@ -43,21 +43,24 @@ __global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
     const int cc = active ? c : 0;
     const int tw = t0 + w * K, mine = count - w * K < 0 ? 0 : count - w * K < K ? count - w * K : K;
 
+    const unsigned ct = active ? c * (unsigned)sizeof(T) : kNowhere, cf = active ? c * 4u : kNowhere;
+    const Rows<T, V> bx(a.x, tw, mine, D), br(a.r, tw, GATED ? mine : 0, D), bi(a.i, tw, GATED ? mine : 0, D);
+    const Rows<float, V> bg(a.g, tw, GATED ? 0 : mine, D);
+
     typename R::raw rx[K], rr[K], ri[K];
     typename RF::raw rg[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int64_t row = (int64_t)(k < mine ? tw + k : t0) * D;
-        rx[k] = R::ld(static_cast<const T *>(a.x) + row + cc);
+        rx[k] = bx.ld(k, ct);
         if constexpr (GATED) {
-            rr[k] = R::ld(static_cast<const T *>(a.r) + row + cc);
-            ri[k] = R::ld(static_cast<const T *>(a.i) + row + cc);
+            rr[k] = br.ld(k, ct);
+            ri[k] = bi.ld(k, ct);
         } else
-            rg[k] = RF::ld(a.g + row + cc);
+            rg[k] = bg.ld(k, cf);
     }
     float nr[V];
     if constexpr (GATED) {
-        const typename RF::raw rate = RF::ld(a.rate + cc);
+        const typename RF::raw rate = ld<V>(a.rate + cc);
 #pragma unroll
         for (int j = 0; j < V; ++j) nr[j] = -RF::get(rate, j);
     }
@@ -67,19 +70,23 @@ __global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
     const uint64_t ends = __ballot(lane < K && s_last[w * K + lane % K] >= 0);
 
     float al[K][V], u[K][V];
+    const auto form = [&](auto near) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            if constexpr (GATED) {
-                const Gates g = gates(R::get(rr[k], j), R::get(ri[k], j), nr[j]);
-                al[k][j] = g.a;
-                u[k][j] = g.b * R::get(rx[k], j);
-            } else {
-                al[k][j] = decay(RF::get(rg[k], j));
-                u[k][j] = R::get(rx[k], j);
+            for (int j = 0; j < V; ++j) {
+                if constexpr (GATED) {
+                    const Gates g = gates<decltype(near)::value>(R::get(rr[k], j), R::get(ri[k], j), nr[j]);
+                    al[k][j] = g.a;
+                    u[k][j] = g.b * R::get(rx[k], j);
+                } else {
+                    al[k][j] = decay(RF::get(rg[k], j));
+                    u[k][j] = R::get(rx[k], j);
+                }
             }
-        }
+    };
+    if (GATED && all_near<V>(nr)) form(std::true_type{});
+    else form(std::false_type{});
     Map m[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) m[j] = Map{1.f, 0.f};
@@ -95,7 +102,7 @@ __global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
             const bool start = starts >> k & 1;
             if (start && a.h0) {
                 const int n = __builtin_amdgcn_readfirstlane(s_first[w * K + k]);
-                const typename RF::raw h0 = RF::ld(a.h0 + (int64_t)n * D + cc);
+                const typename RF::raw h0 = ld<V>(a.h0 + (int64_t)n * D + cc);
 #pragma unroll
                 for (int j = 0; j < V; ++j) u[k][j] = __builtin_fmaf(al[k][j], RF::get(h0, j), u[k][j]);
             }
@@ -132,7 +139,7 @@ __global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
             if (more && active)
 #pragma unroll
                 for (int j = 0; j < V; ++j) put(p + j, m[j]);
-            look_back<V>(p - D, -(int64_t)D, tile, active, in);
+            look_back<8, V>(p - D, -(int64_t)D, tile, active, in);
             if (more && active)
 #pragma unroll
                 for (int j = 0; j < V; ++j) put(p + j, Map{kForget, m[j](in[j])});
@@ -149,14 +156,14 @@ __global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
         for (int i = 0; i < w; ++i) h[j] = s_map[i][lane * V + j](h[j]);
     }
     if (!active || mine == 0) return;
-    if (a.kept && w * K % kKept == 0) RF::st(a.kept + (int64_t)(tw / kKept) * D + c, h);
-    T *out = static_cast<T *>(a.h);
+    if (a.kept && w * K % kKept == 0) st<V>(a.kept + (int64_t)(tw / kKept) * D + c, h);
+    const Rows<T, V> bh(a.h, tw, a.h ? mine : 0, D);
     if (plain && !ends) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
             for (int j = 0; j < V; ++j) h[j] = __builtin_fmaf(al[k][j], h[j], u[k][j]);
-            if (out) R::st(out + (int64_t)(tw + k) * D + c, h);
+            bh.st(k, ct, h);
         }
     } else {
 #pragma unroll
@@ -164,10 +171,10 @@ __global__ __launch_bounds__(NT) void glr_scan_kernel(Args a, Chain chain)
             if (k >= mine) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) h[j] = starts >> k & 1 ? u[k][j] : __builtin_fmaf(al[k][j], h[j], u[k][j]);
-            if (out) R::st(out + (int64_t)(tw + k) * D + c, h);
+            bh.st(k, ct, h);
             if (a.h_T && (ends >> k & 1)) {
                 const int n = __builtin_amdgcn_readfirstlane(s_last[w * K + k]);
-                RF::st(a.h_T + (int64_t)n * D + c, h);
+                st<V>(a.h_T + (int64_t)n * D + c, h);
             }
         }
     }
@@ -183,11 +190,15 @@ __global__ __launch_bounds__(256) void glr_clear_kernel(Chain c, int64_t words)
 int64_t tiles_of(int64_t n_tokens) { return (n_tokens + C - 1) / C; }
 
 template <typename T, bool GATED>
-void launch_v(const Args &a, const Chain &ch, int64_t groups, int V, hipStream_t s)
+void launch_v(const Args &a, const Chain &ch, int V, hipStream_t s)
 {
-    const dim3 grid((unsigned)((int64_t)ch.tiles * ch.blocks + groups));
-    if (V == 2) hipLaunchKernelGGL((glr_scan_kernel<T, GATED, 2>), grid, dim3(NT), 0, s, a, ch);
-    else hipLaunchKernelGGL((glr_scan_kernel<T, GATED, 1>), grid, dim3(NT), 0, s, a, ch);
+    const dim3 grid((unsigned)ch.items);
+    if constexpr (kPairs<T, GATED>)
+        if (V == 2) {
+            hipLaunchKernelGGL((glr_scan_kernel<T, GATED, 2>), grid, dim3(NT), 0, s, a, ch);
+            return;
+        }
+    hipLaunchKernelGGL((glr_scan_kernel<T, GATED, 1>), grid, dim3(NT), 0, s, a, ch);
 }
 
 }  // namespace
@@ -204,14 +215,14 @@ size_t fwd_workspace(int64_t n_tokens, int32_t D) { return chain_bytes(tiles_of(
 
 hipError_t launch_fwd(const Args &a)
 {
-    const int V = pairs(a) ? 2 : 1;
-    const Chain ch = make_chain(a.ws, (int)tiles_of(a.n_tokens), (a.D + WAVE * V - 1) / (WAVE * V));
-    const int64_t groups = empty_groups(a, a.h_T);
-    if ((int64_t)ch.tiles * ch.blocks + groups == 0) return hipSuccess;
+    const int V = channels(a);
+    const Chain ch = make_chain(a.ws, (int)tiles_of(a.n_tokens), (a.D + WAVE * V - 1) / (WAVE * V),
+                                empty_groups(a, a.h_T));
+    if (ch.items == 0) return hipSuccess;
     const hipError_t e = clear_chain(ch, a.D, a.stream);
     if (e != hipSuccess) return e;
-    if (a.bf16) a.gated ? launch_v<bf16, true>(a, ch, groups, V, a.stream) : launch_v<bf16, false>(a, ch, groups, V, a.stream);
-    else a.gated ? launch_v<float, true>(a, ch, groups, V, a.stream) : launch_v<float, false>(a, ch, groups, V, a.stream);
+    if (a.bf16) a.gated ? launch_v<bf16, true>(a, ch, V, a.stream) : launch_v<bf16, false>(a, ch, V, a.stream);
+    else a.gated ? launch_v<float, true>(a, ch, V, a.stream) : launch_v<float, false>(a, ch, V, a.stream);
     return hipGetLastError();
 }
 

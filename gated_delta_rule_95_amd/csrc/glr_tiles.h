@@ -3,6 +3,8 @@
 // tile to tile (gfx950 only).
 #pragma once
 
+#include <type_traits>
+
 #include "glr_device.h"
 
 namespace glr {
@@ -10,21 +12,67 @@ namespace glr {
 // V neighbouring channels of a row, as stored and in fp32
 template <typename T, int V> struct Row {
     typedef T raw __attribute__((ext_vector_type(V)));
-    static __device__ __forceinline__ raw ld(const T *p) { return *reinterpret_cast<const raw *>(p); }
     static __device__ __forceinline__ float get(raw x, int j) { return (float)x[j]; }
-    static __device__ __forceinline__ void st(T *p, const float *x)
+    static __device__ __forceinline__ raw pack(const float *x)
     {
         raw v;
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = (T)x[j];
-        *reinterpret_cast<raw *>(p) = v;
+        return v;
     }
 };
 template <typename T> struct Row<T, 1> {
     typedef T raw;
-    static __device__ __forceinline__ raw ld(const T *p) { return *p; }
     static __device__ __forceinline__ float get(raw x, int) { return (float)x; }
-    static __device__ __forceinline__ void st(T *p, const float *x) { *p = (T)x[0]; }
+    static __device__ __forceinline__ raw pack(const float *x) { return (T)x[0]; }
+};
+template <int V, typename T>
+__device__ __forceinline__ typename Row<T, V>::raw ld(const T *p)
+{
+    return *reinterpret_cast<const typename Row<T, V>::raw *>(p);
+}
+template <int V, typename T>
+__device__ __forceinline__ void st(T *p, const float *x)
+{
+    *reinterpret_cast<typename Row<T, V>::raw *>(p) = Row<T, V>::pack(x);
+}
+
+// A wave's rows of a tensor [.., D] as a buffer resource: `rows` of them from
+// `first` on (D < 2^24 keeps their bytes below 2^31).  A row is a scalar
+// offset and a lane's channel a vector one, so addresses cost no vector
+// arithmetic; rows past the last read zeros and are not written, and so are
+// channels at kNowhere.
+constexpr unsigned kNowhere = 0x80000000u;
+template <typename T, int V> struct Rows {
+    typedef typename Row<T, V>::raw raw;
+    gdr::rsrc_t r;
+    unsigned row;
+    __device__ __forceinline__ Rows(const void *p, int64_t first, int rows, int D)
+        : r(gdr::make_rsrc(static_cast<const T *>(p) + first * D, rows * D * (int)sizeof(T))),
+          row((unsigned)D * (unsigned)sizeof(T))
+    {
+    }
+    // c: the lane's channel times the size of an element, or kNowhere
+    __device__ __forceinline__ raw ld(int k, unsigned c) const
+    {
+        if constexpr (sizeof(raw) == 2)
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, c, k * row, 0));
+        else if constexpr (sizeof(raw) == 4)
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, c, k * row, 0));
+        else
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, c, k * row, 0));
+    }
+    __device__ __forceinline__ void st(int k, unsigned c, const float *x) const
+    {
+        const raw v = Row<T, V>::pack(x);
+        typedef unsigned u2 __attribute__((ext_vector_type(2)));
+        if constexpr (sizeof(raw) == 2)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, c, k * row, 0);
+        else if constexpr (sizeof(raw) == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, c, k * row, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), r, c, k * row, 0);
+    }
 };
 
 // An affine map h -> A h + B of a channel's state.  A = -0 forgets: whatever
@@ -64,64 +112,75 @@ __device__ __forceinline__ Map map_of(uint64_t w)
 }
 
 // Workspace of a chain: a ticket, then one word for each tile and channel.
+// Workgroups take tiles in order, by the ticket, and store a map before they
+// wait, so a tile waits only for tiles that workgroups which run already have
+// taken, and the lowest of those waits for nothing: every wait ends.  (Workgroups that stay, 512 of them, and ask
+// for their next tile ahead were slower: scan of 20011 tokens 155 -> 230 us,
+// gradients 352 -> 535.)
 struct Chain {
     uint32_t *ticket;                    // nullptr: one tile, which needs no chain
     uint64_t *words;
     int tiles, blocks;                   // of tokens, of channels
+    int items;                           // what is handed out: tiles, then groups of sequences
 };
 constexpr size_t kChainHead = 256;
 inline size_t chain_bytes(int64_t tiles, int32_t D)
 {
     return tiles > 1 ? kChainHead + (((size_t)tiles * D * 8 + 255) & ~(size_t)255) : 0;
 }
-inline Chain make_chain(void *ws, int tiles, int blocks)
+inline Chain make_chain(void *ws, int tiles, int blocks, int64_t groups)
 {
-    if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks};
+    const int items = (int)((int64_t)tiles * blocks + groups);
+    if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks, items};
     return Chain{static_cast<uint32_t *>(ws),
-                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + kChainHead), tiles, blocks};
+                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + kChainHead), tiles, blocks, items};
+}
+__device__ __forceinline__ int take(const Chain &c)
+{
+    return c.ticket ? (int)atomicAdd(c.ticket, 1u) : (int)blockIdx.x;
 }
 hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s);
 
-// The state (or cotangent) that comes into a tile: the maps of the tiles
-// before it, nearest first, until one forgets or there is none left.  Words
-// of `n` tiles lie `step` apart, from `p` on.  Waits for words that are
-// empty: every tile before this one was handed out earlier, to a workgroup
-// that runs and stores its map before it waits itself, so each wait ends.
-template <int V>
+// The state (or cotangent) that comes into a tile.  Words of the `n` tiles
+// before it (the first of which forgets) lie `step` apart, from `p` on, the
+// nearest first.  Of the nearest W, those from the first one on that forgets
+// are not wanted; the others' maps are applied to its B, the farthest first.
+// That is what each of these tiles does, or did, to get at the map that
+// forgets which it stores in the end, so the result does not depend on how far
+// they have come, to the last bit.
+template <int W, int V>
 __device__ __forceinline__ void look_back(const uint64_t *p, int64_t step, int n, bool active, float *in)
 {
-    constexpr int W = 8;
-    Map m[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) m[j] = Map{active ? 1.f : kForget, 0.f};
-    int at = 0;
-    while (at < n) {
-        uint64_t w[W][V];
+    uint64_t w[W][V];
+    int from;
+    for (;;) {
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) w[i][j] = peek(p + step * (at + i < n ? at + i : n - 1) + j);
-        bool go = true, forgets = true;
-        int seen = 0;
+            for (int j = 0; j < V; ++j) w[i][j] = peek(p + step * (i < n ? i : n - 1) + j);
+        from = W;
+        bool there = true;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            bool there = true;
+            bool full = true, forgets = true;
 #pragma unroll
-            for (int j = 0; j < V; ++j) there = there && w[i][j] != kEmpty;
-            go = go && at + i < n && __all(there || !active);
-            if (!go) continue;
-            ++seen;
-#pragma unroll
-            for (int j = 0; j < V; ++j) m[j] = after(m[j], map_of(w[i][j]));
+            for (int j = 0; j < V; ++j) {
+                full = full && w[i][j] != kEmpty;
+                forgets = forgets && map_of(w[i][j]).forgets();
+            }
+            there = there && __all(full || !active);
+            if (there && from == W && __all(forgets || !active)) from = i;
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) forgets = forgets && m[j].forgets();
-        if (__all(forgets)) break;
-        at += seen;
-        if (!seen) __builtin_amdgcn_s_sleep(1);
+        if (from < W) break;
+        __builtin_amdgcn_s_sleep(1);
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) in[j] = m[j].B;
+    for (int i = W - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const Map m = map_of(w[i][j]);
+            in[j] = i > from ? 0.f : i == from ? m.B : m(in[j]);
+        }
 }
 
 // Borders of sequences inside tokens [t0, t0 + C): first[k] = the sequence
@@ -177,6 +236,15 @@ __device__ __forceinline__ void empty_states(const gdr::SeqArgs &s, int64_t grou
     }
 }
 
+// the near polynomial does for every channel of the wave
+template <int V> __device__ __forceinline__ bool all_near(const float *neg_rate)
+{
+    bool near = true;
+#pragma unroll
+    for (int j = 0; j < V; ++j) near = near && neg_rate[j] >= -kNear;
+    return __all(near);
+}
+
 // tokens that sequences have: [0, total)
 __device__ __forceinline__ int total_tokens(const gdr::SeqArgs &s)
 {
@@ -189,9 +257,12 @@ inline int64_t empty_groups(const Args &a, bool wanted)
     return wanted && (a.cu_seqlens || !a.n_tokens) ? ((int64_t)a.n_seqs + WAVE - 1) / WAVE : 0;
 }
 
-// Pairs of channels at once where every row of every tensor starts on a pair
-// (D even, addresses to two elements); single channels else.
-inline bool pairs(const Args &a)
+// Pairs of channels a lane where every row of every tensor starts on a pair (D
+// even, addresses to two elements), single channels else; and single ones for
+// the gates of fp32 inputs, whose pairs would not fit the registers beside a
+// second workgroup (and fill whole lines of memory without them).
+template <typename T, bool GATED> constexpr bool kPairs = sizeof(T) == 2 || !GATED;
+inline int channels(const Args &a)
 {
     const size_t es = a.bf16 ? 2 : 4;
     uintptr_t in = 0, st = 0;
@@ -200,7 +271,7 @@ inline bool pairs(const Args &a)
     for (const float *p : {a.g, a.rate, a.h0, (const float *)a.h_T, (const float *)a.kept, a.dh_T, (const float *)a.dg,
                            (const float *)a.drate, (const float *)a.dh0})
         st |= reinterpret_cast<uintptr_t>(p);
-    return a.D % 2 == 0 && in % (2 * es) == 0 && st % 8 == 0;
+    return (a.bf16 || !a.gated) && a.D % 2 == 0 && in % (2 * es) == 0 && st % 8 == 0 ? 2 : 1;
 }
 
 }  // namespace glr

@@ -24,8 +24,6 @@ __all__ = ["glr_fwd_scan", "glr_fwd_scan_gated", "glr_bwd_scan", "glr_bwd_scan_g
            "glr_decode_step", "glr_decode_step_gated", "glr_fwd_workspace_bytes",
            "glr_bwd_workspace_bytes"]
 
-KEPT = 64          # tokens between two kept states
-
 _DT = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
 
 
@@ -76,7 +74,10 @@ class _Batch:
             _need(gates[1], "i", x.dtype, x.shape, dev)
             _need(gates[2], "rate", torch.float32, (self.D,), dev)
         self.state = torch.Size((self.n_seqs, self.D))
-        self.kept = torch.Size((-(-self.N // KEPT), self.D))
+
+    def kept(self):
+        """The shape of the kept states, from the bytes the library asks for."""
+        return torch.Size((_lib.load().glr_kept_bytes(self.N, self.D) // (4 * self.D), self.D))
 
     def workspace(self, need, given):
         if given is not None:
@@ -107,7 +108,7 @@ def _fwd(fn, x, gates, h0, cu_seqlens, output_final_state, keep, h, h_T, workspa
         _need(h_T, "h_T", torch.float32, b.state, b.dev)
     elif output_final_state:
         h_T = torch.empty(b.state, dtype=torch.float32, device=b.dev)
-    kept = torch.empty(b.kept, dtype=torch.float32, device=b.dev) if keep else None
+    kept = torch.empty(b.kept(), dtype=torch.float32, device=b.dev) if keep else None
     ws = b.workspace(_lib.load().glr_fwd_workspace_bytes(b.N, b.D), workspace)
     _run(b.dev, fn, _ptr(x), *(_ptr(t) for t in gates), _ptr(h0), _ptr(cu_seqlens), b.n_seqs, b.N, b.D, b.dt,
          _ptr(h), _ptr(h_T), _ptr(kept), _ptr(ws), 0 if ws is None else ws.numel())
@@ -126,7 +127,7 @@ def glr_fwd_scan(x: torch.Tensor, g: torch.Tensor, h0: Optional[torch.Tensor] = 
     h0 : [n_seqs, D] fp32 or None
     cu_seqlens : int32 [n_seqs + 1] on the device (packed input only); rows of tokens behind
         its last entry are left as they are in a given h, unset in one allocated here
-    keep : also return what the backward wants, the state before every 64th token of the batch
+    keep : also return what the backward wants, the state before every 32nd token of the batch
     Returns (h in x's dtype, h_T fp32 or None), with keep (h, h_T, kept).
     """
     return _fwd(_lib.load().glr_fwd_scan, x, (g,), h0, cu_seqlens, output_final_state, keep, h, h_T, workspace)
@@ -154,7 +155,7 @@ def _bwd(fn, x, gates, dh, h0, dh_T, cu_seqlens, kept, workspace):
     if dh_T is not None:
         _need(dh_T, "dh_T", torch.float32, b.state, b.dev)
     if kept is not None:
-        _need(kept, "kept", torch.float32, b.kept, b.dev)
+        _need(kept, "kept", torch.float32, b.kept(), b.dev)
     ws = b.workspace(_lib.load().glr_bwd_workspace_bytes(b.N, b.D), workspace)
     # the gradients of x and of the gates are shaped like them
     out = [torch.empty_like(x)] + [torch.empty_like(t) for t in gates]

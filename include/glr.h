@@ -25,7 +25,7 @@
  *     g              [n_tokens, D]   float32, natural-log decay, g <= 0
  *     rate           [D]             float32, >= 0
  *     h0, h_T        [n_seqs, D]     float32
- *     kept           [ceil(n_tokens / 64), D] float32
+ *     kept           [ceil(n_tokens / 32), D] float32
  *     cu_seqlens     int32 [n_seqs + 1] in device memory, cu_seqlens[0] = 0,
  *                    non-decreasing, cu_seqlens[n_seqs] <= n_tokens; NULL:
  *                    n_seqs sequences of n_tokens / n_seqs tokens each
@@ -41,7 +41,7 @@
  * the gradients that passes through sqrt(1 - a^2), whose slope is infinite
  * there, is taken as 0.
  *
- * Sizes: D >= 1; 0 <= n_seqs < 2^27; 0 <= n_tokens <= 2^31 - 256; n_tokens, n_seqs
+ * Sizes: 1 <= D < 2^24; 0 <= n_seqs < 2^27; 0 <= n_tokens <= 2^31 - 256; n_tokens, n_seqs
  * and (decode) N times D below 2^40, and the number of (64 tokens, 64
  * channels) tiles below 2^22.  in_dtype KDA_BF16 or KDA_F32.
  *
@@ -53,8 +53,7 @@
  * reported as a kda_status (kda_last_error has the message) before anything
  * is launched, and cu_seqlens and slots that break their contract change
  * results, never the addresses touched.  Two calls in flight need separate
- * workspaces.  Results do not depend on the order in which workgroups run
- * but for the rounding of states that cross tile borders (a few 2^-24).
+ * workspaces.  Results do not depend on the order in which workgroups run.
  */
 #ifndef GLR_H
 #define GLR_H
@@ -71,7 +70,7 @@ extern "C" {
  * Writes h for every token (skipped when NULL) and the state after each
  * sequence's last token to h_T (skipped when NULL), starting from h0 (zeros
  * when NULL).  An empty sequence gives h_T = h0.  kept, when not NULL, gets
- * what the backward wants: the state before every 64th token of the batch
+ * what the backward wants: the state before every 32nd token of the batch
  * (glr_kept_bytes bytes).  The workspace holds glr_fwd_workspace_bytes bytes
  * and may be NULL where that is 0.
  */

@@ -8,9 +8,13 @@ With e = 2^-24 (half a step of fp32), to first order, relative errors:
   step (2 e): the exponent z log2 e is rounded twice (constant and product),
   1.5 e |z|; then 2 e, and e for the sum and 2 e for 1 / x: (1.5 |z| + 5) e;
 - g = -rate s(r): that and e =: eg; below -87 a is held at 1.6e-38;
-- a = e^g: |g| eg + 1.5 e;   e^g - 1: eg + 2 e, as |g e^g / (e^g - 1)| <= 1;
-- m = sqrt(-(e^g - 1)(e^g + 1)): the root halves the errors below it, 2 e for
-  its own step: eg + 2 e + 3 e =: em (with 1 / sqrt: 1 e more);
+- e^g - 1: eg, as |g e^g / (e^g - 1)| <= 1, and 2.2 e (a polynomial off by 0.4 e
+  and two roundings, 1.3e-7 at most in all);
+- a = e^g as 1 + (e^g - 1): |g| eg + e / 2 and 2.2 e (1 / a - 1), which at the far
+  end of what is not reduced, g = -0.69, is 2.2 e: 1.5 e + 2.5 e min(|g|, 0.7);
+- m = sqrt(-(e^g - 1)(e^g + 1)): the product 2 eg + 4.4 e + 2 e, of which the root
+  leaves half; 2 e for its own step, and 2 e more for m = m^2 (1 / sqrt):
+  eg + 7.2 e =: em;
 - u = m s(i) x: em + es(i) + 2 e.
 A state's error obeys  E_t = a E_{t-1} + |a h_{t-1}| (ea + 2 e) + |u| eu + e |h|,
 where 2 e is there for the tiles' products of factors (one rounding a token
@@ -40,8 +44,8 @@ TINY = 2e-38                 # factors below the smallest normal number count as
 def _eps(q):
     es = lambda z: (1.5 * np.minimum(np.abs(z), 90) + 5) * E                 # noqa: E731
     eg = es(q["r"]) + E
-    ea = np.minimum(-q["g"], 90) * eg + 1.5 * E
-    em = eg + 6 * E
+    ea = np.minimum(-q["g"], 90) * eg + (1.5 + 2.5 * np.minimum(-q["g"], 0.7)) * E
+    em = eg + 7.2 * E
     return es(q["r"]), es(q["i"]), ea, em
 
 

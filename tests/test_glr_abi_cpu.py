@@ -53,7 +53,7 @@ def bwd(lib, gated, **kw):
              a["dh0"], a["ws"], a["wsb"], None)
 
 
-SIZES = [(dict(D=0), "D must"), (dict(n=-1), "n_seqs"), (dict(N=-1), "n_tokens"), (dict(N=(1 << 31) - 255), "2^31"),
+SIZES = [(dict(D=0), "D must"), (dict(D=1 << 24), "2^24"), (dict(n=-1), "n_seqs"), (dict(N=-1), "n_tokens"), (dict(N=(1 << 31) - 255), "2^31"),
          (dict(n=7), "multiple"), (dict(n=0), "n_seqs == 0"), (dict(dt=7), "in_dtype"),
          (dict(N=1 << 30, D=1 << 10), "2^40"), (dict(n=1 << 26, D=1 << 15, N=0), "2^40"), (dict(n=1 << 27, N=0), "2^27"),
          (dict(N=1 << 28, D=64), "2^22"), (dict(N=1 << 17, D=1 << 17), "2^22"),
@@ -119,7 +119,7 @@ def test_decode_refusals(lib, gated, kw, msg):
 
 def test_sizes_of_workspaces_and_kept_states(lib):
     import gated_delta_rule_95_amd as m
-    assert lib.glr_kept_bytes(0, 5) == 0 and lib.glr_kept_bytes(1, 5) == 20 and lib.glr_kept_bytes(129, 5) == 60
+    assert lib.glr_kept_bytes(0, 5) == 0 and lib.glr_kept_bytes(1, 5) == 20 and lib.glr_kept_bytes(129, 5) == 100
     for f in (m.glr_fwd_workspace_bytes, m.glr_bwd_workspace_bytes):
         assert f(0, 16) == 0 and f(1 << 20, 16) <= f(1 << 21, 16)
         for bad in ((-1, 16), (16, 0), (1 << 31, 1)):
