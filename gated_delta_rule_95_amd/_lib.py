@@ -32,6 +32,8 @@ def load() -> ctypes.CDLL:
     """Load libkda.so (built by gated_delta_rule_95_amd.build) and declare
     the argument types of every entry point."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -25,6 +25,7 @@ __all__ = ["glr_fwd_scan", "glr_fwd_scan_gated", "glr_bwd_scan", "glr_bwd_scan_g
            "glr_bwd_workspace_bytes"]
 
 _DT = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
+_F32 = torch.float32
 
 
 def _run(dev: torch.device, fn, *args) -> None:
@@ -38,6 +39,21 @@ def _run(dev: torch.device, fn, *args) -> None:
         _lib.check(st)
 
 
+def _check(dev: torch.device, *what) -> None:
+    """what: (tensor or None, name, dtype, shape), each as _need checks it."""
+    for t, name, dtype, shape in what:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                                  and t.is_contiguous() and t.device == dev):
+            _need(t, name, dtype, shape, dev)
+
+
+def _given(*what) -> None:
+    """what: (tensor, name) that must not be None."""
+    for t, name in what:
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+
+
 class _Batch:
     """Sizes of a batch of x [B, T, D] or packed [N, D]; checks everything
     whose shape follows from them."""
@@ -48,40 +64,44 @@ class _Batch:
         self.dev = dev = x.device
         if dev.type != "cuda":
             raise ValueError(f"x is on {dev}: the kernels run on a GPU, there is no CPU fallback")
-        if x.dim() not in (2, 3):
+        self.shape = shape = x.shape
+        dims, dt = len(shape), x.dtype
+        if dims not in (2, 3):
             raise ValueError("x must be [B, T, D] or [N, D]")
-        if x.dtype not in _DT:
-            raise TypeError(f"unsupported dtype {x.dtype}; the gated linear recurrence takes bfloat16 or float32")
-        self.dt, self.shape = _DT[x.dtype], x.shape
-        self.D = x.shape[-1]
+        if dt not in _DT:
+            raise TypeError(f"unsupported dtype {dt}; the gated linear recurrence takes bfloat16 or float32")
+        self.dt, self.D = _DT[dt], shape[-1]
         if self.D < 1:
             raise ValueError("x must have a channel")
-        self.N = x.shape[0] if x.dim() == 2 else x.shape[0] * x.shape[1]
+        self.N = shape[0] if dims == 2 else shape[0] * shape[1]
         if cu_seqlens is not None:
-            if x.dim() == 3 and x.shape[0] != 1:
+            if dims == 3 and shape[0] != 1:
                 raise ValueError("cu_seqlens needs packed input ([N, D] or [1, N, D])")
             if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
                 raise ValueError("cu_seqlens must be a 1-D tensor of n_seqs + 1 entries")
             _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
             self.n_seqs = cu_seqlens.numel() - 1
         else:
-            self.n_seqs = x.shape[0] if x.dim() == 3 else 1
-        _need(x, "x", x.dtype, x.shape, dev)
+            self.n_seqs = shape[0] if dims == 3 else 1
         if len(gates) == 1:
-            _need(gates[0], "g", torch.float32, x.shape, dev)
+            g, = gates
+            _given((g, "g"))
+            _check(dev, (x, "x", dt, shape), (g, "g", _F32, shape))
+            self.ins = (x.data_ptr(), g.data_ptr())
         else:
-            _need(gates[0], "r", x.dtype, x.shape, dev)
-            _need(gates[1], "i", x.dtype, x.shape, dev)
-            _need(gates[2], "rate", torch.float32, (self.D,), dev)
-        self.state = torch.Size((self.n_seqs, self.D))
+            r, i, rate = gates
+            _given((r, "r"), (i, "i"), (rate, "rate"))
+            _check(dev, (x, "x", dt, shape), (r, "r", dt, shape), (i, "i", dt, shape), (rate, "rate", _F32, (self.D,)))
+            self.ins = (x.data_ptr(), r.data_ptr(), i.data_ptr(), rate.data_ptr())
+        self.state = (self.n_seqs, self.D)
 
     def kept(self):
         """The shape of the kept states, from the bytes the library asks for."""
-        return torch.Size((_lib.load().glr_kept_bytes(self.N, self.D) // (4 * self.D), self.D))
+        return _lib.load().glr_kept_bytes(self.N, self.D) // (4 * self.D), self.D
 
     def workspace(self, need, given):
         if given is not None:
-            _need(given, "workspace", torch.uint8, given.shape, self.dev)
+            _need(given, "workspace", torch.uint8, getattr(given, "shape", None), self.dev)
             return given
         return torch.empty(need, dtype=torch.uint8, device=self.dev) if need else None
 
@@ -98,20 +118,15 @@ def glr_bwd_workspace_bytes(n_tokens: int, D: int) -> int:
 
 def _fwd(fn, x, gates, h0, cu_seqlens, output_final_state, keep, h, h_T, workspace):
     b = _Batch(x, gates, cu_seqlens)
-    if h0 is not None:
-        _need(h0, "h0", torch.float32, b.state, b.dev)
+    _check(b.dev, (h0, "h0", _F32, b.state), (h, "h", x.dtype, b.shape), (h_T, "h_T", _F32, b.state))
     if h is None:
         h = torch.empty_like(x)
-    else:
-        _need(h, "h", x.dtype, x.shape, b.dev)
-    if h_T is not None:
-        _need(h_T, "h_T", torch.float32, b.state, b.dev)
-    elif output_final_state:
-        h_T = torch.empty(b.state, dtype=torch.float32, device=b.dev)
-    kept = torch.empty(b.kept(), dtype=torch.float32, device=b.dev) if keep else None
+    if h_T is None and output_final_state:
+        h_T = torch.empty(b.state, dtype=_F32, device=b.dev)
+    kept = torch.empty(b.kept(), dtype=_F32, device=b.dev) if keep else None
     ws = b.workspace(_lib.load().glr_fwd_workspace_bytes(b.N, b.D), workspace)
-    _run(b.dev, fn, _ptr(x), *(_ptr(t) for t in gates), _ptr(h0), _ptr(cu_seqlens), b.n_seqs, b.N, b.D, b.dt,
-         _ptr(h), _ptr(h_T), _ptr(kept), _ptr(ws), 0 if ws is None else ws.numel())
+    _run(b.dev, fn, *b.ins, _ptr(h0), _ptr(cu_seqlens), b.n_seqs, b.N, b.D, b.dt, h.data_ptr(), _ptr(h_T), _ptr(kept),
+         _ptr(ws), 0 if ws is None else ws.numel())
     return (h, h_T, kept) if keep else (h, h_T)
 
 
@@ -149,19 +164,16 @@ def glr_fwd_scan_gated(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, rate: 
 
 def _bwd(fn, x, gates, dh, h0, dh_T, cu_seqlens, kept, workspace):
     b = _Batch(x, gates, cu_seqlens)
-    _need(dh, "dh", x.dtype, x.shape, b.dev)
-    if h0 is not None:
-        _need(h0, "h0", torch.float32, b.state, b.dev)
-    if dh_T is not None:
-        _need(dh_T, "dh_T", torch.float32, b.state, b.dev)
+    _given((dh, "dh"))
+    _check(b.dev, (dh, "dh", x.dtype, b.shape), (h0, "h0", _F32, b.state), (dh_T, "dh_T", _F32, b.state))
     if kept is not None:
-        _need(kept, "kept", torch.float32, b.kept(), b.dev)
+        _check(b.dev, (kept, "kept", _F32, b.kept()))
     ws = b.workspace(_lib.load().glr_bwd_workspace_bytes(b.N, b.D), workspace)
     # the gradients of x and of the gates are shaped like them
     out = [torch.empty_like(x)] + [torch.empty_like(t) for t in gates]
-    out.append(torch.empty(b.state, dtype=torch.float32, device=b.dev))
-    _run(b.dev, fn, _ptr(x), *(_ptr(t) for t in gates), _ptr(h0), _ptr(cu_seqlens), b.n_seqs, b.N, b.D, b.dt,
-         _ptr(kept), _ptr(dh), _ptr(dh_T), *(_ptr(t) for t in out), _ptr(ws), 0 if ws is None else ws.numel())
+    out.append(torch.empty(b.state, dtype=_F32, device=b.dev))
+    _run(b.dev, fn, *b.ins, _ptr(h0), _ptr(cu_seqlens), b.n_seqs, b.N, b.D, b.dt, _ptr(kept), dh.data_ptr(), _ptr(dh_T),
+         *[t.data_ptr() for t in out], _ptr(ws), 0 if ws is None else ws.numel())
     return tuple(out)
 
 
@@ -189,19 +201,18 @@ def glr_bwd_scan_gated(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, rate: 
 
 
 def _decode(fn, x, gates, S, slots, h):
-    if isinstance(x, torch.Tensor) and x.dim() != 2:
-        raise ValueError("x must be [N, D]")
     b = _Batch(x, gates, None)
+    shape = b.shape
+    if len(shape) != 2:
+        raise ValueError("x must be [N, D]")
     if not isinstance(S, torch.Tensor) or S.dim() != 2:
         raise ValueError("S must be [n_slots, D]")
-    _need(S, "S", torch.float32, S.shape[:1] + b.shape[1:], b.dev)
-    if slots is not None:
-        _need(slots, "slots", torch.int32, x.shape[:1], b.dev)
+    n_slots = S.shape[0]
+    _check(b.dev, (S, "S", _F32, (n_slots, b.D)), (slots, "slots", torch.int32, shape[:1]), (h, "h", x.dtype, shape))
     if h is None:
         h = torch.empty_like(x)
-    else:
-        _need(h, "h", x.dtype, x.shape, b.dev)
-    _run(b.dev, fn, _ptr(x), *(_ptr(t) for t in gates), _ptr(S), _ptr(slots), S.shape[0], b.N, b.D, b.dt, _ptr(h))
+    _run(b.dev, fn, *b.ins, S.data_ptr(), None if slots is None else slots.data_ptr(), n_slots, b.N, b.D, b.dt,
+         h.data_ptr())
     return h
 
 

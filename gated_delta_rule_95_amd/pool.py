@@ -14,7 +14,8 @@ kernels on the device of the slot numbers and its current stream.
 """
 from __future__ import annotations
 
-import ctypes
+import array
+import math
 from typing import Optional, Sequence, Union
 
 import torch
@@ -45,21 +46,24 @@ def _rows(pools: Pools, name: str, n_slots: Optional[int], dev):
     for p in pools:
         if not isinstance(p, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor or a list of them")
-        if p.dim() < 1:
+        shape = p.shape
+        if not shape:
             raise ValueError(f"{name} must be [n_slots, ...]")
         if n_slots is None:
-            n_slots = p.shape[0]
-        _need(p, name, p.dtype, (n_slots,) + p.shape[1:], dev)
-        row = p.element_size()
-        for x in p.shape[1:]:
-            row *= x
+            n_slots = shape[0]
+        if shape[0] != n_slots or p.device != dev or not p.is_contiguous():
+            _need(p, name, p.dtype, (n_slots,) + shape[1:], dev)
+        row = math.prod(shape[1:]) * p.element_size()
         if row == 0:
             raise ValueError(f"{name} must have rows of one element at least")
         words += (p.data_ptr(), row)
-    return (ctypes.c_size_t * len(words))(*words), len(words) // 2, 0 if n_slots is None else n_slots
+    return array.array("Q", words), len(words) // 2, 0 if n_slots is None else n_slots
 
 
 def _used(used):
+    if isinstance(used, torch.Tensor) and used.dtype is torch.bool and used.is_cuda and used.dim() == 1 \
+            and used.is_contiguous():
+        return used.device, used.shape[0]
     dev = _device(used, "used")
     if used.dim() != 1:
         raise ValueError("used must be [n_slots]")
@@ -68,6 +72,8 @@ def _used(used):
 
 
 def _numbers(t, name, dev):
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev and t.dim() == 1 and t.is_contiguous():
+        return t.shape[0]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 1:
@@ -85,7 +91,7 @@ def pool_alloc(pools: Pools, used: torch.Tensor, n: int) -> torch.Tensor:
     if n < 0:
         raise ValueError("n must be >= 0")
     slots = torch.empty(n, dtype=torch.int32, device=dev)
-    _run(dev, _lib.load().pool_alloc, rows, k, _ptr(used), n_slots, n, _ptr(slots))
+    _run(dev, _lib.load().pool_alloc, rows.buffer_info()[0], k, _ptr(used), n_slots, n, _ptr(slots))
     return slots
 
 
@@ -98,7 +104,7 @@ def pool_fork(pools: Pools, used: torch.Tensor, src: torch.Tensor) -> torch.Tens
     n = _numbers(src, "src", dev)
     rows, k, _ = _rows(pools, "pools", n_slots, dev)
     dst = torch.empty_like(src)
-    _run(dev, _lib.load().pool_fork, rows, k, _ptr(used), n_slots, _ptr(src), n, _ptr(dst))
+    _run(dev, _lib.load().pool_fork, rows.buffer_info()[0], k, _ptr(used), n_slots, _ptr(src), n, _ptr(dst))
     return dst
 
 
@@ -131,7 +137,7 @@ def pool_compact(pools: Pools, used: torch.Tensor, table: Optional[torch.Tensor]
     else:
         _need(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
     remap = torch.empty(n_slots, dtype=torch.int32, device=dev)
-    _run(dev, _lib.load().pool_compact, rows, k, _ptr(used), n_slots, _ptr(table),
+    _run(dev, _lib.load().pool_compact, rows.buffer_info()[0], k, _ptr(used), n_slots, _ptr(table),
          0 if table is None else table.numel(), _ptr(remap), _ptr(workspace), workspace.numel())
     return remap
 
@@ -150,4 +156,4 @@ def pool_copy(from_pools: Pools, src: torch.Tensor, to_pools: Pools, dst: torch.
     b, m, to_slots = _rows(to_pools, "to_pools", None, dev)
     if k != m:
         raise ValueError("to_pools must be as many as from_pools")
-    _run(dev, _lib.load().pool_copy, a, b, k, from_slots, to_slots, _ptr(src), _ptr(dst), n)
+    _run(dev, _lib.load().pool_copy, a.buffer_info()[0], b.buffer_info()[0], k, from_slots, to_slots, _ptr(src), _ptr(dst), n)
