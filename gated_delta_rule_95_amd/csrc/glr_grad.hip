@@ -351,8 +351,13 @@ hipError_t launch_bwd(const Args &arg)
         f.ws = chain;
         if ((e = launch_fwd(f)) != hipSuccess) return e;
     }
-    const int V = channels(a);
-    const Chain ch = make_chain(chain, (int)tiles_of(a.n_tokens, a.gated, V), (a.D + WAVE * V - 1) / (WAVE * V),
+    // gated, pairs of channels (and their smaller tiles) once there are 16
+    // workgroups of them for each compute unit (4096 channels: 2048 tokens 45.3
+    // us with pairs and 43.8 without, 4096 tokens 73.2 and 75.7); plain, always
+    // (256 tokens 10.5 and 11.0)
+    const int least = a.gated ? 4096 : 0;
+    const int V = pairs_fit(a) && tiles_of(a.n_tokens, a.gated, 2) * blocks_of(a.D, 2) >= least ? 2 : 1;
+    const Chain ch = make_chain(chain, (int)tiles_of(a.n_tokens, a.gated, V), blocks_of(a.D, V),
                                 empty_groups(a, a.dh0));
     if (ch.items) {
         if ((e = clear_chain(ch, a.D, a.stream)) != hipSuccess) return e;

@@ -262,7 +262,7 @@ inline int64_t empty_groups(const Args &a, bool wanted)
 // the gates of fp32 inputs, whose pairs would not fit the registers beside a
 // second workgroup (and fill whole lines of memory without them).
 template <typename T, bool GATED> constexpr bool kPairs = sizeof(T) == 2 || !GATED;
-inline int channels(const Args &a)
+inline bool pairs_fit(const Args &a)
 {
     const size_t es = a.bf16 ? 2 : 4;
     uintptr_t in = 0, st = 0;
@@ -271,7 +271,8 @@ inline int channels(const Args &a)
     for (const float *p : {a.g, a.rate, a.h0, (const float *)a.h_T, (const float *)a.kept, a.dh_T, (const float *)a.dg,
                            (const float *)a.drate, (const float *)a.dh0})
         st |= reinterpret_cast<uintptr_t>(p);
-    return (a.bf16 || !a.gated) && a.D % 2 == 0 && in % (2 * es) == 0 && st % 8 == 0 ? 2 : 1;
+    return (a.bf16 || !a.gated) && a.D % 2 == 0 && in % (2 * es) == 0 && st % 8 == 0;
 }
+inline int blocks_of(int32_t D, int V) { return (D + WAVE * V - 1) / (WAVE * V); }
 
 }  // namespace glr
