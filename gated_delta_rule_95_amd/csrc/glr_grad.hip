@@ -296,6 +296,7 @@ __global__ __launch_bounds__(RW * WAVE) void glr_rate_kernel(Args a, const float
     const int tiles = (total_tokens(seq_args(a)) + C - 1) / C;
     double sum = 0;
     if (c < a.D)
+#pragma unroll 8
         for (int t = w; t < tiles; t += RW) sum += (double)part[(int64_t)t * a.D + c];
     s_sum[w][lane] = sum;
     __syncthreads();

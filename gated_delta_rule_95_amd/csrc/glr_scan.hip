@@ -183,8 +183,9 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
 __global__ __launch_bounds__(256) void glr_clear_kernel(Chain c, int64_t words)
 {
     if (blockIdx.x == 0 && threadIdx.x == 0) *c.ticket = 0;
-    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256)
-        c.words[i] = kEmpty;
+    typedef uint64_t u2 __attribute__((ext_vector_type(2)));        // (chain_bytes leaves room for an even count)
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; 2 * i < words; i += (int64_t)gridDim.x * 256)
+        reinterpret_cast<u2 *>(c.words)[i] = u2{kEmpty, kEmpty};
 }
 
 int64_t tiles_of(int64_t n_tokens) { return (n_tokens + C - 1) / C; }
@@ -206,8 +207,8 @@ void launch_v(const Args &a, const Chain &ch, int V, hipStream_t s)
 hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s)
 {
     if (!c.ticket) return hipSuccess;
-    const int64_t words = (int64_t)c.tiles * D, blocks = (words + 1023) / 1024;
-    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, c, words);
+    const int64_t words = (int64_t)c.tiles * D, blocks = (words + 511) / 512;
+    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, c, words);
     return hipGetLastError();
 }
 

@@ -42,8 +42,13 @@ __device__ __forceinline__ void st(T *p, const float *x)
 // offset and a lane's channel a vector one, so addresses cost no vector
 // arithmetic; rows past the last read zeros and are not written, and so are
 // channels at kNowhere.
+// Pairs (the large calls) stream past the caches, "nt" both ways: 65536 tokens
+// of 4096 channels 421 -> 397 us, the gradients of 20011 gated ones 299 -> 290;
+// single channels (the small calls, whose rows the caches may hold) do not:
+// 1517 tokens of 1001 in fp32 took 25.6 us, with it 26.5.
 constexpr unsigned kNowhere = 0x80000000u;
 template <typename T, int V> struct Rows {
+    static constexpr int kCache = V == 2 ? 2 : 0;
     typedef typename Row<T, V>::raw raw;
     gdr::rsrc_t r;
     unsigned row;
@@ -56,22 +61,22 @@ template <typename T, int V> struct Rows {
     __device__ __forceinline__ raw ld(int k, unsigned c) const
     {
         if constexpr (sizeof(raw) == 2)
-            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, c, k * row, 0));
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, c, k * row, kCache));
         else if constexpr (sizeof(raw) == 4)
-            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, c, k * row, 0));
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, c, k * row, kCache));
         else
-            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, c, k * row, 0));
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, c, k * row, kCache));
     }
     __device__ __forceinline__ void st(int k, unsigned c, const float *x) const
     {
         const raw v = Row<T, V>::pack(x);
         typedef unsigned u2 __attribute__((ext_vector_type(2)));
         if constexpr (sizeof(raw) == 2)
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, c, k * row, 0);
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, c, k * row, kCache);
         else if constexpr (sizeof(raw) == 4)
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, c, k * row, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, c, k * row, kCache);
         else
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), r, c, k * row, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), r, c, k * row, kCache);
     }
 };
 

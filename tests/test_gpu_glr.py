@@ -104,6 +104,63 @@ def test_random_batches(seed):
     compare(b, kept=bool(r.integers(2)))
 
 
+WIDE = [(BF, True, 8192), (BF, False, 8192), (F32, False, 8190), (F32, True, 8192), (BF, True, 8191)]
+
+
+@pytest.mark.parametrize("dtype,gated,D", WIDE)
+def test_wide_batches(dtype, gated, D):
+    """Calls large enough for the forms with pairs of channels: borders of every
+    kind inside, on and around the tiles' own, empty sequences, rows behind."""
+    lens = [1, 0, 31, 32, 33, 500, 127, 128, 129, 0, 2, 700, 64, 0, 300, 5, 40]
+    b = make(24, lens, D, dtype, gated, behind=70)
+    compare(b, kept=False)
+    compare({**b, "h0": None, "dh_T": None})
+
+
+@pytest.mark.parametrize("dtype,gated,D", [(BF, True, 512), (BF, False, 256), (F32, False, 256)])
+def test_long_batches(dtype, gated, D):
+    """The same forms, many tiles of few channels in a chain."""
+    compare(make(25, [33000, 1, 200], D, dtype, gated, decays="slow"))
+
+
+@pytest.mark.parametrize("dtype,gated,D", WIDE[:3])
+def test_wide_nonfinite_values_and_rows_of_no_sequence(dtype, gated, D):
+    """As the small tests below, in the forms with pairs of channels."""
+    lens = [70, 1500, 0, 300, 5, 140]
+    N = sum(lens)
+    b = make(26, lens, D, dtype, gated, behind=200)
+    for k in ("x", "dh") + (("r", "i") if gated else ("g",)):
+        b[k][N:] = float("nan")
+    good_h, good = [torch.full_like(b["x"], FILL), None], bwd(b)
+    _, good_hT = fwd(b, h=good_h[0])
+    torch.cuda.synchronize()
+    assert bool((good_h[0][N:] == FILL).all())
+    for k in ("x", "dh") + (("r", "i") if gated else ("g",)):
+        for bad in (float("nan"), float("inf")):
+            c = dict(b, **{k: b[k].clone()})
+            c[k][700, 3] = bad
+            h, h_T = fwd(c, h=torch.full_like(b["x"], FILL))
+            grads = bwd(c)
+            torch.cuda.synchronize()
+            keep = torch.ones(N, D, dtype=torch.bool, device="cuda")
+            keep[70:1570, 3] = False
+            n = torch.ones(len(lens), D, dtype=torch.bool, device="cuda")
+            n[1, 3] = False
+            if k != "dh":
+                assert torch.equal(h[:N][keep], good_h[0][:N][keep]) and torch.equal(h_T[n], good_hT[n])
+                if bad != bad:
+                    assert bool(torch.isnan(h[700:1570, 3]).all())
+            for x, y, name in zip(grads, good, names(b)):
+                x, y = (x[:N], y[:N]) if x.shape[0] == N + 200 else (x, y)
+                m = keep if x.shape == keep.shape else n if x.shape == n.shape else n[1]
+                assert torch.equal(x[m], y[m]), (k, name)
+    # gradients of outputs that are guarded: nothing behind the last sequence is written
+    _, _, kept = fwd(b, keep=True)
+    for x in call_bwd(b, len(lens), b["cu"], kept):
+        if x.shape[0] == N + 200:
+            assert bool((x[N:] == FILL).all())
+
+
 @pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
 def test_kept_states_are_optional(gated):
     b = make(3, [100, 0, 301, 64], 66, F32, gated)
@@ -373,11 +430,11 @@ def test_streams_and_devices():
 
 
 @pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
-@pytest.mark.parametrize("D", [64, 1024])
-def test_runs_are_bit_identical(D, gated):
+@pytest.mark.parametrize("D,lens", [(64, [9000, 1, 7000]), (1024, [9000, 1, 7000]), (4096, [4000, 300])])
+def test_runs_are_bit_identical(D, lens, gated):
     """However far the tiles before a tile have come when it looks: beside
     nothing and beside a stream of other work."""
-    b = make(23, [9000, 1, 7000], D, BF, gated)
+    b = make(23, lens, D, BF, gated)
     want = fwd(b, keep=True) + bwd(b)
     other, side = torch.randn(4096, 4096, device="cuda"), torch.cuda.Stream()
     for k in range(6):
