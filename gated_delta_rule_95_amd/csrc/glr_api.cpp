@@ -5,6 +5,7 @@
 #include "api_checks.h"
 #include "glr.h"
 #include "glr_launch.h"
+#include "glr_plan.h"
 
 #define GLR_API extern "C" __attribute__((visibility("default")))
 
@@ -49,10 +50,8 @@ kda_status check_seqs(int32_t n_seqs, int64_t n_tokens, int32_t D, const int32_t
     return KDA_OK;
 }
 
-size_t kept_bytes(int64_t n_tokens, int32_t D)
-{
-    return (size_t)((n_tokens + glr::kKept - 1) / glr::kKept) * D * 4;
-}
+size_t kept_bytes(int64_t n_tokens, int32_t D) { return (size_t)glr::tiles_of(n_tokens, glr::kKept) * D * 4; }
+size_t fwd_bytes(int64_t n_tokens, int32_t D) { return glr::chain_bytes(glr::tiles_of(n_tokens, glr::kScanTile), D); }
 
 kda_status check_workspace(const void *ws, size_t bytes, size_t need, const char *fn)
 {
@@ -73,7 +72,7 @@ kda_status fwd(const char *fn, glr::Args a, int64_t n_tokens, kda_dtype in_dtype
     if (a.n_seqs == 0) return ok();
     const bool tok = n_tokens > 0;
     const size_t ib = in_dtype == KDA_BF16 ? 2 : 4, row = (size_t)n_tokens * a.D;
-    const size_t st = (size_t)a.n_seqs * a.D * 4, need = glr::fwd_workspace(n_tokens, a.D);
+    const size_t st = (size_t)a.n_seqs * a.D * 4, need = fwd_bytes(n_tokens, a.D);
     if ((s = check_workspace(a.ws, ws_bytes, need, "glr_fwd_workspace_bytes")) != KDA_OK) return s;
     const bool gt = a.gated;
     const Buf bufs[] = {
@@ -99,7 +98,7 @@ kda_status bwd(const char *fn, glr::Args a, int64_t n_tokens, kda_dtype in_dtype
     if ((s = check_seqs(a.n_seqs, n_tokens, a.D, a.cu_seqlens)) != KDA_OK) return s;
     const bool tok = n_tokens > 0, gt = a.gated;
     const size_t ib = in_dtype == KDA_BF16 ? 2 : 4, row = (size_t)n_tokens * a.D;
-    const size_t st = (size_t)a.n_seqs * a.D * 4, need = glr::bwd_workspace(n_tokens, a.D);
+    const size_t st = (size_t)a.n_seqs * a.D * 4, need = glr::GradParts::bytes(n_tokens, a.D);
     if ((s = check_workspace(a.ws, ws_bytes, need, "glr_bwd_workspace_bytes")) != KDA_OK) return s;
     const Buf bufs[] = {
         {a.x, "x", tok, ib, row * ib, false}, {a.r, "r", tok && gt, ib, row * ib, false},
@@ -162,12 +161,12 @@ GLR_API size_t glr_kept_bytes(int64_t n_tokens, int32_t D)
 
 GLR_API size_t glr_fwd_workspace_bytes(int64_t n_tokens, int32_t D)
 {
-    return check_sizes(n_tokens, D) == KDA_OK ? glr::fwd_workspace(n_tokens, D) : 0;
+    return check_sizes(n_tokens, D) == KDA_OK ? fwd_bytes(n_tokens, D) : 0;
 }
 
 GLR_API size_t glr_bwd_workspace_bytes(int64_t n_tokens, int32_t D)
 {
-    return check_sizes(n_tokens, D) == KDA_OK ? glr::bwd_workspace(n_tokens, D) : 0;
+    return check_sizes(n_tokens, D) == KDA_OK ? glr::GradParts::bytes(n_tokens, D) : 0;
 }
 
 GLR_API kda_status glr_fwd_scan(const void *x, const float *g, const float *h0,

@@ -14,17 +14,12 @@
 namespace glr {
 namespace {
 
-constexpr int K = 8;
-// Eight waves a tile, but four where each lane forms the gates of two channels
-// and a workgroup of eight would leave room for no second one beside it.
-constexpr int waves(bool gated, int V) { return gated && V == 2 ? 4 : 8; }
-constexpr int tokens(bool gated, int V) { return waves(gated, V) * K; }
-static_assert(tokens(true, 2) % kKept == 0 && tokens(true, 1) % kKept == 0, "a tile starts from a kept state");
+constexpr int K = kGradTokens;
 
 template <typename T, bool GATED, int V>
-__global__ __launch_bounds__(waves(GATED, V) * WAVE) void glr_grad_kernel(Args a, Chain chain, float *part)
+__global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(Args a, Chain chain, float *part)
 {
-    constexpr int NW = waves(GATED, V), C = tokens(GATED, V), NT = NW * WAVE;
+    constexpr int NW = grad_waves(GATED, V), C = grad_tile(GATED, V), NT = NW * WAVE;
     typedef Row<T, V> R;
     typedef Row<float, V> RF;
     __shared__ int s_idx, s_first[C], s_last[C];
@@ -306,73 +301,48 @@ __global__ __launch_bounds__(RW * WAVE) void glr_rate_kernel(Args a, const float
     }
 }
 
-int64_t tiles_of(int64_t n_tokens, bool gated, int V)
-{
-    return (n_tokens + tokens(gated, V) - 1) / tokens(gated, V);
-}
-// one fp32 row for each kept state, and no fewer than tiles
-size_t rows_bytes(int64_t n_tokens, int32_t D)
-{
-    return ((size_t)((n_tokens + kKept - 1) / kKept) * D * 4 + 255) & ~(size_t)255;
-}
-
 template <typename T, bool GATED>
 void launch_v(const Args &a, const Chain &ch, float *part, int V, hipStream_t s)
 {
     const dim3 grid((unsigned)ch.items);
     if constexpr (kPairs<T, GATED>)
         if (V == 2) {
-            hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 2>), grid, dim3(waves(GATED, 2) * WAVE), 0, s, a, ch, part);
+            hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 2>), grid, dim3(grad_waves(GATED, 2) * WAVE), 0, s, a, ch, part);
             return;
         }
-    hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 1>), grid, dim3(waves(GATED, 1) * WAVE), 0, s, a, ch, part);
+    hipLaunchKernelGGL((glr_grad_kernel<T, GATED, 1>), grid, dim3(grad_waves(GATED, 1) * WAVE), 0, s, a, ch, part);
 }
 
 }  // namespace
 
-// kept states (where they are formed again), the tiles' shares of drate, the
-// chain (the forward's first, which is never longer)
-size_t bwd_workspace(int64_t n_tokens, int32_t D)
-{
-    return 2 * rows_bytes(n_tokens, D) + chain_bytes(tiles_of(n_tokens, true, 2), D);
-}
-
 hipError_t launch_bwd(const Args &arg)
 {
     Args a = arg;
-    const size_t rows = rows_bytes(a.n_tokens, a.D);
-    float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + rows);
-    void *chain = static_cast<char *>(a.ws) + 2 * rows;
+    const GradParts w(a);
     hipError_t e;
     if (!a.kept && a.n_tokens) {
-        a.kept = static_cast<float *>(a.ws);
+        a.kept = w.kept;
         Args f = a;
         f.h = nullptr;
         f.h_T = nullptr;
-        f.ws = chain;
+        f.ws = w.chain;
         if ((e = launch_fwd(f)) != hipSuccess) return e;
     }
-    // gated, pairs of channels (and their smaller tiles) once there are 16
-    // workgroups of them for each compute unit (4096 channels: 2048 tokens 45.3
-    // us with pairs and 43.8 without, 4096 tokens 73.2 and 75.7); plain, always
-    // (256 tokens 10.5 and 11.0)
-    const int least = a.gated ? 4096 : 0;
-    const int V = pairs_fit(a) && tiles_of(a.n_tokens, a.gated, 2) * blocks_of(a.D, 2) >= least ? 2 : 1;
-    const Chain ch = make_chain(chain, (int)tiles_of(a.n_tokens, a.gated, V), blocks_of(a.D, V),
-                                empty_groups(a, a.dh0));
-    if (ch.items) {
-        if ((e = clear_chain(ch, a.D, a.stream)) != hipSuccess) return e;
-        if (a.bf16) a.gated ? launch_v<bf16, true>(a, ch, part, V, a.stream) : launch_v<bf16, false>(a, ch, part, V, a.stream);
-        else a.gated ? launch_v<float, true>(a, ch, part, V, a.stream) : launch_v<float, false>(a, ch, part, V, a.stream);
+    const Plan p = plan_grad(a, w.chain);
+    if (p.chain.items) {
+        if ((e = clear_chain(p.chain, a.D, a.stream)) != hipSuccess) return e;
+        if (a.bf16)
+            a.gated ? launch_v<bf16, true>(a, p.chain, w.part, p.V, a.stream)
+                    : launch_v<bf16, false>(a, p.chain, w.part, p.V, a.stream);
+        else
+            a.gated ? launch_v<float, true>(a, p.chain, w.part, p.V, a.stream)
+                    : launch_v<float, false>(a, p.chain, w.part, p.V, a.stream);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (a.gated) {
-        hipLaunchKernelGGL(glr_rate_kernel, dim3((unsigned)((a.D + WAVE - 1) / WAVE)), dim3(RW * WAVE), 0, a.stream, a, part,
-                           tokens(true, V));
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    if (!a.gated) return hipSuccess;
+    hipLaunchKernelGGL(glr_rate_kernel, dim3((unsigned)blocks_of(a.D, 1)), dim3(RW * WAVE), 0, a.stream, a, w.part,
+                       grad_tile(true, p.V));
+    return hipGetLastError();
 }
 
 }  // namespace glr

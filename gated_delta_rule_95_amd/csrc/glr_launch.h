@@ -42,8 +42,6 @@ struct DecodeArgs {
     hipStream_t stream;
 };
 
-size_t fwd_workspace(int64_t n_tokens, int32_t D);
-size_t bwd_workspace(int64_t n_tokens, int32_t D);
 hipError_t launch_fwd(const Args &a);
 hipError_t launch_bwd(const Args &a);
 hipError_t launch_decode(const DecodeArgs &a);

@@ -1,0 +1,126 @@
+// How a call of the gated linear recurrence is cut into tiles, and what its
+// workspace holds: host arithmetic of sizes only.
+#pragma once
+
+#include "glr_launch.h"
+
+namespace glr {
+
+constexpr int kLanes = 64;
+
+// The scan: a tile is 128 tokens, eight waves of 16.
+constexpr int kScanWaves = 8, kScanTokens = 16, kScanTile = kScanWaves * kScanTokens;
+
+// The gradients: waves of eight tokens, eight to a tile, but four where each
+// lane forms the gates of two channels and a workgroup of eight would leave
+// room for no second one beside it (20011 tokens of 4096 channels: 401 us with
+// eight, 300 with four; plain, 221 with eight and 281 with four).
+constexpr int kGradTokens = 8;
+constexpr int grad_waves(bool gated, int V) { return gated && V == 2 ? 4 : 8; }
+constexpr int grad_tile(bool gated, int V) { return grad_waves(gated, V) * kGradTokens; }
+static_assert(grad_tile(true, 2) % kKept == 0 && grad_tile(true, 1) % kKept == 0, "a tile starts from a kept state");
+static_assert(kScanTile % kKept == 0 && kKept % kScanTokens == 0, "kept states lie at the waves' borders");
+
+inline int64_t tiles_of(int64_t n_tokens, int tile) { return (n_tokens + tile - 1) / tile; }
+inline int blocks_of(int32_t D, int V) { return (D + kLanes * V - 1) / (kLanes * V); }
+inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Workspace of a chain: a ticket, then one word for each tile and channel.
+// Workgroups take tiles in order, by the ticket, and store a map before they
+// wait, so a tile waits only for tiles that workgroups which run already have
+// taken, and the lowest of those waits for nothing: every wait ends.
+// (Workgroups that stay and ask for their next tile ahead were slower, 20011
+// tokens of 4096 channels 155 -> 223 us and their gradients 297 -> 353: the
+// tile they hold waits for the one they are at.  Without asking ahead the
+// gradients took as long as now, and the scan, short of registers, 195.)
+struct Chain {
+    uint32_t *ticket;                    // nullptr: one tile, which needs no chain
+    uint64_t *words;
+    int tiles, blocks;                   // of tokens, of channels
+    int items;                           // what is handed out: tiles, then groups of sequences
+};
+constexpr size_t kChainHead = 256;
+inline size_t chain_bytes(int64_t tiles, int32_t D)
+{
+    return tiles > 1 ? kChainHead + round256((size_t)tiles * D * 8) : 0;
+}
+inline Chain make_chain(void *ws, int tiles, int blocks, int64_t groups)
+{
+    const int items = (int)((int64_t)tiles * blocks + groups);
+    if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks, items};
+    return Chain{static_cast<uint32_t *>(ws),
+                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + kChainHead), tiles, blocks, items};
+}
+
+// workgroups that look for empty sequences, 64 each
+inline int64_t empty_groups(const Args &a, bool wanted)
+{
+    return wanted && (a.cu_seqlens || !a.n_tokens) ? ((int64_t)a.n_seqs + kLanes - 1) / kLanes : 0;
+}
+
+// Pairs of channels a lane can be taken where every row of every tensor starts
+// on a pair (D even, addresses to two elements); but not for the gates of fp32
+// inputs, whose pairs would not fit the registers beside a second workgroup
+// (and fill whole lines of memory without them).
+inline bool pairs_fit(const Args &a)
+{
+    const size_t es = a.bf16 ? 2 : 4;
+    uintptr_t in = 0, st = 0;
+    for (const void *p : {a.x, a.r, a.i, (const void *)a.h, a.dh, (const void *)a.dx, (const void *)a.dr, (const void *)a.di})
+        in |= reinterpret_cast<uintptr_t>(p);
+    for (const float *p : {a.g, a.rate, a.h0, (const float *)a.h_T, (const float *)a.kept, a.dh_T, (const float *)a.dg,
+                           (const float *)a.drate, (const float *)a.dh0})
+        st |= reinterpret_cast<uintptr_t>(p);
+    return (a.bf16 || !a.gated) && a.D % 2 == 0 && in % (2 * es) == 0 && st % 8 == 0;
+}
+
+struct Plan {
+    int V;                               // channels a lane
+    Chain chain;
+};
+
+inline Plan plan_scan(const Args &a)
+{
+    // pairs of channels once there is a workgroup of them for each compute unit,
+    // half the work one after another before that (bf16, gated, 4096 channels:
+    // 77 tokens 9.7 us with pairs and 7.6 without, 512 tokens 12.9 and 12.1,
+    // 1024 tokens 17.4 and 18.6)
+    const int64_t tiles = tiles_of(a.n_tokens, kScanTile);
+    const int V = pairs_fit(a) && tiles * blocks_of(a.D, 2) >= 256 ? 2 : 1;
+    return Plan{V, make_chain(a.ws, (int)tiles, blocks_of(a.D, V), empty_groups(a, a.h_T))};
+}
+
+// workspace of the backward: kept states (where they are formed again), the
+// tiles' shares of drate, the chain (the forward's first, which is never longer)
+struct GradParts {
+    float *kept, *part;
+    void *chain;
+    // one fp32 row for each kept state, and no fewer than tiles
+    static size_t rows(int64_t n_tokens, int32_t D) { return round256((size_t)tiles_of(n_tokens, kKept) * D * 4); }
+    static size_t bytes(int64_t n_tokens, int32_t D)
+    {
+        return 2 * rows(n_tokens, D) + chain_bytes(tiles_of(n_tokens, grad_tile(true, 2)), D);
+    }
+    explicit GradParts(const Args &a)
+    {
+        char *w = static_cast<char *>(a.ws);
+        const size_t r = rows(a.n_tokens, a.D);
+        kept = reinterpret_cast<float *>(w);
+        part = reinterpret_cast<float *>(w + r);
+        chain = w + 2 * r;
+    }
+};
+
+inline Plan plan_grad(const Args &a, void *chain)
+{
+    // gated, pairs of channels (and their smaller tiles) once there are 16
+    // workgroups of them for each compute unit (4096 channels: 2048 tokens 45.3
+    // us with pairs and 43.8 without, 4096 tokens 73.2 and 75.7); plain, always
+    // (256 tokens 10.5 and 11.0)
+    const int least = a.gated ? 4096 : 0;
+    const int V = pairs_fit(a) && tiles_of(a.n_tokens, grad_tile(a.gated, 2)) * blocks_of(a.D, 2) >= least ? 2 : 1;
+    const int tiles = (int)tiles_of(a.n_tokens, grad_tile(a.gated, V));
+    return Plan{V, make_chain(chain, tiles, blocks_of(a.D, V), empty_groups(a, a.dh0))};
+}
+
+}  // namespace glr

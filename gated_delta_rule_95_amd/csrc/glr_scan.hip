@@ -14,7 +14,7 @@
 namespace glr {
 namespace {
 
-constexpr int NW = 8, K = 16, C = NW * K, NT = NW * WAVE;
+constexpr int NW = kScanWaves, K = kScanTokens, C = kScanTile, NT = NW * WAVE;
 
 template <typename T, bool GATED, int V>
 __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
@@ -188,8 +188,6 @@ __global__ __launch_bounds__(256) void glr_clear_kernel(Chain c, int64_t words)
         reinterpret_cast<u2 *>(c.words)[i] = u2{kEmpty, kEmpty};
 }
 
-int64_t tiles_of(int64_t n_tokens) { return (n_tokens + C - 1) / C; }
-
 template <typename T, bool GATED>
 void launch_v(const Args &a, const Chain &ch, int V, hipStream_t s)
 {
@@ -212,22 +210,14 @@ hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s)
     return hipGetLastError();
 }
 
-size_t fwd_workspace(int64_t n_tokens, int32_t D) { return chain_bytes(tiles_of(n_tokens), D); }
-
 hipError_t launch_fwd(const Args &a)
 {
-    // pairs of channels once there is a workgroup of them for each compute unit,
-    // half the work one after another before that (bf16, gated, 4096 channels:
-    // 77 tokens 9.7 us with pairs and 7.6 without, 512 tokens 12.9 and 12.1,
-    // 1024 tokens 17.4 and 18.6)
-    const int64_t tiles = tiles_of(a.n_tokens);
-    const int V = pairs_fit(a) && tiles * blocks_of(a.D, 2) >= 256 ? 2 : 1;
-    const Chain ch = make_chain(a.ws, (int)tiles, blocks_of(a.D, V), empty_groups(a, a.h_T));
-    if (ch.items == 0) return hipSuccess;
-    const hipError_t e = clear_chain(ch, a.D, a.stream);
+    const Plan p = plan_scan(a);
+    if (p.chain.items == 0) return hipSuccess;
+    const hipError_t e = clear_chain(p.chain, a.D, a.stream);
     if (e != hipSuccess) return e;
-    if (a.bf16) a.gated ? launch_v<bf16, true>(a, ch, V, a.stream) : launch_v<bf16, false>(a, ch, V, a.stream);
-    else a.gated ? launch_v<float, true>(a, ch, V, a.stream) : launch_v<float, false>(a, ch, V, a.stream);
+    if (a.bf16) a.gated ? launch_v<bf16, true>(a, p.chain, p.V, a.stream) : launch_v<bf16, false>(a, p.chain, p.V, a.stream);
+    else a.gated ? launch_v<float, true>(a, p.chain, p.V, a.stream) : launch_v<float, false>(a, p.chain, p.V, a.stream);
     return hipGetLastError();
 }
 

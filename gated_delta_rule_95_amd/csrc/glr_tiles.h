@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "glr_device.h"
+#include "glr_plan.h"
 
 namespace glr {
 
@@ -116,30 +117,7 @@ __device__ __forceinline__ Map map_of(uint64_t w)
     return Map{__uint_as_float((uint32_t)(w >> 32)), __uint_as_float((uint32_t)w)};
 }
 
-// Workspace of a chain: a ticket, then one word for each tile and channel.
-// Workgroups take tiles in order, by the ticket, and store a map before they
-// wait, so a tile waits only for tiles that workgroups which run already have
-// taken, and the lowest of those waits for nothing: every wait ends.  (Workgroups that stay, 512 of them, and ask
-// for their next tile ahead were slower: scan of 20011 tokens 155 -> 230 us,
-// gradients 352 -> 535.)
-struct Chain {
-    uint32_t *ticket;                    // nullptr: one tile, which needs no chain
-    uint64_t *words;
-    int tiles, blocks;                   // of tokens, of channels
-    int items;                           // what is handed out: tiles, then groups of sequences
-};
-constexpr size_t kChainHead = 256;
-inline size_t chain_bytes(int64_t tiles, int32_t D)
-{
-    return tiles > 1 ? kChainHead + (((size_t)tiles * D * 8 + 255) & ~(size_t)255) : 0;
-}
-inline Chain make_chain(void *ws, int tiles, int blocks, int64_t groups)
-{
-    const int items = (int)((int64_t)tiles * blocks + groups);
-    if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks, items};
-    return Chain{static_cast<uint32_t *>(ws),
-                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + kChainHead), tiles, blocks, items};
-}
+// the next tile (Chain, in glr_plan.h)
 __device__ __forceinline__ int take(const Chain &c)
 {
     return c.ticket ? (int)atomicAdd(c.ticket, 1u) : (int)blockIdx.x;
@@ -241,6 +219,9 @@ __device__ __forceinline__ void empty_states(const gdr::SeqArgs &s, int64_t grou
     }
 }
 
+// the forms with pairs of channels that are reached (pairs_fit)
+template <typename T, bool GATED> constexpr bool kPairs = sizeof(T) == 2 || !GATED;
+
 // the near polynomial does for every channel of the wave
 template <int V> __device__ __forceinline__ bool all_near(const float *neg_rate)
 {
@@ -255,29 +236,5 @@ __device__ __forceinline__ int total_tokens(const gdr::SeqArgs &s)
 {
     return s.cu_seqlens ? gdr::seq_edge(s, s.n_seqs) : s.n_tokens;
 }
-
-// workgroups that look for empty sequences
-inline int64_t empty_groups(const Args &a, bool wanted)
-{
-    return wanted && (a.cu_seqlens || !a.n_tokens) ? ((int64_t)a.n_seqs + WAVE - 1) / WAVE : 0;
-}
-
-// Pairs of channels a lane where every row of every tensor starts on a pair (D
-// even, addresses to two elements), single channels else; and single ones for
-// the gates of fp32 inputs, whose pairs would not fit the registers beside a
-// second workgroup (and fill whole lines of memory without them).
-template <typename T, bool GATED> constexpr bool kPairs = sizeof(T) == 2 || !GATED;
-inline bool pairs_fit(const Args &a)
-{
-    const size_t es = a.bf16 ? 2 : 4;
-    uintptr_t in = 0, st = 0;
-    for (const void *p : {a.x, a.r, a.i, (const void *)a.h, a.dh, (const void *)a.dx, (const void *)a.dr, (const void *)a.di})
-        in |= reinterpret_cast<uintptr_t>(p);
-    for (const float *p : {a.g, a.rate, a.h0, (const float *)a.h_T, (const float *)a.kept, a.dh_T, (const float *)a.dg,
-                           (const float *)a.drate, (const float *)a.dh0})
-        st |= reinterpret_cast<uintptr_t>(p);
-    return (a.bf16 || !a.gated) && a.D % 2 == 0 && in % (2 * es) == 0 && st % 8 == 0;
-}
-inline int blocks_of(int32_t D, int V) { return (D + WAVE * V - 1) / (WAVE * V); }
 
 }  // namespace glr
