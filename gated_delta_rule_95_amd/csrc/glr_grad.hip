@@ -37,11 +37,16 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
         return;
     }
     const int order = idx / chain.blocks, tile = chain.tiles - 1 - order, t0 = tile * C;
-    if (t0 >= total) return;
-    const int count = total - t0 < C ? total - t0 : C;
     const int c = (idx - order * chain.blocks) * WAVE * V + lane * V;
     const bool active = c < D;
     const int cc = active ? c : 0;
+    uint64_t *const p = chain.words + (int64_t)tile * D + cc;
+    const bool more = tile > 0;
+    if (t0 >= total) {
+        if (more) put_nothing<V>(p, active);
+        return;
+    }
+    const int count = total - t0 < C ? total - t0 : C;
     const int tw = t0 + w * K, mine = count - w * K < 0 ? 0 : count - w * K < K ? count - w * K : K;
 
     const unsigned ct = active ? c * (unsigned)sizeof(T) : kNowhere, cf = active ? c * 4u : kNowhere;
@@ -171,9 +176,7 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
 
     // the tile's map of the cotangent: wave 0 stores it for the tiles before
     // this one as soon as it is there
-    const bool more = chain.ticket && tile > 0;
     const bool alone = t0 + C >= total || s_last[C - 1] >= 0;
-    uint64_t *const p = chain.words + (int64_t)tile * D + cc;
     Map t[V];
     if (w == 0) {
 #pragma unroll
@@ -211,7 +214,7 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
     if (w == 0) {
         float in[V] = {};
         if (!alone) {
-            look_back<8 / V, V>(p + D, D, (total - 1) / C - tile, active, in);
+            look_back<8 / V, V>(p + D, D, chain.tiles - 1 - tile, active, in);
             if (more && active)
 #pragma unroll
                 for (int j = 0; j < V; ++j) put(p + j, Map{kForget, t[j](in[j])});

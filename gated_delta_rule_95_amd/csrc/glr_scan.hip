@@ -36,11 +36,16 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
         return;
     }
     const int tile = idx / chain.blocks, t0 = tile * C;
-    if (t0 >= total) return;
-    const int count = total - t0 < C ? total - t0 : C;
     const int c = (idx - tile * chain.blocks) * WAVE * V + lane * V;
     const bool active = c < D;
     const int cc = active ? c : 0;
+    uint64_t *const p = chain.words + (int64_t)tile * D + cc;
+    const bool more = tile + 1 < chain.tiles;       // a tile behind this one
+    if (t0 >= total) {
+        if (more) put_nothing<V>(p, active);
+        return;
+    }
+    const int count = total - t0 < C ? total - t0 : C;
     const int tw = t0 + w * K, mine = count - w * K < 0 ? 0 : count - w * K < K ? count - w * K : K;
 
     const unsigned ct = active ? c * (unsigned)sizeof(T) : kNowhere, cf = active ? c * 4u : kNowhere;
@@ -125,9 +130,7 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
         for (int i = 1; i < NW; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) m[j] = after(s_map[i][lane * V + j], m[j]);
-        const bool more = chain.ticket && t0 + C < total;       // a tile behind this one
         const bool alone = tile == 0 || s_first[0] >= 0;        // nothing comes in
-        uint64_t *p = chain.words + (int64_t)tile * D + cc;
         float in[V];
         if (alone) {
 #pragma unroll

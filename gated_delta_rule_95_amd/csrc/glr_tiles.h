@@ -131,12 +131,16 @@ hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s);
 // That is what each of these tiles does, or did, to get at the map that
 // forgets which it stores in the end, so the result does not depend on how far
 // they have come, to the last bit.
+// The wait is bounded all the same, for a workspace that something else writes
+// while the call runs: after kPatience looks (a second or more; the longest
+// wait of a sound call is some 100 us) the state becomes NaN.
+constexpr int kPatience = 1 << 20;
 template <int W, int V>
 __device__ __forceinline__ void look_back(const uint64_t *p, int64_t step, int n, bool active, float *in)
 {
     uint64_t w[W][V];
-    int from;
-    for (;;) {
+    int from = W;
+    for (int looks = 0; looks < kPatience; ++looks) {
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
@@ -164,6 +168,9 @@ __device__ __forceinline__ void look_back(const uint64_t *p, int64_t step, int n
             const Map m = map_of(w[i][j]);
             in[j] = i > from ? 0.f : i == from ? m.B : m(in[j]);
         }
+    if (from == W)
+#pragma unroll
+        for (int j = 0; j < V; ++j) in[j] = __builtin_nanf("");
 }
 
 // Borders of sequences inside tokens [t0, t0 + C): first[k] = the sequence
@@ -229,6 +236,16 @@ template <int V> __device__ __forceinline__ bool all_near(const float *neg_rate)
 #pragma unroll
     for (int j = 0; j < V; ++j) near = near && neg_rate[j] >= -kNear;
     return __all(near);
+}
+
+// What a tile behind the last sequence stores for the tiles that come to it:
+// every tile but the chain's last stores a map whatever the table of sequences
+// says, so no wait hangs on what the table says to whom.
+template <int V> __device__ __forceinline__ void put_nothing(uint64_t *p, bool active)
+{
+    if (threadIdx.x >= WAVE || !active) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) put(p + j, Map{kForget, 0.f});
 }
 
 // tokens that sequences have: [0, total)
