@@ -1,7 +1,7 @@
 // Gated linear recurrence, backward.
 //
-// The forward's tiles the other way round: 64 tokens by 64 V channels, each of
-// eight waves eight tokens in registers.  Two maps come out of a wave: of the
+// The forward's tiles the other way round: 64 tokens (gated, with pairs of
+// channels: 32) by 64 V channels, eight tokens a wave in registers.  Two maps come out of a wave: of the
 // state, forwards, which starts from the state that the forward kept before
 // the tile, and of the cotangent M_t = a_t L_t, L_t = dh_t + M_{t+1},
 // backwards, which is chained from tile to tile as the forward's state is.
@@ -9,6 +9,12 @@
 // for L_t and the gradients.  Inputs are read once and gradients written
 // once; the rate's gradient, a sum over all tokens, goes through one row a
 // tile, summed up in order by a second launch.
+//
+// Plain, bf16, 20011 tokens of 4096 channels: 1.15 GB in 210 us, 5.4 TB/s.
+// Gated, the same size: 1.15 GB in 287 us; a token and channel is 67 vector
+// operations (half the time) and eight numbers, which with two channels a lane
+// take 147 registers once two of them are laid aside in the LDS: three
+// workgroups of four waves a compute unit, whose phases overlap in part.
 #include "glr_tiles.h"
 
 namespace glr {
