@@ -173,10 +173,29 @@ __device__ __forceinline__ void look_back(const uint64_t *p, int64_t step, int n
         for (int j = 0; j < V; ++j) in[j] = __builtin_nanf("");
 }
 
+// The first sequence from `lo` on that ends behind token t (n_seqs where none
+// does), 64 table entries at a time.  One wave; uniform.
+__device__ __forceinline__ int ends_behind(const gdr::SeqArgs &s, int lo, int t, int lane)
+{
+    int hi = s.n_seqs;
+    while (lo < hi) {
+        const int step = (hi - lo + WAVE - 1) / WAVE;
+        const int64_t n = lo + (int64_t)lane * step;
+        const int ended = __popcll(__ballot(n < hi && gdr::seq_edge(s, (int)(n < hi ? n : lo) + 1) <= t));
+        const int64_t next = lo + (int64_t)ended * step;
+        if (ended) lo += (ended - 1) * step + 1;
+        hi = next < hi ? (int)next : hi;
+    }
+    return lo;
+}
+
 // Borders of sequences inside tokens [t0, t0 + C): first[k] = the sequence
 // whose first token is t0 + k, last[k] = the one whose last it is (entries
 // that are neither keep the -1 that the caller put there).  One wave; a table
 // that breaks its contract gives any sequences, but only such as there are.
+// Empty sequences in a row are looked over 64 at once, and from the first 64
+// that end in one on by a search, so that a table padded with any number of
+// them costs a tile no more than its tokens' worth of searches.
 __device__ __forceinline__ void mark_borders(const gdr::SeqArgs &s, int t0, int C, int lane, int *first, int *last)
 {
     if (!s.cu_seqlens) {
@@ -188,28 +207,21 @@ __device__ __forceinline__ void mark_borders(const gdr::SeqArgs &s, int t0, int 
         }
         return;
     }
-    // the count of sequences that end at or before t0, 64 at a time
-    int lo = 0, hi = s.n_seqs;
-    while (lo < hi) {
-        const int step = (hi - lo + WAVE - 1) / WAVE;
-        const int64_t n = lo + (int64_t)lane * step;
-        const int ended = __popcll(__ballot(n < hi && gdr::seq_edge(s, (int)(n < hi ? n : lo) + 1) <= t0));
-        const int64_t next = lo + (int64_t)ended * step;
-        if (ended) lo += (ended - 1) * step + 1;
-        hi = next < hi ? (int)next : hi;
-    }
-    for (int64_t base = lo; base < s.n_seqs; base += WAVE) {
+    for (int64_t base = ends_behind(s, 0, t0, lane); base < s.n_seqs;) {
         const int64_t n = base + lane;
-        int b = t0 + C;
+        int b = t0 + C, e = b;
         if (n < s.n_seqs) {
             b = gdr::seq_edge(s, (int)n);
-            const int e = gdr::seq_edge(s, (int)n + 1);
+            e = gdr::seq_edge(s, (int)n + 1);
             if (e > b) {
                 if (b >= t0 && b - t0 < C) first[b - t0] = (int)n;
                 if (e - 1 >= t0 && e - 1 - t0 < C) last[e - 1 - t0] = (int)n;
             }
         }
         if (__any(b - t0 >= C)) break;
+        base += WAVE;
+        const int at = __builtin_amdgcn_readlane(e, WAVE - 1);
+        if (at == __builtin_amdgcn_readlane(b, WAVE - 1)) base = ends_behind(s, (int)base, at, lane);
     }
 }
 

@@ -15,12 +15,9 @@ def edge(cu, n, tokens):
     return min(max(cu[n], 0), tokens)
 
 
-def borders(cu, tokens, t0, C):
-    """mark_borders, lane by lane; asserts that every index it forms is inside
-    the table and the tile."""
+def ends_behind(cu, tokens, lo, t, reads):
     n_seqs = len(cu) - 1
-    first, last, reads = {}, {}, 0
-    lo, hi = 0, n_seqs
+    hi, rounds = n_seqs, 0
     while lo < hi:
         step = -(-(hi - lo) // WAVE)
         ended = 0
@@ -28,18 +25,29 @@ def borders(cu, tokens, t0, C):
             n = lo + lane * step
             at = (n if n < hi else lo) + 1
             assert 0 <= at <= n_seqs
-            ended += n < hi and edge(cu, at, tokens) <= t0
+            ended += n < hi and edge(cu, at, tokens) <= t
         nxt = lo + ended * step
         if ended:
             lo += (ended - 1) * step + 1
         hi = min(nxt, hi)
-        reads += 1
-        assert reads < 8 and 0 <= lo <= n_seqs
-    base = lo
+        rounds += 1
+        assert rounds < 8 and 0 <= lo <= n_seqs
+    reads.append(rounds)
+    return lo
+
+
+def borders(cu, tokens, t0, C, reads=None):
+    """mark_borders, lane by lane; asserts that every index it forms is inside
+    the table and the tile.  reads gets the rounds of loads that follow each
+    other."""
+    n_seqs = len(cu) - 1
+    first, last, reads = {}, {}, [] if reads is None else reads
+    base = ends_behind(cu, tokens, 0, t0, reads)
     while base < n_seqs:
+        reads.append(1)
         stop = False
         for n in range(base, base + WAVE):
-            b = t0 + C
+            b = e = t0 + C
             if n < n_seqs:
                 b, e = edge(cu, n, tokens), edge(cu, n + 1, tokens)
                 if e > b:
@@ -51,6 +59,9 @@ def borders(cu, tokens, t0, C):
         if stop:
             break
         base += WAVE
+        if e == b:
+            lo, base = base, ends_behind(cu, tokens, base, e, reads)
+            assert base >= lo
     return first, last
 
 
@@ -84,6 +95,23 @@ def test_borders_of_any_table(valid, C):
             if valid:
                 assert first == {t - t0: n for t, n in want_first.items() if t0 <= t < t0 + C}
                 assert last == {t - t0: n for t, n in want_last.items() if t0 <= t < t0 + C}
+
+
+@pytest.mark.parametrize("C", [32, 128])
+def test_empty_sequences_cost_no_walk(C):
+    """Runs of empty sequences inside a tile and behind the last token, far more
+    than a wave looks at one after another."""
+    run = 70000
+    for cu in ([0] * run + [5] + [40] * run + [200] * run, [0, 7] + [7 + C] * run, [0] * run + [1], [0, 10, 10, 11] + [64] * run):
+        tokens = cu[-1]
+        for t0 in range(0, tokens, C):
+            reads = []
+            first, last = borders(cu, tokens, t0, C, reads)
+            starts = {a - t0: n for n, (a, b) in enumerate(zip(cu, cu[1:])) if b > a and t0 <= a < t0 + C}
+            ends = {b - 1 - t0: n for n, (a, b) in enumerate(zip(cu, cu[1:])) if b > a and t0 < b <= t0 + C}
+            assert first == starts and last == ends
+            # a search (3 rounds here) and one look for each token at which sequences end, and the first
+            assert sum(reads) <= 4 * (len(ends) + 2)
 
 
 def test_look_back_does_not_depend_on_progress():

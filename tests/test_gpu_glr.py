@@ -88,6 +88,14 @@ def test_forward_and_gradients(lens, D, dtype, gated):
 
 
 @pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+def test_runs_of_empty_sequences(gated):
+    """More of them at one token, and behind the last, than a wave looks at one
+    after another."""
+    run = [0] * 9000
+    compare(make(24, run + [5] + run + [35, 0, 160] + run, 3, F32, gated))
+
+
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
 @pytest.mark.parametrize("decays", ["slow", "fast"])
 @pytest.mark.parametrize("states", [True, False])
 def test_decays_and_states(states, decays, gated):
@@ -384,6 +392,61 @@ def test_decode(N, D, dtype, gated):
     assert f(*ins(b), pool2, h=out) is out
     h2, h2_T = fwd({**b, "h0": before[:N].contiguous()})
     assert torch.equal(pool2[:N], h2_T) and torch.equal(out, h2) and torch.equal(pool2[N:], before[N:])
+
+
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+def test_slots_named_twice_touch_nothing_else(gated):
+    """The state and rows of such a slot are undefined, everything else is as without them."""
+    b = make(26, [6], 260, BF, gated)
+    f = lib().glr_decode_step_gated if gated else lib().glr_decode_step
+    S = torch.randn(9, 260, device="cuda")
+    T, slots = S.clone(), torch.tensor([3, 7, 3, 1, -1, 8], dtype=torch.int32, device="cuda")
+    h = f(*ins(b), S, slots)
+    slots[2] = 20
+    want = f(*ins(b), T, slots)
+    torch.cuda.synchronize()
+    for k in range(9):
+        assert k == 3 or torch.equal(S[k], T[k])
+    for n in (1, 3, 4, 5):
+        assert torch.equal(h[n], want[n])
+
+
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+def test_one_workspace_for_calls_in_order(gated):
+    """A workspace given by the caller, dirty from a larger call, for forward and
+    gradients in turn, eagerly and in two graphs that share it."""
+    b, c = make(27, [900, 500], 130, BF, gated), make(28, [3, 700, 0, 150], 130, BF, gated)
+    m = lib()
+    need = max(f(1400, 130) for f in (m.glr_fwd_workspace_bytes, m.glr_bwd_workspace_bytes))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    run = lambda x, w: fwd(x, keep=True, workspace=w) + bwd(x, workspace=w)                # noqa: E731
+    want = [run(b, None), run(c, None)]
+    for k in (0, 1, 0):
+        for x, y in zip(run((b, c)[k], ws), want[k]):
+            assert torch.equal(x, y)
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g, x in zip(graphs, (b, c)):
+        with torch.cuda.graph(g):
+            outs.append(run(x, ws))
+    for k in (0, 1, 1, 0, 1):
+        for o in outs[k]:
+            o.fill_(FILL)
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        for x, y in zip(outs[k], want[k]):
+            assert torch.equal(x, y)
+        run((c, b)[k], ws)                                                                  # eager work between
+
+
+@pytest.mark.parametrize("dtype,gated,D", [(BF, True, 4096), (F32, True, 200)])
+def test_near_and_far_rates_side_by_side(dtype, gated, D):
+    """Rates on both sides of the near form's end, in one wave and in waves of their own."""
+    b = make(29, [130, 2500 if D < 1000 else 1030], D, dtype, gated)
+    b["rate"] = torch.linspace(0.0, 1.4, D, device="cuda")
+    compare(b)
+    b["rate"] = b["rate"].view(2, -1).t().reshape(-1).contiguous()
+    compare(b)
 
 
 def test_decode_from_an_empty_pool():
