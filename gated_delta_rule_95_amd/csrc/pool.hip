@@ -43,6 +43,9 @@ __device__ __forceinline__ bool valid(const uint8_t *used, int n_slots, const in
 // dst first holds the free slots in order (entry k the k-th lowest, k < n);
 // rows, from the last to the first, then replace them by their own: row i
 // has rank <= i, so what rows before it still want is not yet replaced.
+// (What comes back from memory here, in the plan and at the copies is held
+// against the bounds again: a list or workspace that another call writes
+// meanwhile, against the contract, must not move an address out of its array.)
 __global__ __launch_bounds__(PT) void pool_take_kernel(uint8_t *used, int n_slots, const int32_t *src, int n,
                                                        int32_t *dst)
 {
@@ -68,13 +71,15 @@ __global__ __launch_bounds__(PT) void pool_take_kernel(uint8_t *used, int n_slot
         int k = rank_of(v, s, total);
         before -= total;
         k += before;
-        const int to = v && k < nfree ? dst[k] : -1;
+        const int to = v && k >= 0 && k < nfree ? dst[k] : -1;
         __syncthreads();
         if (i < n) dst[i] = to;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += PT)
-        if (dst[i] >= 0) used[dst[i]] = 1;
+    for (int i = threadIdx.x; i < n; i += PT) {
+        const int j = dst[i];
+        if (j >= 0 && j < n_slots) used[j] = 1;
+    }
 }
 
 __global__ __launch_bounds__(CT) void pool_free_kernel(uint8_t *used, int n_slots, const int32_t *slots, int n)
@@ -103,12 +108,17 @@ __global__ __launch_bounds__(PT) void pool_plan_kernel(uint8_t *used, int n_slot
         holes += total;
         const int km = movers + rank_of(mover, s, total);
         movers += total;
-        if (hole) m.dst[kh] = j;
-        if (mover) m.src[km] = j;
+        if (hole && kh < n_slots / 2) m.dst[kh] = j;
+        if (mover && km < n_slots / 2) m.src[km] = j;
         if (j < n_slots) remap[j] = u ? j : -1;
     }
+    // as many holes as movers, of n_slots in all
+    movers = movers < n_slots / 2 ? movers : n_slots / 2;
     __syncthreads();
-    for (int k = threadIdx.x; k < movers; k += PT) remap[m.src[k]] = m.dst[k];
+    for (int k = threadIdx.x; k < movers; k += PT) {
+        const int j = m.src[k];
+        if (j >= 0 && j < n_slots) remap[j] = m.dst[k];
+    }
     for (int j = threadIdx.x; j < n_slots; j += PT) used[j] = j < live;
     if (threadIdx.x == 0) *m.count = movers;
     __syncthreads();
@@ -159,7 +169,8 @@ __global__ __launch_bounds__(CT) void pool_copy_kernel(CopyArgs a)
     char *to = a.pool[blockIdx.y].to;
     const size_t row = a.pool[blockIdx.y].row;
     const int64_t pieces = (row + kPiece - 1) / kPiece;
-    const int n = a.pairs.count ? *a.pairs.count : a.pairs.n;
+    int n = a.pairs.n;
+    if (a.pairs.count) n = *a.pairs.count < n ? *a.pairs.count : n;
     const size_t odd = reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to) | row;
     for (int64_t unit = blockIdx.x; unit < n * pieces; unit += gridDim.x) {
         const int64_t i = unit / pieces, at = (unit - i * pieces) * kPiece;

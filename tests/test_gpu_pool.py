@@ -166,6 +166,44 @@ def test_large_counts(n_slots, n):
     same(pools, want)
 
 
+def test_destinations_named_twice_touch_nothing_else():
+    """Such a slot may hold either row's bytes or some of both."""
+    m = lib()
+    pools, _, _, _ = make(11, 30, ROWS["odd"], 0)
+    want = raw(pools)
+    m.pool_copy(pools, i32([1, 2, 3, 4]), pools, i32([20, 20, 21, 21]))
+    torch.cuda.synchronize()
+    for p, w in zip(raw(pools), want):
+        for at, a, b in ((20, 1, 2), (21, 3, 4)):
+            assert ((p[at] == w[a]) | (p[at] == w[b])).all()
+        rest = np.delete(np.arange(30), [20, 21])
+        assert np.array_equal(p[rest], w[rest])
+
+
+def test_two_streams_with_their_own_pools():
+    m = lib()
+    runs = [make(seed, 300, ROWS["odd"], 0.5) for seed in (12, 13)]
+    streams = [torch.cuda.Stream() for _ in runs]
+    wants, ws = [raw(p) for p, *_ in runs], [torch.empty(m.pool_compact_workspace_bytes(300), dtype=torch.uint8, device="cuda")
+                                             for _ in runs]
+    torch.cuda.synchronize()
+    for k in range(6):
+        srcs = [i32(np.flatnonzero(u)[k:k + 9]) for _, _, u, _ in runs]
+        torch.cuda.synchronize()
+        got = []
+        for (pools, used, _, _), src, side, w in zip(runs, srcs, streams, ws):
+            with torch.cuda.stream(side):
+                dst = m.pool_fork(pools, used, src)
+                m.pool_free(used, src)
+                got.append((dst, m.pool_compact(pools, used, workspace=w)))
+        torch.cuda.synchronize()
+        for (pools, used, u, _), want, src, (dst, remap) in zip(runs, wants, srcs, got):
+            assert dst.tolist() == forked(want, u, src.tolist())
+            u[src.tolist()] = False
+            assert remap.tolist() == compacted(want, u, [])[0] and used.tolist() == u.tolist()
+            same(pools, want)
+
+
 def test_nothing_to_do():
     m = lib()
     pools, used, u, _ = make(5, 9, ROWS["one"], 0.5)
