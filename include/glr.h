@@ -37,9 +37,9 @@
  * where no product of successive factors overflows.  NaN or an infinity in
  * an input of a token (but g = -inf) may reach any output of its own channel
  * and sequence, and the gradient of rate_c, and none of another's.  Where a
- * gate is so far closed that a is 1 in fp32 exactly, u is 0 and the part of
- * the gradients that passes through sqrt(1 - a^2), whose slope is infinite
- * there, is taken as 0.
+ * gate is so far closed that 1 - a^2 is below fp32's smallest normal number
+ * (1.2e-38), u is 0 and the part of the gradients that passes through
+ * sqrt(1 - a^2), whose slope is infinite at 0, is taken as 0.
  *
  * Sizes: 1 <= D < 2^24; 0 <= n_seqs < 2^27; 0 <= n_tokens <= 2^31 - 256; n_tokens, n_seqs
  * and (decode) N times D below 2^40, and the number of (64 tokens, 64

@@ -25,9 +25,10 @@ errors of their factors.  A sum over n tokens in fp32 by parts adds
 tokens at most in some order of pairs, parts are summed in 64 bits).
 Numbers below the smallest normal one (1.2e-38) count as it or as zero, so a
 product of factors of which one is that small is off by TINY = 2e-38 times
-the others, whatever its own size.  A decay gate below -87 counts as -87,
-where s(r) is 1.6e-38: m, and with it s(r) / m times the rate, is then off by
-at most sqrt(2 * 1.6e-38 rate) < 4e-19 sqrt(rate) =: CLOSED.
+the others, whatever its own size.  A decay gate below -87, where s(r) is
+1.6e-38 or less, may count as -87 or as closed (s = 0): m, and with it s(r) / m
+times the rate, is then off by at most sqrt(2 * 1.6e-38 rate) < 4e-19
+sqrt(rate) =: CLOSED.
 All bounds are doubled for what is second order and for sums that round at
 an intermediate size.  A value stored in bf16 is off by its half step
 besides.
