@@ -28,22 +28,24 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
     constexpr int NW = grad_waves(GATED, V), C = grad_tile(GATED, V), NT = NW * WAVE;
     typedef Row<T, V> R;
     typedef Row<float, V> RF;
-    __shared__ int s_idx, s_first[C], s_last[C];
+    __shared__ int s_tile, s_first[C], s_last[C];
     __shared__ Map s_up[NW - 1][WAVE * V], s_down[NW][WAVE * V];
     __shared__ float s_in[WAVE * V], s_late[GATED ? K : 1][2][V][NT];
     const int tid = threadIdx.x, lane = tid % WAVE, w = __builtin_amdgcn_readfirstlane(tid / WAVE), D = a.D;
     const gdr::SeqArgs sa = seq_args(a);
     const int total = total_tokens(sa);
-    if (tid == 0) s_idx = take(chain);
-    if (tid < C) s_first[tid] = s_last[tid] = -1;
-    __syncthreads();
-    const int idx = __builtin_amdgcn_readfirstlane(s_idx);
+    const int idx = blockIdx.x;
     if (idx >= chain.tiles * chain.blocks) {
         empty_states(sa, idx - chain.tiles * chain.blocks, D, a.dh_T, a.dh0, NT);
         return;
     }
-    const int order = idx / chain.blocks, tile = chain.tiles - 1 - order, t0 = tile * C;
-    const int c = (idx - order * chain.blocks) * WAVE * V + lane * V;
+    const int block = block_of(chain, idx);
+    if (tid == 0) s_tile = take(chain, block);
+    const Edges few = few_edges(sa, lane);
+    if (tid < C) s_first[tid] = s_last[tid] = -1;
+    __syncthreads();
+    const int taken = __builtin_amdgcn_readfirstlane(s_tile);
+    const int tile = chain.tiles - 1 - taken, t0 = tile * C, c = block * WAVE * V + lane * V;
     const bool active = c < D;
     const int cc = active ? c : 0;
     uint64_t *const p = chain.words + (int64_t)tile * D + cc;
@@ -79,7 +81,7 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
         for (int j = 0; j < V; ++j) nr[j] = -RF::get(rate, j);
     }
     const typename RF::raw left = ld<V>(a.kept + (int64_t)(t0 / kKept) * D + cc);
-    if (w == 0) mark_borders(sa, t0, C, lane, s_first, s_last);
+    if (w == 0) mark_borders(sa, few, t0, C, lane, s_first, s_last);
     __syncthreads();
     const uint64_t starts = __ballot(lane < K && s_first[w * K + lane % K] >= 0);
     const uint64_t ends = __ballot(lane < K && s_last[w * K + lane % K] >= 0);

@@ -25,31 +25,35 @@ inline int64_t tiles_of(int64_t n_tokens, int tile) { return (n_tokens + tile - 
 inline int blocks_of(int32_t D, int V) { return (D + kLanes * V - 1) / (kLanes * V); }
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Workspace of a chain: a ticket, then one word for each tile and channel.
-// Workgroups take tiles in order, by the ticket, and store a map before they
-// wait, so a tile waits only for tiles that workgroups which run already have
-// taken, and the lowest of those waits for nothing: every wait ends.
+// Workspace of a chain: a ticket for each block of channels, then one word for
+// each tile and channel.  A block's workgroups take its tiles in order, by its
+// ticket, and store a map before they wait, so a tile waits only for tiles that
+// workgroups which run already have taken, and the lowest of those waits for
+// nothing: every wait ends.  Tickets lie 256 bytes apart (in one
+// line they are as slow as one ticket for all: 1517 tokens of 1001 channels in
+// fp32, the gradients 14.8 us, apart 12.6; 20011 of 4096, gated, 286 and 277).
 // (Workgroups that stay and ask for their next tile ahead were slower, 20011
 // tokens of 4096 channels 155 -> 223 us and their gradients 297 -> 353: the
 // tile they hold waits for the one they are at.  Without asking ahead the
 // gradients took as long as now, and the scan, short of registers, 195.)
 struct Chain {
-    uint32_t *ticket;                    // nullptr: one tile, which needs no chain
+    uint32_t *tickets;                   // nullptr: one tile, which needs no chain
     uint64_t *words;
     int tiles, blocks;                   // of tokens, of channels
-    int items;                           // what is handed out: tiles, then groups of sequences
+    int items;                           // workgroups: of the tiles, then of groups of sequences
 };
-constexpr size_t kChainHead = 256;
+constexpr size_t kTicket = 256;
+inline size_t tickets_bytes(int32_t D) { return blocks_of(D, 1) * kTicket; }
 inline size_t chain_bytes(int64_t tiles, int32_t D)
 {
-    return tiles > 1 ? kChainHead + round256((size_t)tiles * D * 8) : 0;
+    return tiles > 1 ? tickets_bytes(D) + round256((size_t)tiles * D * 8) : 0;
 }
-inline Chain make_chain(void *ws, int tiles, int blocks, int64_t groups)
+inline Chain make_chain(void *ws, int32_t D, int tiles, int blocks, int64_t groups)
 {
     const int items = (int)((int64_t)tiles * blocks + groups);
     if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks, items};
     return Chain{static_cast<uint32_t *>(ws),
-                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + kChainHead), tiles, blocks, items};
+                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + tickets_bytes(D)), tiles, blocks, items};
 }
 
 // workgroups that look for empty sequences, 64 each
@@ -87,7 +91,7 @@ inline Plan plan_scan(const Args &a)
     // 1024 tokens 17.4 and 18.6)
     const int64_t tiles = tiles_of(a.n_tokens, kScanTile);
     const int V = pairs_fit(a) && tiles * blocks_of(a.D, 2) >= 256 ? 2 : 1;
-    return Plan{V, make_chain(a.ws, (int)tiles, blocks_of(a.D, V), empty_groups(a, a.h_T))};
+    return Plan{V, make_chain(a.ws, a.D, (int)tiles, blocks_of(a.D, V), empty_groups(a, a.h_T))};
 }
 
 // workspace of the backward: kept states (where they are formed again), the
@@ -120,7 +124,7 @@ inline Plan plan_grad(const Args &a, void *chain)
     const int least = a.gated ? 4096 : 0;
     const int V = pairs_fit(a) && tiles_of(a.n_tokens, grad_tile(a.gated, 2)) * blocks_of(a.D, 2) >= least ? 2 : 1;
     const int tiles = (int)tiles_of(a.n_tokens, grad_tile(a.gated, V));
-    return Plan{V, make_chain(chain, tiles, blocks_of(a.D, V), empty_groups(a, a.dh0))};
+    return Plan{V, make_chain(chain, a.D, tiles, blocks_of(a.D, V), empty_groups(a, a.dh0))};
 }
 
 }  // namespace glr

@@ -29,22 +29,24 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
 {
     typedef Row<T, V> R;
     typedef Row<float, V> RF;
-    __shared__ int s_idx, s_first[C], s_last[C];
+    __shared__ int s_tile, s_first[C], s_last[C];
     __shared__ Map s_map[NW][WAVE * V];
     __shared__ float s_in[WAVE * V];
     const int tid = threadIdx.x, lane = tid % WAVE, w = __builtin_amdgcn_readfirstlane(tid / WAVE), D = a.D;
     const gdr::SeqArgs sa = seq_args(a);
     const int total = total_tokens(sa);
-    if (tid == 0) s_idx = take(chain);
-    if (tid < C) s_first[tid] = s_last[tid] = -1;
-    __syncthreads();
-    const int idx = __builtin_amdgcn_readfirstlane(s_idx);
+    const int idx = blockIdx.x;
     if (idx >= chain.tiles * chain.blocks) {
         empty_states(sa, idx - chain.tiles * chain.blocks, D, a.h0, a.h_T, NT);
         return;
     }
-    const int tile = idx / chain.blocks, t0 = tile * C;
-    const int c = (idx - tile * chain.blocks) * WAVE * V + lane * V;
+    const int block = block_of(chain, idx);
+    if (tid == 0) s_tile = take(chain, block);
+    const Edges few = few_edges(sa, lane);
+    if (tid < C) s_first[tid] = s_last[tid] = -1;
+    __syncthreads();
+    const int taken = __builtin_amdgcn_readfirstlane(s_tile);
+    const int tile = taken, t0 = tile * C, c = block * WAVE * V + lane * V;
     const bool active = c < D;
     const int cc = active ? c : 0;
     uint64_t *const p = chain.words + (int64_t)tile * D + cc;
@@ -77,7 +79,7 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
 #pragma unroll
         for (int j = 0; j < V; ++j) nr[j] = -RF::get(rate, j);
     }
-    if (w == 0) mark_borders(sa, t0, C, lane, s_first, s_last);
+    if (w == 0) mark_borders(sa, few, t0, C, lane, s_first, s_last);
     __syncthreads();
     const uint64_t starts = __ballot(lane < K && s_first[w * K + lane % K] >= 0);
     const uint64_t ends = __ballot(lane < K && s_last[w * K + lane % K] >= 0);
@@ -150,7 +152,7 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
             if (more && active)
 #pragma unroll
                 for (int j = 0; j < V; ++j) put(p + j, m[j]);
-            look_back<8, V>(p - D, -(int64_t)D, tile, active, in);
+            look_back<8 / V, V>(p - D, -(int64_t)D, tile, active, in);
             if (more && active)
 #pragma unroll
                 for (int j = 0; j < V; ++j) put(p + j, Map{kForget, m[j](in[j])});
@@ -191,12 +193,12 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
     }
 }
 
-__global__ __launch_bounds__(256) void glr_clear_kernel(Chain c, int64_t words)
+// tickets and words, 16 bytes at a time (chain_bytes leaves room for an even count)
+__global__ __launch_bounds__(256) void glr_clear_kernel(uint64_t *p, int64_t words)
 {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *c.ticket = 0;
-    typedef uint64_t u2 __attribute__((ext_vector_type(2)));        // (chain_bytes leaves room for an even count)
+    typedef uint64_t u2 __attribute__((ext_vector_type(2)));
     for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; 2 * i < words; i += (int64_t)gridDim.x * 256)
-        reinterpret_cast<u2 *>(c.words)[i] = u2{kEmpty, kEmpty};
+        reinterpret_cast<u2 *>(p)[i] = u2{kEmpty, kEmpty};
 }
 
 template <typename T, bool GATED>
@@ -215,9 +217,10 @@ void launch_v(const Args &a, const Chain &ch, int V, hipStream_t s)
 
 hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s)
 {
-    if (!c.ticket) return hipSuccess;
-    const int64_t words = (int64_t)c.tiles * D, blocks = (words + 511) / 512;
-    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, c, words);
+    if (!c.tickets) return hipSuccess;
+    uint64_t *const p = reinterpret_cast<uint64_t *>(c.tickets);
+    const int64_t words = c.words - p + (int64_t)c.tiles * D, blocks = (words + 511) / 512;
+    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, p, words);
     return hipGetLastError();
 }
 

@@ -103,11 +103,11 @@ static void check_chain(const glr::Plan &q, const char *ws, size_t bytes, int64_
     EXPECT((int64_t)c.tiles * tile >= N && ((int64_t)c.tiles - 1) * tile < (N ? N : 1));
     EXPECT((int64_t)c.blocks * 64 * q.V >= D && ((int64_t)c.blocks - 1) * 64 * q.V < D);
     EXPECT((uint64_t)c.items * threads < (uint64_t)1 << 32 && c.items >= (int64_t)c.tiles * c.blocks);
-    if (!c.ticket) {
+    if (!c.tickets) {
         EXPECT(c.tiles <= 1);
         return;
     }
-    EXPECT((char *)c.ticket >= ws && (char *)(c.ticket + 1) <= (char *)c.words);
+    EXPECT((char *)c.tickets >= ws && (char *)c.tickets + ((size_t)c.blocks - 1) * glr::kTicket + 4 <= (char *)c.words);
     // the clearing kernel writes words in pairs
     const size_t words = (size_t)c.tiles * D;
     EXPECT((char *)(c.words + (words + words % 2)) <= ws + bytes);
