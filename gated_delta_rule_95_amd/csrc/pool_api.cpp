@@ -104,11 +104,8 @@ POOL_API kda_status pool_alloc(const pool_rows *pools, int32_t n_pools, uint8_t 
     if ((s = check_bufs(bufs, 2)) != KDA_OK) return s;
     if ((s = check_apart(pools, n_pools, n_slots, "pools", bufs, 2)) != KDA_OK) return s;
     if (!n) return ok();
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = pool::launch_take(used, n_slots, nullptr, n, slots, st);
-    if (e == hipSuccess && n_pools && n_slots)
-        e = pool::launch_copy(nullptr, pools, n_pools, pool::Pairs{nullptr, slots, nullptr, n, 0, n_slots}, st);
-    return hip_status(e, "pool_alloc launch");
+    return hip_status(pool::launch_take(pools, n_pools, used, n_slots, nullptr, n, slots, static_cast<hipStream_t>(stream)),
+                      "pool_alloc launch");
 }
 
 POOL_API kda_status pool_fork(const pool_rows *pools, int32_t n_pools, uint8_t *used, int32_t n_slots,
@@ -124,11 +121,8 @@ POOL_API kda_status pool_fork(const pool_rows *pools, int32_t n_pools, uint8_t *
     if ((s = check_bufs(bufs, 3)) != KDA_OK) return s;
     if ((s = check_apart(pools, n_pools, n_slots, "pools", bufs, 3)) != KDA_OK) return s;
     if (!n) return ok();
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = pool::launch_take(used, n_slots, src, n, dst, st);
-    if (e == hipSuccess && n_pools && n_slots)
-        e = pool::launch_copy(pools, pools, n_pools, pool::Pairs{src, dst, nullptr, n, n_slots, n_slots}, st);
-    return hip_status(e, "pool_fork launch");
+    return hip_status(pool::launch_take(pools, n_pools, used, n_slots, src, n, dst, static_cast<hipStream_t>(stream)),
+                      "pool_fork launch");
 }
 
 POOL_API kda_status pool_free(uint8_t *used, int32_t n_slots, const int32_t *slots, int32_t n,

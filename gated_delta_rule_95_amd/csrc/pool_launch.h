@@ -20,9 +20,10 @@ struct Pairs {
 // rows to rows (from nullptr: zeros to rows; pairs.src is not read then)
 hipError_t launch_copy(const pool_rows *from, const pool_rows *to, int32_t n_pools, const Pairs &pairs,
                        hipStream_t s);
-// dst[i]: the free slot row i gets, or -1; src nullptr: every row wants one
-hipError_t launch_take(uint8_t *used, int32_t n_slots, const int32_t *src, int32_t n, int32_t *dst,
-                       hipStream_t s);
+// dst[i]: the free slot row i gets, or -1, with the rows of slot src[i]; src
+// nullptr: every row wants one, of zeros
+hipError_t launch_take(const pool_rows *pools, int32_t n_pools, uint8_t *used, int32_t n_slots,
+                       const int32_t *src, int32_t n, int32_t *dst, hipStream_t s);
 hipError_t launch_free(uint8_t *used, int32_t n_slots, const int32_t *slots, int32_t n, hipStream_t s);
 
 // the workspace of a compaction: how many slots move, from where, to where

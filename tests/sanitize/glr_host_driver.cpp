@@ -50,7 +50,15 @@ hipError_t launch_copy(const pool_rows *from, const pool_rows *to, int32_t n_poo
         if (!to[i].base || (from && from[i].row_bytes != to[i].row_bytes)) return hipErrorInvalidValue;
     return result;
 }
-hipError_t launch_take(uint8_t *, int32_t, const int32_t *, int32_t, int32_t *, hipStream_t) { ++taken; return result; }
+hipError_t launch_take(const pool_rows *pools, int32_t n_pools, uint8_t *, int32_t, const int32_t *src, int32_t, int32_t *,
+                       hipStream_t)
+{
+    ++taken;
+    zeros = !src;
+    for (int i = 0; i < n_pools; ++i)
+        if (!pools[i].base) return hipErrorInvalidValue;
+    return result;
+}
 hipError_t launch_free(uint8_t *, int32_t, const int32_t *, int32_t, hipStream_t) { ++freed; return result; }
 hipError_t launch_plan(uint8_t *, int32_t, int32_t *, int64_t, int32_t *, const Moves &, hipStream_t) { ++planned; return result; }
 }  // namespace pool

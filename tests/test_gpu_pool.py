@@ -118,6 +118,28 @@ def test_fork_free_compact_alloc_copy(n_slots, rows):
         same(pools, want)
 
 
+@pytest.mark.parametrize("rows,n", [([(F32, (1024,))], 64), ([(F32, (1024,))], 65), ([(F32, (1025,)), (I8, (4096,))], 21),
+                                    ([(F32, (1025,)), (I8, (4096,))], 22), ([(I8, (1,))] * 32, 2), ([(I8, (1,))] * 33, 1),
+                                    ([(F32, (65536,))], 1), ([(F32, (65537,))], 1), ([(BF, (2056,)), (I8, (8193,))], 12)])
+def test_sizes_at_which_the_copies_get_a_launch_of_their_own(rows, n):
+    m = lib()
+    pools, used, u, r = make(14, 150, rows, 0.4)
+    want = raw(pools)
+    src = r.choice(np.flatnonzero(u), n)
+    src[::5] = -1
+    assert m.pool_fork(pools, used, i32(src)).tolist() == forked(want, u, src.tolist())
+    same(pools, want)
+    m.pool_free(used, i32(np.flatnonzero(u)[:70]))
+    u[np.flatnonzero(u)[:70]] = False
+    free = np.flatnonzero(~u)[:n]
+    assert m.pool_alloc(pools, used, n).tolist() == free.tolist()
+    u[free] = True
+    for p in want:
+        p[free] = 0
+    assert used.tolist() == u.tolist()
+    same(pools, want)
+
+
 def test_copy_inside_a_pool():
     m = lib()
     pools, _, _, _ = make(3, 20, ROWS["odd"], 0)
