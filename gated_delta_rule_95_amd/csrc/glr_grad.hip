@@ -48,7 +48,7 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
     const int tile = chain.tiles - 1 - taken, t0 = tile * C, c = block * WAVE * V + lane * V;
     const bool active = c < D;
     const int cc = active ? c : 0;
-    uint64_t *const p = chain.words + (int64_t)tile * D + cc;
+    uint64_t *const p = chain.words + (int64_t)tile * chain.pitch + block * (WAVE * V) + lane;
     const bool more = tile > 0;
     if (t0 >= total) {
         if (more) put_nothing<V>(p, active);
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
             for (int j = 0; j < V; ++j) t[j] = after(s_down[i][lane * V + j], t[j]);
         if (more && active)
 #pragma unroll
-            for (int j = 0; j < V; ++j) put(p + j, alone ? Map{kForget, t[j].B} : t[j]);
+            for (int j = 0; j < V; ++j) put(p + j * kLanes, alone ? Map{kForget, t[j].B} : t[j]);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -222,10 +222,10 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
     if (w == 0) {
         float in[V] = {};
         if (!alone) {
-            look_back<8 / V, V>(p + D, D, chain.tiles - 1 - tile, active, in);
+            look_back<8 / V, V>(p + chain.pitch, chain.pitch, chain.tiles - 1 - tile, active, in);
             if (more && active)
 #pragma unroll
-                for (int j = 0; j < V; ++j) put(p + j, Map{kForget, t[j](in[j])});
+                for (int j = 0; j < V; ++j) put(p + j * kLanes, Map{kForget, t[j](in[j])});
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) s_in[lane * V + j] = in[j];
@@ -341,7 +341,7 @@ hipError_t launch_bwd(const Args &arg)
     }
     const Plan p = plan_grad(a, w.chain);
     if (p.chain.items) {
-        if ((e = clear_chain(p.chain, a.D, a.stream)) != hipSuccess) return e;
+        if ((e = clear_chain(p.chain, a.stream)) != hipSuccess) return e;
         if (a.bf16)
             a.gated ? launch_v<bf16, true>(a, p.chain, w.part, p.V, a.stream)
                     : launch_v<bf16, false>(a, p.chain, w.part, p.V, a.stream);

@@ -26,7 +26,8 @@ inline int blocks_of(int32_t D, int V) { return (D + kLanes * V - 1) / (kLanes *
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace of a chain: a ticket for each block of channels, then one word for
-// each tile and channel.  A block's workgroups take its tiles in order, by its
+// each tile and channel (a block's by the lanes' first channels, then their
+// second ones, so that a wave's words are whole lines).  A block's workgroups take its tiles in order, by its
 // ticket, and store a map before they wait, so a tile waits only for tiles that
 // workgroups which run already have taken, and the lowest of those waits for
 // nothing: every wait ends.  Tickets lie 256 bytes apart (in one
@@ -40,20 +41,22 @@ struct Chain {
     uint32_t *tickets;                   // nullptr: one tile, which needs no chain
     uint64_t *words;
     int tiles, blocks;                   // of tokens, of channels
+    int pitch;                           // words a tile
     int items;                           // workgroups: of the tiles, then of groups of sequences
 };
 constexpr size_t kTicket = 256;
 inline size_t tickets_bytes(int32_t D) { return blocks_of(D, 1) * kTicket; }
 inline size_t chain_bytes(int64_t tiles, int32_t D)
 {
-    return tiles > 1 ? tickets_bytes(D) + round256((size_t)tiles * D * 8) : 0;
+    return tiles > 1 ? tickets_bytes(D) + (size_t)tiles * blocks_of(D, 2) * (2 * kLanes * 8) : 0;
 }
-inline Chain make_chain(void *ws, int32_t D, int tiles, int blocks, int64_t groups)
+inline Chain make_chain(void *ws, int32_t D, int V, int tiles, int64_t groups)
 {
+    const int blocks = blocks_of(D, V), pitch = blocks * kLanes * V;
     const int items = (int)((int64_t)tiles * blocks + groups);
-    if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks, items};
+    if (tiles < 2) return Chain{nullptr, nullptr, tiles, blocks, pitch, items};
     return Chain{static_cast<uint32_t *>(ws),
-                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + tickets_bytes(D)), tiles, blocks, items};
+                 reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + tickets_bytes(D)), tiles, blocks, pitch, items};
 }
 
 // workgroups that look for empty sequences, 64 each
@@ -91,7 +94,7 @@ inline Plan plan_scan(const Args &a)
     // 1024 tokens 17.4 and 18.6)
     const int64_t tiles = tiles_of(a.n_tokens, kScanTile);
     const int V = pairs_fit(a) && tiles * blocks_of(a.D, 2) >= 256 ? 2 : 1;
-    return Plan{V, make_chain(a.ws, a.D, (int)tiles, blocks_of(a.D, V), empty_groups(a, a.h_T))};
+    return Plan{V, make_chain(a.ws, a.D, V, (int)tiles, empty_groups(a, a.h_T))};
 }
 
 // workspace of the backward: kept states (where they are formed again), the
@@ -124,7 +127,7 @@ inline Plan plan_grad(const Args &a, void *chain)
     const int least = a.gated ? 4096 : 0;
     const int V = pairs_fit(a) && tiles_of(a.n_tokens, grad_tile(a.gated, 2)) * blocks_of(a.D, 2) >= least ? 2 : 1;
     const int tiles = (int)tiles_of(a.n_tokens, grad_tile(a.gated, V));
-    return Plan{V, make_chain(chain, a.D, tiles, blocks_of(a.D, V), empty_groups(a, a.dh0))};
+    return Plan{V, make_chain(chain, a.D, V, tiles, empty_groups(a, a.dh0))};
 }
 
 }  // namespace glr

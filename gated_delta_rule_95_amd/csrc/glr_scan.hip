@@ -49,7 +49,7 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
     const int tile = taken, t0 = tile * C, c = block * WAVE * V + lane * V;
     const bool active = c < D;
     const int cc = active ? c : 0;
-    uint64_t *const p = chain.words + (int64_t)tile * D + cc;
+    uint64_t *const p = chain.words + (int64_t)tile * chain.pitch + block * (WAVE * V) + lane;
     const bool more = tile + 1 < chain.tiles;       // a tile behind this one
     if (t0 >= total) {
         if (more) put_nothing<V>(p, active);
@@ -146,16 +146,16 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 in[j] = 0.f;
-                if (more && active) put(p + j, Map{kForget, m[j].B});
+                if (more && active) put(p + j * kLanes, Map{kForget, m[j].B});
             }
         } else {
             if (more && active)
 #pragma unroll
-                for (int j = 0; j < V; ++j) put(p + j, m[j]);
-            look_back<8 / V, V>(p - D, -(int64_t)D, tile, active, in);
+                for (int j = 0; j < V; ++j) put(p + j * kLanes, m[j]);
+            look_back<8 / V, V>(p - chain.pitch, -(int64_t)chain.pitch, tile, active, in);
             if (more && active)
 #pragma unroll
-                for (int j = 0; j < V; ++j) put(p + j, Map{kForget, m[j](in[j])});
+                for (int j = 0; j < V; ++j) put(p + j * kLanes, Map{kForget, m[j](in[j])});
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) s_in[lane * V + j] = in[j];
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
     }
 }
 
-// tickets and words, 16 bytes at a time (chain_bytes leaves room for an even count)
+// tickets and words, 16 bytes at a time (both are whole lines)
 __global__ __launch_bounds__(256) void glr_clear_kernel(uint64_t *p, int64_t words)
 {
     typedef uint64_t u2 __attribute__((ext_vector_type(2)));
@@ -215,11 +215,11 @@ void launch_v(const Args &a, const Chain &ch, int V, hipStream_t s)
 
 }  // namespace
 
-hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s)
+hipError_t clear_chain(const Chain &c, hipStream_t s)
 {
     if (!c.tickets) return hipSuccess;
     uint64_t *const p = reinterpret_cast<uint64_t *>(c.tickets);
-    const int64_t words = c.words - p + (int64_t)c.tiles * D, blocks = (words + 511) / 512;
+    const int64_t words = c.words - p + (int64_t)c.tiles * c.pitch, blocks = (words + 511) / 512;
     hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, p, words);
     return hipGetLastError();
 }
@@ -228,7 +228,7 @@ hipError_t launch_fwd(const Args &a)
 {
     const Plan p = plan_scan(a);
     if (p.chain.items == 0) return hipSuccess;
-    const hipError_t e = clear_chain(p.chain, a.D, a.stream);
+    const hipError_t e = clear_chain(p.chain, a.stream);
     if (e != hipSuccess) return e;
     if (a.bf16) a.gated ? launch_v<bf16, true>(a, p.chain, p.V, a.stream) : launch_v<bf16, false>(a, p.chain, p.V, a.stream);
     else a.gated ? launch_v<float, true>(a, p.chain, p.V, a.stream) : launch_v<float, false>(a, p.chain, p.V, a.stream);

@@ -132,7 +132,7 @@ __device__ __forceinline__ int take(const Chain &c, int block)
     const unsigned n = atomicAdd(c.tickets + block * (kTicket / 4), 1u) + 1u, last = (unsigned)c.tiles - 1;
     return (int)(n < last ? n : last);
 }
-hipError_t clear_chain(const Chain &c, int32_t D, hipStream_t s);
+hipError_t clear_chain(const Chain &c, hipStream_t s);
 
 // The state (or cotangent) that comes into a tile.  Words of the `n` tiles
 // before it (the first of which forgets) lie `step` apart, from `p` on, the
@@ -156,7 +156,7 @@ __device__ __forceinline__ void look_back(const uint64_t *p, int64_t step, int n
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) w[i][j] = peek(p + step * (i < n ? i : n - 1) + j);
+            for (int j = 0; j < V; ++j) w[i][j] = peek(p + step * (i < n ? i : n - 1) + j * kLanes);
         from = W;
         bool there = true;
 #pragma unroll
@@ -292,7 +292,7 @@ template <int V> __device__ __forceinline__ void put_nothing(uint64_t *p, bool a
 {
     if (threadIdx.x >= WAVE || !active) return;
 #pragma unroll
-    for (int j = 0; j < V; ++j) put(p + j, Map{kForget, 0.f});
+    for (int j = 0; j < V; ++j) put(p + j * kLanes, Map{kForget, 0.f});
 }
 
 // tokens that sequences have: [0, total)

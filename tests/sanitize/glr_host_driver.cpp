@@ -116,9 +116,8 @@ static void check_chain(const glr::Plan &q, const char *ws, size_t bytes, int64_
         return;
     }
     EXPECT((char *)c.tickets >= ws && (char *)c.tickets + ((size_t)c.blocks - 1) * glr::kTicket + 4 <= (char *)c.words);
-    // the clearing kernel writes words in pairs
-    const size_t words = (size_t)c.tiles * D;
-    EXPECT((char *)(c.words + (words + words % 2)) <= ws + bytes);
+    EXPECT(c.pitch >= D && c.pitch == c.blocks * 64 * q.V);
+    EXPECT((char *)(c.words + (size_t)c.tiles * c.pitch) <= ws + bytes);
 }
 
 int main()
