@@ -1,20 +1,22 @@
 // Gated linear recurrence, backward.
 //
 // The forward's tiles the other way round: 64 tokens (gated, with pairs of
-// channels: 32) by 64 V channels, eight tokens a wave in registers.  Two maps come out of a wave: of the
-// state, forwards, which starts from the state that the forward kept before
-// the tile, and of the cotangent M_t = a_t L_t, L_t = dh_t + M_{t+1},
-// backwards, which is chained from tile to tile as the forward's state is.
-// Then every wave runs its tokens up once more for a_t h_{t-1} and down once
-// for L_t and the gradients.  Inputs are read once and gradients written
-// once; the rate's gradient, a sum over all tokens, goes through one row a
-// tile, summed up in order by a second launch.
+// channels: 32) by 64 V channels, eight tokens a wave in registers.  Two maps
+// come out of a wave: of the state, forwards, which starts from the state that
+// the forward kept before the tile, and of the cotangent M_t = a_t L_t, L_t =
+// dh_t + M_{t+1}, backwards, which is chained from tile to tile as the
+// forward's state is.  Then every wave runs its tokens up once more for a_t
+// h_{t-1} and down once for L_t and the gradients.  Inputs are read once and
+// gradients written once; the rate's gradient, a sum over all tokens, goes
+// through one row a tile, summed up in order by a second launch.
 //
-// Plain, bf16, 20011 tokens of 4096 channels: 1.15 GB in 210 us, 5.4 TB/s.
-// Gated, the same size: 1.15 GB in 287 us; a token and channel is 67 vector
+// Plain, bf16, 20011 tokens of 4096 channels: 1.15 GB in 191 us, 6.0 TB/s.
+// Gated, the same size: 1.15 GB in 272 us; a token and channel is 67 vector
 // operations (half the time) and eight numbers, which with two channels a lane
-// take 147 registers once two of them are laid aside in the LDS: three
-// workgroups of four waves a compute unit, whose phases overlap in part.
+// take 149 registers once two of them are laid aside in the LDS: three
+// workgroups of four waves a compute unit, whose phases overlap in part.  (Four
+// tokens a wave, eight waves: 85 registers and two workgroups, 333 us; made to
+// fit three, 297.)
 #include "glr_tiles.h"
 
 namespace glr {

@@ -13,8 +13,8 @@ constexpr int kScanWaves = 8, kScanTokens = 16, kScanTile = kScanWaves * kScanTo
 
 // The gradients: waves of eight tokens, eight to a tile, but four where each
 // lane forms the gates of two channels and a workgroup of eight would leave
-// room for no second one beside it (20011 tokens of 4096 channels: 401 us with
-// eight, 300 with four; plain, 221 with eight and 281 with four).
+// room for no second one beside it (20011 tokens of 4096 channels: 364 us with
+// eight, 272 with four; plain, 191 with eight and 211 with four).
 constexpr int kGradTokens = 8;
 constexpr int grad_waves(bool gated, int V) { return gated && V == 2 ? 4 : 8; }
 constexpr int grad_tile(bool gated, int V) { return grad_waves(gated, V) * kGradTokens; }
@@ -32,11 +32,11 @@ inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // workgroups which run already have taken, and the lowest of those waits for
 // nothing: every wait ends.  Tickets lie 256 bytes apart (in one
 // line they are as slow as one ticket for all: 1517 tokens of 1001 channels in
-// fp32, the gradients 14.8 us, apart 12.6; 20011 of 4096, gated, 286 and 277).
+// fp32, the gradients 14.8 us, apart 12.4; 20011 of 4096, gated, 286 and 277).
 // (Workgroups that stay and ask for their next tile ahead were slower, 20011
-// tokens of 4096 channels 155 -> 223 us and their gradients 297 -> 353: the
-// tile they hold waits for the one they are at.  Without asking ahead the
-// gradients took as long as now, and the scan, short of registers, 195.)
+// tokens of 4096 channels by 44% and their gradients by 19%: the tile they hold
+// waits for the one they are at.  Without asking ahead the gradients took as
+// long as now, and the scan, short of registers, 26% longer.)
 struct Chain {
     uint32_t *tickets;                   // nullptr: one tile, which needs no chain
     uint64_t *words;
@@ -88,12 +88,12 @@ struct Plan {
 
 inline Plan plan_scan(const Args &a)
 {
-    // pairs of channels once there is a workgroup of them for each compute unit,
-    // half the work one after another before that (bf16, gated, 4096 channels:
-    // 77 tokens 9.7 us with pairs and 7.6 without, 512 tokens 12.9 and 12.1,
-    // 1024 tokens 17.4 and 18.6)
+    // pairs of channels where the workgroups of single ones would be more than
+    // two for each of 256 compute units, half the work one after another before
+    // that (bf16, gated, 4096 channels: 77 tokens 9.9 us with pairs and 7.8
+    // without, 1024 tokens 14.1 and 12.5, 2048 tokens 20.9 and 26.5)
     const int64_t tiles = tiles_of(a.n_tokens, kScanTile);
-    const int V = pairs_fit(a) && tiles * blocks_of(a.D, 2) >= 256 ? 2 : 1;
+    const int V = pairs_fit(a) && tiles * blocks_of(a.D, 2) > 256 ? 2 : 1;
     return Plan{V, make_chain(a.ws, a.D, V, (int)tiles, empty_groups(a, a.h_T))};
 }
 
@@ -121,9 +121,9 @@ struct GradParts {
 inline Plan plan_grad(const Args &a, void *chain)
 {
     // gated, pairs of channels (and their smaller tiles) once there are 16
-    // workgroups of them for each compute unit (4096 channels: 2048 tokens 45.3
-    // us with pairs and 43.8 without, 4096 tokens 73.2 and 75.7); plain, always
-    // (256 tokens 10.5 and 11.0)
+    // workgroups of them for each compute unit (4096 channels: 2048 tokens 38.9
+    // us with pairs and 37.2 without, 4096 tokens 61.9 and 69.0); plain, always
+    // (256 tokens 9.2 and 8.7, 512 tokens 10.3 and 10.6, 1024 tokens 15.4 and 17.6)
     const int least = a.gated ? 4096 : 0;
     const int V = pairs_fit(a) && tiles_of(a.n_tokens, grad_tile(a.gated, 2)) * blocks_of(a.D, 2) >= least ? 2 : 1;
     const int tiles = (int)tiles_of(a.n_tokens, grad_tile(a.gated, V));

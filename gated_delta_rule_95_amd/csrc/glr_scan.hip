@@ -11,12 +11,13 @@
 // so borders cost nothing elsewhere.
 //
 // Bound by HBM where the factors are given (65536 tokens of 4096 channels,
-// bf16: 2.15 GB in 382 us, 5.6 TB/s), by HBM and the vector ALU together where
-// the gates are formed (20011 tokens, bf16: 0.66 GB in 155 us; 37 vector
+// bf16: 2.15 GB in 356 us, 6.0 TB/s), by HBM and the vector ALU together where
+// the gates are formed (20011 tokens, bf16: 0.66 GB in 147 us; 37 vector
 // operations an element, 78 us of them).  128 tokens: enough that the words of
 // the chain (24 bytes a tile and channel) and a workgroup's latencies are a
 // few percent, and two workgroups fit a compute unit, one loading while the
-// other forms its gates (64 tokens 190 us, 64 tokens by four waves 185).
+// other forms its gates.  (Where these take 138 us, 64 tokens by eight waves
+// take 154 and by four 143; plain, 65536 tokens, 378, 440 and 434.)
 #include "glr_tiles.h"
 
 namespace glr {
