@@ -27,12 +27,13 @@ inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace of a chain: a ticket for each block of channels, then one word for
 // each tile and channel (a block's by the lanes' first channels, then their
-// second ones, so that a wave's words are whole lines).  A block's workgroups take its tiles in order, by its
-// ticket, and store a map before they wait, so a tile waits only for tiles that
-// workgroups which run already have taken, and the lowest of those waits for
-// nothing: every wait ends.  Tickets lie 256 bytes apart (in one
-// line they are as slow as one ticket for all: 1517 tokens of 1001 channels in
-// fp32, the gradients 14.8 us, apart 12.4; 20011 of 4096, gated, 286 and 277).
+// second ones, so that a wave's words are whole lines).  A block's workgroups
+// take its tiles in order, by its ticket, and store a map before they wait, so a
+// tile waits only for tiles that workgroups which run already have taken, and
+// the lowest of those waits for nothing: every wait ends.  Tickets lie 256 bytes
+// apart (in one line they are as slow as one ticket for all: 1517 tokens of 1001
+// channels in fp32, the gradients 14.8 us, apart 12.4; 20011 of 4096, gated, 286
+// and 277).
 // (Workgroups that stay and ask for their next tile ahead were slower, 20011
 // tokens of 4096 channels by 44% and their gradients by 19%: the tile they hold
 // waits for the one they are at.  Without asking ahead the gradients took as

@@ -395,6 +395,21 @@ def test_decode(N, D, dtype, gated):
 
 
 @pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+@pytest.mark.parametrize("D", [40002, 33001])
+def test_many_blocks_of_channels(D, gated):
+    compare(make(30, [150, 0, 23], D, BF, gated))
+
+
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+@pytest.mark.parametrize("n", [63, 64, 65, 66])
+def test_counts_of_sequences_around_a_wave(n, gated):
+    """Up to a wave of sequences a tile knows the borders from the start, of more it searches them."""
+    lens = [(7 * k) % 5 * (k % 3) for k in range(n)]
+    compare(make(31, lens, 100, BF, gated, behind=9))
+    compare(make(32, [0] * (n - 1) + [300], 100, F32, gated))
+
+
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
 def test_slots_named_twice_touch_nothing_else(gated):
     """The state and rows of such a slot are undefined, everything else is as without them."""
     b = make(26, [6], 260, BF, gated)
