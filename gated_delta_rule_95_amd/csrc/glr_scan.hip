@@ -171,8 +171,9 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
     }
     if (!active || mine == 0) return;
     if (a.kept && w * K % kKept == 0) st<V>(a.kept + (int64_t)(tw / kKept) * D + c, h);
-    const Rows<T, V> bh(a.h, tw, a.h ? mine : 0, D);
+    const Rows<T, V> bh(a.h, tw, mine, D);
     if (plain && !ends) {
+        if (!a.h) return;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
             if (k >= mine) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) h[j] = starts >> k & 1 ? u[k][j] : __builtin_fmaf(al[k][j], h[j], u[k][j]);
-            bh.st(k, ct, h);
+            if (a.h) bh.st(k, ct, h);
             if (a.h_T && (ends >> k & 1)) {
                 const int n = __builtin_amdgcn_readfirstlane(s_last[w * K + k]);
                 st<V>(a.h_T + (int64_t)n * D + c, h);

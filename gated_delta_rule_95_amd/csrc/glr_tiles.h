@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "glr_device.h"
+#include "glr_index.h"
 #include "glr_plan.h"
 
 namespace glr {
@@ -41,43 +42,45 @@ __device__ __forceinline__ void st(T *p, const float *x)
 // A wave's rows of a tensor [.., D] as a buffer resource: `rows` of them from
 // `first` on (D < 2^24 keeps their bytes below 2^31).  A row is a scalar
 // offset and a lane's channel a vector one, so addresses cost no vector
-// arithmetic; rows past the last read zeros and are not written, and so are
-// channels at kNowhere.
+// arithmetic.  The resource's size drops channels at kNowhere, and all where
+// there is no row; it is not relied on for rows, as the scalar offset may be no
+// part of its check: a row past the last is read as the last, and not stored.
 // Pairs (the large calls) stream past the caches, "nt" both ways: 65536 tokens
 // of 4096 channels 408 -> 391 us, the gradients of 20011 gated ones 281 -> 272;
 // single channels (the small calls, whose rows the caches may hold) do not:
 // 1517 tokens of 1001 in fp32 took 25.6 us, with it 26.5.
-constexpr unsigned kNowhere = 0x80000000u;
 template <typename T, int V> struct Rows {
     static constexpr int kCache = V == 2 ? 2 : 0;
     typedef typename Row<T, V>::raw raw;
     gdr::rsrc_t r;
-    unsigned row;
+    RowSpan span;
     __device__ __forceinline__ Rows(const void *p, int64_t first, int rows, int D)
         : r(gdr::make_rsrc(static_cast<const T *>(p) + first * D, rows * D * (int)sizeof(T))),
-          row((unsigned)D * (unsigned)sizeof(T))
+          span(rows, (unsigned)D * (unsigned)sizeof(T))
     {
     }
-    // c: the lane's channel times the size of an element, or kNowhere
+    // c: the lane's channel times the size of an element, or kNowhere; st: k below `rows`
     __device__ __forceinline__ raw ld(int k, unsigned c) const
     {
+        const unsigned at = span.at(k);
         if constexpr (sizeof(raw) == 2)
-            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, c, k * row, kCache));
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, c, at, kCache));
         else if constexpr (sizeof(raw) == 4)
-            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, c, k * row, kCache));
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, c, at, kCache));
         else
-            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, c, k * row, kCache));
+            return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, c, at, kCache));
     }
     __device__ __forceinline__ void st(int k, unsigned c, const float *x) const
     {
         const raw v = Row<T, V>::pack(x);
+        const unsigned at = span.at(k);
         typedef unsigned u2 __attribute__((ext_vector_type(2)));
         if constexpr (sizeof(raw) == 2)
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, c, k * row, kCache);
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, c, at, kCache);
         else if constexpr (sizeof(raw) == 4)
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, c, k * row, kCache);
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, c, at, kCache);
         else
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), r, c, k * row, kCache);
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), r, c, at, kCache);
     }
 };
 
