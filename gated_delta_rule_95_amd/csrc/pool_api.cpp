@@ -40,7 +40,8 @@ kda_status check_pools(const pool_rows *p, int32_t n_pools, int32_t n_slots, con
     for (int i = 0; i < n_pools; ++i) {
         if (p[i].row_bytes < 1 || p[i].row_bytes > (size_t)1 << 40)
             return set_error(KDA_ERR_INVALID_ARG, "row_bytes of %s[%d] must be 1 .. 2^40", name, i);
-        if (bytes_of(p[i], n_slots) >= (size_t)1 << 46)
+        // (by division: 2^40 times 2^24 is 0 in 64 bits)
+        if (n_slots && p[i].row_bytes > (((size_t)1 << 46) - 1) / (size_t)n_slots)
             return set_error(KDA_ERR_INVALID_ARG, "%s[%d] must be below 2^46 bytes", name, i);
         if (n_slots && !p[i].base) return set_error(KDA_ERR_INVALID_ARG, "%s[%d] is NULL", name, i);
     }

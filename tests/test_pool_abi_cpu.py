@@ -71,6 +71,17 @@ def test_refusals(lib, fns, kw, msg):
         assert msg in _lib.last_error(), (fn, _lib.last_error())
 
 
+def test_pools_whose_bytes_are_zero_in_64_bits(lib):
+    """2^40 bytes a slot and 2^24 slots, and sizes on both sides of 2^46 bytes."""
+    for fn in POOLS:
+        for row, ns in ((1 << 40, 1 << 24), (1 << 40, 64), ((1 << 22) + 1, 1 << 24), (1 << 22, 1 << 24)):
+            assert call(lib, fn, pools=((20 * P, 64), (30 * P, row)), ns=ns, ts=ns) == 1, fn
+            assert "pools[1] must be below 2^46" in _lib.last_error() or "from[1] must be below 2^46" in _lib.last_error()
+    # the largest that fits is refused for something else only
+    assert call(lib, "alloc", pools=((1 << 50, 1), (1 << 51, (1 << 22) - 1)), ns=1 << 24, used=None) == 1
+    assert _lib.last_error() == "used is NULL"
+
+
 def test_nothing_to_do_is_ok(lib):
     for fn in ("copy", "alloc", "fork", "free"):
         assert call(lib, fn, n=0) == 0 and _lib.last_error() == ""
