@@ -54,6 +54,13 @@ def _given(*what) -> None:
             raise TypeError(f"{name} must be a torch.Tensor")
 
 
+def _int32(*what) -> None:
+    """what: (size, name) that the library takes in 32 bits."""
+    for n, name in what:
+        if n >> 31:
+            raise ValueError(f"{name} must be below 2^31 (got {n})")
+
+
 class _Batch:
     """Sizes of a batch of x [B, T, D] or packed [N, D]; checks everything
     whose shape follows from them."""
@@ -83,6 +90,8 @@ class _Batch:
             self.n_seqs = cu_seqlens.numel() - 1
         else:
             self.n_seqs = shape[0] if dims == 3 else 1
+        if (self.D | self.n_seqs) >> 31:
+            _int32((self.D, "D"), (self.n_seqs, "n_seqs"))
         if len(gates) == 1:
             g, = gates
             _given((g, "g"))
@@ -107,13 +116,13 @@ class _Batch:
 
 
 def glr_fwd_workspace_bytes(n_tokens: int, D: int) -> int:
-    """Bytes of workspace glr_fwd_scan and glr_fwd_scan_gated need for these sizes (0: none)."""
-    return int(_lib.load().glr_fwd_workspace_bytes(n_tokens, D))
+    """Bytes of workspace glr_fwd_scan and glr_fwd_scan_gated need for these sizes (0: none, or sizes that they refuse)."""
+    return 0 if D >> 31 or n_tokens >> 63 else int(_lib.load().glr_fwd_workspace_bytes(n_tokens, D))
 
 
 def glr_bwd_workspace_bytes(n_tokens: int, D: int) -> int:
-    """Bytes of workspace glr_bwd_scan and glr_bwd_scan_gated need for these sizes (0: none)."""
-    return int(_lib.load().glr_bwd_workspace_bytes(n_tokens, D))
+    """Bytes of workspace glr_bwd_scan and glr_bwd_scan_gated need for these sizes (0: none, or sizes that they refuse)."""
+    return 0 if D >> 31 or n_tokens >> 63 else int(_lib.load().glr_bwd_workspace_bytes(n_tokens, D))
 
 
 def _fwd(fn, x, gates, h0, cu_seqlens, output_final_state, keep, h, h_T, workspace):
@@ -208,6 +217,8 @@ def _decode(fn, x, gates, S, slots, h):
     if not isinstance(S, torch.Tensor) or S.dim() != 2:
         raise ValueError("S must be [n_slots, D]")
     n_slots = S.shape[0]
+    if (b.N | n_slots) >> 31:
+        _int32((b.N, "N"), (n_slots, "n_slots"))
     _check(b.dev, (S, "S", _F32, (n_slots, b.D)), (slots, "slots", torch.int32, shape[:1]), (h, "h", x.dtype, shape))
     if h is None:
         h = torch.empty_like(x)

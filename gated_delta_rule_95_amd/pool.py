@@ -22,7 +22,7 @@ import torch
 
 from . import _lib
 from .gdr import _need, _ptr
-from .glr import _run
+from .glr import _int32, _run
 
 __all__ = ["pool_alloc", "pool_fork", "pool_free", "pool_compact", "pool_copy",
            "pool_compact_workspace_bytes"]
@@ -51,6 +51,7 @@ def _rows(pools: Pools, name: str, n_slots: Optional[int], dev):
             raise ValueError(f"{name} must be [n_slots, ...]")
         if n_slots is None:
             n_slots = shape[0]
+            _int32((n_slots, "n_slots"))
         if shape[0] != n_slots or p.device != dev or not p.is_contiguous():
             _need(p, name, p.dtype, (n_slots,) + shape[1:], dev)
         row = math.prod(shape[1:]) * p.element_size()
@@ -62,22 +63,25 @@ def _rows(pools: Pools, name: str, n_slots: Optional[int], dev):
 
 def _used(used):
     if isinstance(used, torch.Tensor) and used.dtype is torch.bool and used.is_cuda and used.dim() == 1 \
-            and used.is_contiguous():
+            and used.is_contiguous() and not used.shape[0] >> 31:
         return used.device, used.shape[0]
     dev = _device(used, "used")
     if used.dim() != 1:
         raise ValueError("used must be [n_slots]")
+    _int32((used.shape[0], "n_slots"))
     _need(used, "used", torch.bool, used.shape, dev)
     return dev, used.shape[0]
 
 
 def _numbers(t, name, dev):
-    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev and t.dim() == 1 and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev and t.dim() == 1 and t.is_contiguous() \
+            and not t.shape[0] >> 31:
         return t.shape[0]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 1:
         raise ValueError(f"{name} must have one dimension")
+    _int32((t.shape[0], f"the length of {name}"))
     _need(t, name, torch.int32, t.shape, dev)
     return t.shape[0]
 
@@ -90,6 +94,7 @@ def pool_alloc(pools: Pools, used: torch.Tensor, n: int) -> torch.Tensor:
     rows, k, _ = _rows(pools, "pools", n_slots, dev)
     if n < 0:
         raise ValueError("n must be >= 0")
+    _int32((n, "n"))
     slots = torch.empty(n, dtype=torch.int32, device=dev)
     _run(dev, _lib.load().pool_alloc, rows.buffer_info()[0], k, _ptr(used), n_slots, n, _ptr(slots))
     return slots
@@ -117,8 +122,8 @@ def pool_free(used: torch.Tensor, slots: torch.Tensor) -> None:
 
 
 def pool_compact_workspace_bytes(n_slots: int) -> int:
-    """Bytes of workspace pool_compact needs for this count of slots."""
-    return int(_lib.load().pool_compact_workspace_bytes(n_slots))
+    """Bytes of workspace pool_compact needs for this count of slots (0 for one that it refuses)."""
+    return 0 if n_slots >> 31 else int(_lib.load().pool_compact_workspace_bytes(n_slots))
 
 
 def pool_compact(pools: Pools, used: torch.Tensor, table: Optional[torch.Tensor] = None,

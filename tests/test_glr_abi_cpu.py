@@ -126,6 +126,15 @@ def test_sizes_of_workspaces_and_kept_states(lib):
             assert f(*bad) == 0
 
 
+def test_sizes_past_32_bits_are_not_taken_for_small_ones():
+    import gated_delta_rule_95_amd as m
+    for f in (m.glr_fwd_workspace_bytes, m.glr_bwd_workspace_bytes):
+        for bad in ((1000, (1 << 32) + 64), (1000, (1 << 31) + 64), (1000, 64 - (1 << 32)), ((1 << 64) + 1000, 64)):
+            assert f(*bad) == 0, bad
+    for bad in ((1 << 32) + 1000, 1000 - (1 << 32)):
+        assert m.pool_compact_workspace_bytes(bad) == 0
+
+
 def test_python_refuses_cpu_tensors_and_types():
     import gated_delta_rule_95_amd as m
     x, g = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, 16)

@@ -464,6 +464,31 @@ def test_near_and_far_rates_side_by_side(dtype, gated, D):
     compare(b)
 
 
+def test_sizes_past_32_bits_are_refused():
+    """Shapes alone: a refused call reads nothing, and mostly one element stands for all."""
+    m, W = lib(), (1 << 32) + 2
+    one = lambda t, *shape: torch.zeros(1, dtype=t, device="cuda").expand(*shape)          # noqa: E731
+    x, f, i = one(BF, 1, W), one(F32, 1, W), torch.int32
+    with pytest.raises(ValueError, match="D must be below"):
+        m.glr_fwd_scan(x, f)
+    with pytest.raises(ValueError, match="D must be below"):
+        m.glr_bwd_scan_gated(x, x, x, f[0], x)
+    with pytest.raises(ValueError, match="n_seqs must be below"):
+        m.glr_fwd_scan(one(BF, W, 0, 3), one(F32, W, 0, 3))
+    b = make(35, [1, 1], 3)
+    with pytest.raises(ValueError, match="n_slots must be below"):
+        m.glr_decode_step_gated(*ins(b), one(F32, W, 3))
+    with pytest.raises(ValueError, match="N must be below"):
+        m.glr_decode_step(torch.empty(W, 1, dtype=BF, device="cuda"), torch.empty(W, 1, device="cuda"),
+                          torch.zeros(4, 1, device="cuda"))
+    pool, used, few = torch.zeros(4, 3, device="cuda"), torch.zeros(4, dtype=torch.bool, device="cuda"), one(i, 2).contiguous()
+    for call, what in ((lambda: m.pool_alloc(pool, used, W), "n"), (lambda: m.pool_fork(pool, used, one(i, W)), "length of src"),
+                       (lambda: m.pool_free(one(torch.bool, W), few), "n_slots"), (lambda: m.pool_free(used, one(i, W)), "length of slots"),
+                       (lambda: m.pool_copy(one(F32, W, 3), few, pool, few), "n_slots")):
+        with pytest.raises(ValueError, match=what + " must be below"):
+            call()
+
+
 def test_decode_from_an_empty_pool():
     b = make(15, [1] * 3, 40)
     h = lib().glr_decode_step_gated(*ins(b), torch.empty(0, 40, device="cuda"),
