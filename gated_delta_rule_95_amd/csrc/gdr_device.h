@@ -58,12 +58,6 @@ template <> struct OutOf<e4m3> { typedef bf16 type; };
 struct Seq {
     int bos, len;
 };
-__device__ __forceinline__ int seq_edge(const SeqArgs &s, int n)
-{
-    if (!s.cu_seqlens) return n * s.seqlen;
-    const int x = s.cu_seqlens[n];
-    return x < 0 ? 0 : x > s.n_tokens ? s.n_tokens : x;
-}
 __device__ __forceinline__ Seq seq_of(const SeqArgs &s, int n)
 {
     const int b = seq_edge(s, n), e = seq_edge(s, n + 1);

@@ -19,6 +19,14 @@ struct SeqArgs {
     int32_t n_tokens;
     int32_t seqlen;
 };
+// where sequence n starts and the one before it ends; a table that breaks its
+// contract gives places inside [0, n_tokens]
+__host__ __device__ __forceinline__ int seq_edge(const SeqArgs &s, int n)
+{
+    if (!s.cu_seqlens) return n * s.seqlen;
+    const int x = s.cu_seqlens[n];
+    return x < 0 ? 0 : x > s.n_tokens ? s.n_tokens : x;
+}
 
 struct Args {
     const void *q, *k, *v;

@@ -83,7 +83,7 @@ __global__ __launch_bounds__(grad_waves(GATED, V) * WAVE) void glr_grad_kernel(A
         for (int j = 0; j < V; ++j) nr[j] = -RF::get(rate, j);
     }
     const typename RF::raw left = ld<V>(a.kept + (int64_t)(t0 / kKept) * D + cc);
-    if (w == 0) mark_borders(sa, few, t0, C, lane, s_first, s_last);
+    if (w == 0) mark_borders(Lane{lane}, sa, [&](int) { return few; }, t0, C, s_first, s_last);
     __syncthreads();
     const uint64_t starts = __ballot(lane < K && s_first[w * K + lane % K] >= 0);
     const uint64_t ends = __ballot(lane < K && s_last[w * K + lane % K] >= 0);

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(NT, 4) void glr_scan_kernel(Args a, Chain chain)
 #pragma unroll
         for (int j = 0; j < V; ++j) nr[j] = -RF::get(rate, j);
     }
-    if (w == 0) mark_borders(sa, few, t0, C, lane, s_first, s_last);
+    if (w == 0) mark_borders(Lane{lane}, sa, [&](int) { return few; }, t0, C, s_first, s_last);
     __syncthreads();
     const uint64_t starts = __ballot(lane < K && s_first[w * K + lane % K] >= 0);
     const uint64_t ends = __ballot(lane < K && s_last[w * K + lane % K] >= 0);

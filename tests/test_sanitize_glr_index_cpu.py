@@ -1,5 +1,6 @@
-"""Host-side AddressSanitizer + UndefinedBehaviorSanitizer run of the index
-arithmetic that the gated linear recurrence's kernels run, through
+"""Host-side AddressSanitizer + UndefinedBehaviorSanitizer run of what the gated
+linear recurrence's kernels do with indices, tables of sequences and the words
+of the chain (csrc/glr_index.h, the kernels' own code), through
 tests/sanitize/glr_index_driver.cpp.  CPU only: no GPU code is built with a
 sanitizer."""
 import os
@@ -18,7 +19,7 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 def test_index_arithmetic_under_asan_ubsan(tmp_path):
     csrc = os.path.join(ROOT, "gated_delta_rule_95_amd", "csrc")
     exe = tmp_path / "glr_index_driver"
-    cmd = ["g++", "-std=c++17", "-Wall", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include"),
+    cmd = ["g++", "-std=c++17", "-Wall", "-Wno-unknown-pragmas", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include"),
            "-I" + os.path.join(ROOT, "include"), "-I" + csrc,
            os.path.join(ROOT, "tests", "sanitize", "glr_index_driver.cpp"), "-o", str(exe),
            "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer", "-g", "-O1"]
