@@ -6,6 +6,7 @@
 // of 1000 slots takes 3 us, the latency of its loads and counts; copies are
 // bound by HBM (32 copies of 8 slots of 4 MB: 168 MB in 28.6 us, 5.9 TB/s).
 #include "kda_device.h"
+#include "pool_index.h"
 #include "pool_launch.h"
 
 namespace pool {
@@ -16,76 +17,40 @@ constexpr int CT = 256;                  // threads that copy
 constexpr int kPools = 32;               // pools a launch
 constexpr int kPiece = 64 * CT;      // bytes of a row that one workgroup moves at a time
 
-// Exclusive rank of `x` among the workgroup's threads in order, and the
-// total.  All threads call it; `s` holds PT / 64 + 1 counts.
-__device__ __forceinline__ int rank_of(bool x, int *s, int &total)
-{
-    const uint64_t b = __ballot(x);
-    const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
-    __syncthreads();
-    if (lane == 0) s[w] = __popcll(b);
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int i = 0; i < PT / 64; ++i) {
-        if (i == w) before = all;
-        all += s[i];
-    }
-    total = all;
-    return before + __popcll(b & (((uint64_t)1 << lane) - 1));
-}
-
-__device__ __forceinline__ bool valid(const uint8_t *used, int n_slots, const int32_t *src, int i)
-{
-    if (!src) return true;
-    const int j = src[i];
-    return j >= 0 && j < n_slots && used[j];
-}
-
-// dst first holds the free slots in order (entry k the k-th lowest, k < n);
-// rows, from the last to the first, then replace them by their own: row i
-// has rank <= i, so what rows before it still want is not yet replaced.
-// (What comes back from memory here, in the plan and at the copies is held
-// against the bounds again: a list or workspace that another call writes
-// meanwhile, against the contract, must not move an address out of its array.)
-__device__ __forceinline__ void take(uint8_t *used, int n_slots, const int32_t *src, int n, int32_t *dst)
-{
-    __shared__ int s[PT / 64];
-    int nfree = 0, total;
-    for (int base = 0; base < n_slots && nfree < n; base += PT) {
-        const int j = base + threadIdx.x;
-        const bool f = j < n_slots && !used[j];
-        const int k = nfree + rank_of(f, s, total);
-        if (f && k < n) dst[k] = j;
-        nfree += total;
-    }
-    int before = 0;
-    for (int base = 0; base < n; base += PT) {
-        const int i = base + threadIdx.x;
-        rank_of(i < n && valid(used, n_slots, src, i), s, total);
-        before += total;
-    }
-    __syncthreads();
-    for (int base = (n - 1) / PT * PT; base >= 0; base -= PT) {
-        const int i = base + threadIdx.x;
-        const bool v = i < n && valid(used, n_slots, src, i);
-        int k = rank_of(v, s, total);
-        before -= total;
-        k += before;
-        const int to = v && k >= 0 && k < nfree ? dst[k] : -1;
+// The block of pool_index.h: the workgroup, a thread each.  `s` holds PT / 64
+// counts.
+struct Group {
+    static constexpr int threads = PT;
+    int *s;
+    template <typename T> struct Each {
+        T x;
+        __device__ __forceinline__ T &operator[](int) { return x; }
+    };
+    template <typename F> __device__ __forceinline__ void each(const F &f) const { f((int)threadIdx.x); }
+    __device__ __forceinline__ void sync() const { __syncthreads(); }
+    template <typename F, typename G> __device__ __forceinline__ int rank(const F &f, const G &g) const
+    {
+        const bool x = f((int)threadIdx.x);
+        const uint64_t b = __ballot(x);
+        const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
         __syncthreads();
-        if (i < n) dst[i] = to;
+        if (lane == 0) s[w] = __popcll(b);
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int i = 0; i < PT / 64; ++i) {
+            if (i == w) before = all;
+            all += s[i];
+        }
+        g((int)threadIdx.x, x, before + __popcll(b & (((uint64_t)1 << lane) - 1)), all);
+        return all;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += PT) {
-        const int j = dst[i];
-        if (j >= 0 && j < n_slots) used[j] = 1;
-    }
-}
+};
 
 __global__ __launch_bounds__(PT) void pool_take_kernel(uint8_t *used, int n_slots, const int32_t *src, int n,
                                                        int32_t *dst)
 {
-    take(used, n_slots, src, n, dst);
+    __shared__ int s[PT / 64];
+    take(Group{s}, used, n_slots, src, n, dst);
 }
 
 __global__ __launch_bounds__(CT) void pool_free_kernel(uint8_t *used, int n_slots, const int32_t *slots, int n)
@@ -100,38 +65,7 @@ __global__ __launch_bounds__(PT) void pool_plan_kernel(uint8_t *used, int n_slot
                                                        int32_t *remap, Moves m)
 {
     __shared__ int s[PT / 64];
-    int live = 0, total;
-    for (int base = 0; base < n_slots; base += PT) {
-        const int j = base + threadIdx.x;
-        rank_of(j < n_slots && used[j], s, total);
-        live += total;
-    }
-    int holes = 0, movers = 0;
-    for (int base = 0; base < n_slots; base += PT) {
-        const int j = base + threadIdx.x;
-        const bool u = j < n_slots && used[j], hole = !u && j < live, mover = u && j >= live;
-        const int kh = holes + rank_of(hole, s, total);
-        holes += total;
-        const int km = movers + rank_of(mover, s, total);
-        movers += total;
-        if (hole && kh < n_slots / 2) m.dst[kh] = j;
-        if (mover && km < n_slots / 2) m.src[km] = j;
-        if (j < n_slots) remap[j] = u ? j : -1;
-    }
-    // as many holes as movers, of n_slots in all
-    movers = movers < n_slots / 2 ? movers : n_slots / 2;
-    __syncthreads();
-    for (int k = threadIdx.x; k < movers; k += PT) {
-        const int j = m.src[k];
-        if (j >= 0 && j < n_slots) remap[j] = m.dst[k];
-    }
-    for (int j = threadIdx.x; j < n_slots; j += PT) used[j] = j < live;
-    if (threadIdx.x == 0) *m.count = movers;
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < n_table; i += PT) {
-        const int j = table[i];
-        if (j >= 0 && j < n_slots) table[i] = remap[j];
-    }
+    plan(Group{s}, used, n_slots, table, n_table, remap, m);
 }
 
 struct CopyArgs {
@@ -207,7 +141,8 @@ constexpr int kWavePiece = 64 * 64;
 __global__ __launch_bounds__(PT) void pool_take_copy_kernel(uint8_t *used, int n_slots, const int32_t *src, int n,
                                                             int32_t *dst, CopyArgs a, int pools)
 {
-    take(used, n_slots, src, n, dst);
+    __shared__ int s[PT / 64];
+    take(Group{s}, used, n_slots, src, n, dst);
     __syncthreads();
     constexpr int waves = PT / 64;
     int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
