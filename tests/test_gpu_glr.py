@@ -319,6 +319,56 @@ def test_nonfinite_values_stay_in_their_sequence_and_channel(bad, gated):
                 assert torch.equal(x[m], y[m]), (k, name)
 
 
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+@pytest.mark.parametrize("D", [7, 8192])
+def test_nonfinite_states_stay_in_their_sequence_and_channel(D, gated):
+    """Infinities and NaN in a sequence's first state and last cotangent, borders inside and between tiles."""
+    lens = [70, 300, 0, 5, 40, 128, 200]
+    b = make(33, lens, D, BF, gated)
+    good_h, good = fwd(b), bwd(b)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        c = dict(b, h0=b["h0"].clone(), dh_T=b["dh_T"].clone())
+        for n in (1, 2, 5):
+            c["h0"][n, 3] = c["dh_T"][n, 3] = bad
+        h, h_T = fwd(c)
+        grads = bwd(c)
+        torch.cuda.synchronize()
+        keep, n = torch.ones(sum(lens), D, dtype=torch.bool, device="cuda"), torch.ones(len(lens), D, dtype=torch.bool, device="cuda")
+        for k in (1, 2, 5):
+            keep[sum(lens[:k]):sum(lens[:k + 1]), 3] = False
+            n[k, 3] = False
+        assert torch.equal(h[keep], good_h[0][keep]) and torch.equal(h_T[n], good_h[1][n])
+        for x, y, name in zip(grads, good, names(b)):
+            m = keep if x.shape == keep.shape else n if x.shape == n.shape else n[1]
+            assert torch.equal(x[m], y[m]), name
+        # an empty sequence hands both on as they are
+        assert torch.equal(h_T[2], c["h0"][2]) if bad == bad else bool(torch.isnan(h_T[2, 3]))
+        assert torch.equal(grads[-1][2], c["dh_T"][2]) if bad == bad else bool(torch.isnan(grads[-1][2, 3]))
+
+
+@pytest.mark.parametrize("dtype,gated,lens", [(BF, True, [150, 3]), (F32, False, [20]), (F32, True, [5, 28])])
+def test_widest_rows(dtype, gated, lens):
+    """The most channels there can be: a wave's rows take up to 2^30 bytes.  Some channels against the oracle."""
+    D, N = (1 << 24) - 1, sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(34)
+    rnd = lambda t, *shape: torch.empty(shape, dtype=t, device="cuda").normal_(generator=gen)              # noqa: E731
+    b = dict(x=rnd(dtype, N, D), dh=rnd(dtype, N, D), h0=rnd(F32, len(lens), D), dh_T=rnd(F32, len(lens), D), gated=gated)
+    if gated:
+        b.update(r=rnd(dtype, N, D), i=rnd(dtype, N, D), rate=rnd(F32, D).abs_())
+    else:
+        b["g"] = rnd(F32, N, D).abs_().neg_()
+    b["cu"] = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    cols = torch.tensor([0, 1, 63, 64, 8388607, 8388608, D - 128, D - 65, D - 64, D - 2, D - 1], device="cuda")
+    some = {k: v[..., cols] if isinstance(v, torch.Tensor) and k != "cu" else v for k, v in b.items()}
+    want = bars.reference(host(some), b["cu"].tolist(), gated)
+    h, h_T, kept = fwd(b, keep=True)
+    bars.check("h", h[:, cols], want["h"])
+    bars.check("h_T", h_T[:, cols], want["h_T"])
+    del h
+    for name, x in zip(names(b), bwd(b, kept=kept)):
+        bars.check(name, x[..., cols], want[name])
+
+
 def test_forgetting_and_closed_gates():
     """g = -inf forgets; gates so closed or open that factors reach their ends."""
     b = make(10, [200, 90], 64, F32, False)
