@@ -23,7 +23,7 @@
  * need not be a power of two or a multiple of anything):
  *     x, h, r, i     [n_tokens, D]   in_dtype
  *     g              [n_tokens, D]   float32, natural-log decay, g <= 0
- *     rate           [D]             float32, >= 0
+ *     rate           [D]             float32, >= 0 and finite
  *     h0, h_T        [n_seqs, D]     float32
  *     kept           [ceil(n_tokens / 32), D] float32
  *     cu_seqlens     int32 [n_seqs + 1] in device memory, cu_seqlens[0] = 0,
@@ -31,7 +31,8 @@
  *                    n_seqs sequences of n_tokens / n_seqs tokens each
  * h is rounded to in_dtype where it is stored; the recurrence runs in fp32.
  * Rows of tokens behind the last sequence are not read, and in the outputs
- * not written.
+ * not written.  A sequence's first token is scaled by sqrt(1 - a^2) like any
+ * other.
  *
  * g = -inf is allowed and forgets the state.  g > 0 is computed as given
  * where no product of successive factors overflows.  NaN or an infinity in
@@ -53,7 +54,14 @@
  * reported as a kda_status (kda_last_error has the message) before anything
  * is launched, and cu_seqlens and slots that break their contract change
  * results, never the addresses touched.  Two calls in flight need separate
- * workspaces.  Results do not depend on the order in which workgroups run.
+ * workspaces: in one that something else writes meanwhile a call finds any
+ * states, or NaN where a wait for one gives up after a second or more.
+ *
+ * Results do not depend on the order in which workgroups run, and a call
+ * repeated gives the same bits.  Their last bits (within the same error bounds)
+ * do depend on the form that is taken by sizes and alignment and, gated, on
+ * whether all rates of the 64 or 128 channels that a wave takes at once are at
+ * most 0.69.
  */
 #ifndef GLR_H
 #define GLR_H

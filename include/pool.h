@@ -27,7 +27,7 @@
  * Calls that touch the same pools, `used` or tables must be ordered by the
  * caller (one stream does).
  *
- * Sizes: 0 <= n_slots, n <= 2^24 each; 0 <= n_pools; 1 <= row_bytes <= 2^40;
+ * Sizes: 0 <= n_slots, n, n_table <= 2^24 each; 0 <= n_pools; 1 <= row_bytes <= 2^40;
  * n_slots row_bytes below 2^46.  Alignment: int32 arrays 4 bytes, pools 1.
  * (Rows are moved 16 bytes at a time where bases and row_bytes allow, else 4
  * or 1.)  Workspaces: 256 bytes.
