@@ -2,6 +2,7 @@
 // workspace holds: host arithmetic of sizes only.
 #pragma once
 
+#include "api_checks.h"
 #include "glr_launch.h"
 
 namespace glr {
@@ -23,7 +24,6 @@ static_assert(kScanTile % kKept == 0 && kKept % kScanTokens == 0, "kept states l
 
 inline int64_t tiles_of(int64_t n_tokens, int tile) { return (n_tokens + tile - 1) / tile; }
 inline int blocks_of(int32_t D, int V) { return (D + kLanes * V - 1) / (kLanes * V); }
-inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace of a chain: a ticket for each block of channels, then one word for
 // each tile and channel (a block's by the lanes' first channels, then their
@@ -104,7 +104,7 @@ struct GradParts {
     float *kept, *part;
     void *chain;
     // one fp32 row for each kept state, and no fewer than tiles
-    static size_t rows(int64_t n_tokens, int32_t D) { return round256((size_t)tiles_of(n_tokens, kKept) * D * 4); }
+    static size_t rows(int64_t n_tokens, int32_t D) { return api::round256((size_t)tiles_of(n_tokens, kKept) * D * 4); }
     static size_t bytes(int64_t n_tokens, int32_t D)
     {
         return 2 * rows(n_tokens, D) + chain_bytes(tiles_of(n_tokens, grad_tile(true, 2)), D);
