@@ -2,7 +2,7 @@
 // updated in place in a pool.  A thread has V neighbouring channels of one
 // request, a workgroup part of a request's row: inputs and states are read
 // once and written once.  256 requests of 8192 channels, gated, bf16: 33.6 MB
-// in 7.5 us (4.5 TB/s, launch included); one request of 4096: 2.4 us, its
+// in 7.4 us (4.5 TB/s, launch included); one request of 4096: 2.6 us, its
 // latency.  (With 64 or 256 threads a workgroup 7.9 us, one channel a thread
 // 8.4.)
 #include "glr_tiles.h"

@@ -11,12 +11,17 @@
 // through one row a tile, summed up in order by a second launch.
 //
 // Plain, bf16, 20011 tokens of 4096 channels: 1.15 GB in 191 us, 6.0 TB/s.
-// Gated, the same size: 1.15 GB in 272 us; a token and channel is 67 vector
-// operations (half the time) and eight numbers, which with two channels a lane
+// Gated, the same size: 1.15 GB in 256 us; a token and channel is 62 vector
+// instructions (54% of the time) and eight numbers, which with two channels a lane
 // take 149 registers once two of them are laid aside in the LDS: three
 // workgroups of four waves a compute unit, whose phases overlap in part.  (Four
 // tokens a wave, eight waves: 85 registers and two workgroups, 333 us; made to
-// fit three, 297.)
+// fit three, 297; then, three of four waves took 272.)
+//
+// A token at a border loads the state before it and the cotangent behind it
+// where it wants them, twice each, and the second time behind its neighbours'
+// stores: 20011 sequences of one token with states, gated, take 684 us for 2.1
+// GB, twice what the bytes take.
 #include "glr_tiles.h"
 
 namespace glr {

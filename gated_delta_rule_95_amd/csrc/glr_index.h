@@ -83,8 +83,8 @@ __host__ __device__ __forceinline__ Map map_of(uint64_t w)
 // applied to its B, the farthest first.  That is what each of these tiles does,
 // or did, to get at the map that forgets which it stores in the end, so the
 // result does not depend on how far they have come, to the last bit.  (Eight words a lane; with 16 the scan of 65536
-// tokens of 4096 channels takes 392 us and not 382, the gradients of 20011 plain
-// ones 214 and not 199: every look goes past the caches.)
+// tokens of 4096 channels takes 369 us and not 357, scan and gradients of 20011
+// plain ones 331 and not 316: every look goes past the caches.)
 // The wait is bounded all the same, for a workspace that something else writes
 // while the call runs: after kPatience looks (a second or more; the longest
 // wait of a sound call is some 100 us) the state becomes NaN.

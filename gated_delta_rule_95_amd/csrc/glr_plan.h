@@ -124,7 +124,8 @@ inline Plan plan_grad(const Args &a, void *chain)
     // gated, pairs of channels (and their smaller tiles) once there are 16
     // workgroups of them for each compute unit (4096 channels: 2048 tokens 38.9
     // us with pairs and 37.2 without, 4096 tokens 61.9 and 69.0); plain, always
-    // (256 tokens 9.2 and 8.7, 512 tokens 10.3 and 10.6, 1024 tokens 15.4 and 17.6)
+    // (bf16: 256 tokens 9.2 and 8.7, 512 tokens 10.3 and 10.6, 1024 tokens 15.4 and
+    // 17.6; fp32 was measured where there is work for all compute units only)
     const int least = a.gated ? 4096 : 0;
     const int V = pairs_fit(a) && tiles_of(a.n_tokens, grad_tile(a.gated, 2)) * blocks_of(a.D, 2) >= least ? 2 : 1;
     const int tiles = (int)tiles_of(a.n_tokens, grad_tile(a.gated, V));

@@ -11,9 +11,11 @@
 // so borders cost nothing elsewhere.
 //
 // Bound by HBM where the factors are given (65536 tokens of 4096 channels,
-// bf16: 2.15 GB in 356 us, 6.0 TB/s), by HBM and the vector ALU together where
-// the gates are formed (20011 tokens, bf16: 0.66 GB in 147 us; 37 vector
-// operations an element, 78 us of them).  128 tokens: enough that the words of
+// bf16: 2.15 GB in 349 us, 6.2 TB/s), by HBM and the vector ALU together where
+// the gates are formed (20011 tokens, bf16: 0.66 GB in 134 us, 4.9 TB/s; 32 vector
+// instructions an element, which take 54% of it).  One long sequence of few
+// channels is bound by the chain, 128 looks at four tiles in a row: 65536 tokens of
+// 64 channels take 125 us, of 512 128.  128 tokens: enough that the words of
 // the chain (24 bytes a tile and channel) and a workgroup's latencies are a
 // few percent, and two workgroups fit a compute unit, one loading while the
 // other forms its gates.  (Where these take 138 us, 64 tokens by eight waves

@@ -3,8 +3,12 @@
 // One workgroup plans (the free slots' ranks and the rows' ranks are running
 // counts over at most 2^24 bytes), and a second launch moves the bytes (of a
 // few rows, the same).  A plan
-// of 1000 slots takes 3 us, the latency of its loads and counts; copies are
-// bound by HBM (32 copies of 8 slots of 4 MB: 168 MB in 28.6 us, 5.9 TB/s).
+// of 1000 slots takes 3.3 us, the latency of its loads and counts, which steps of
+// 1024 slots add up (a fork in 2^20 slots 356 us, a compaction 2.8 ms, of which
+// a table of 2^20 entries is 0.54); copies are bound by HBM (32 copies of 8 slots
+// of 4 MB: 168 MB in 26.6 us, 6.3 TB/s), but for rows that 16 does not divide,
+// whose words are requested one at a time (16 slots of 299 999 fp32 take 9.3 us,
+// of 599 999 bf16, byte by byte, 22.8, of 300 000 fp32 6.1).
 #include "kda_device.h"
 #include "pool_index.h"
 #include "pool_launch.h"
