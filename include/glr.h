@@ -42,7 +42,8 @@
  * (1.2e-38), u is 0 and the part of the gradients that passes through
  * sqrt(1 - a^2), whose slope is infinite at 0, is taken as 0.
  *
- * Sizes: 1 <= D < 2^24; 0 <= n_seqs < 2^27; 0 <= n_tokens <= 2^31 - 256; n_tokens, n_seqs
+ * Sizes: 1 <= D < 2^24; 0 <= n_seqs < 2^27; 0 <= n_tokens <= 2^31 - 256, and 0 where
+ * n_seqs is; n_tokens, n_seqs
  * and (decode) N times D below 2^40, and the number of (64 tokens, 64
  * channels) tiles below 2^22.  in_dtype KDA_BF16 or KDA_F32.
  *
