@@ -3,7 +3,7 @@
 // A tile is 128 tokens by 64 V channels, one workgroup: each of eight waves
 // takes 16 tokens in registers (each lane V channels), forms their factors
 // and inputs, and folds them into one map h -> A h + B.  The waves' maps meet
-// in the LDS, the tile's goes to the tiles behind it (glr_tiles.h), the state
+// in the LDS, the tile's goes to the tiles behind it (glr_index.h), the state
 // that comes in is looked up from the tiles before it, and every wave runs
 // its 16 tokens once more from the state that reaches it and stores them.
 // Everything is read and written once, by one launch, however the batch is

@@ -1,6 +1,6 @@
-// What the scan and its gradients share: tiles of tokens and channels handed
-// out in order, sequence borders inside a tile, and the chain of states from
-// tile to tile (gfx950 only).
+// What the scan and its gradients share on the device: rows of a tensor, tiles
+// of tokens and channels handed out in order, and the lanes and words by which
+// glr_index.h finds the borders in a tile and what comes into it (gfx950 only).
 #pragma once
 
 #include <type_traits>
